@@ -82,6 +82,7 @@ typedef enum pa_kv_dtype {
 #define PA_DEVERR_TIMEOUT     0x4u /* a wait for a page copy exceeded its time limit; output invalid */
 #define PA_DEVERR_BAD_SLOT    0x8u /* slot_mapping entry >= num_blocks * block_size: token skipped */
 #define PA_DEVERR_OUT_OF_BLOCKS 0x10u /* pa_block_alloc: free stack too short; nothing changed */
+#define PA_DEVERR_BAD_AXIS    0x20u /* pa_rope_append: pair_axis entry outside [0, num_axes): axis 0 taken */
 
 /*
  * pa_slot_mapping -- slot of each sequence's newest token.
@@ -416,6 +417,122 @@ pa_status pa_prefill_mma(const void *q, const void *k_cache, const void *v_cache
                          int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
                          int head_dim, int num_blocks, int block_size, pa_kv_dtype kv_dtype,
                          float kv_scale, float softmax_scale, void *out, cudaStream_t stream);
+
+/*
+ * pa_rope_append -- rotate the new tokens' q and k rows by their positions and
+ * write k and v into the paged cache, in one kernel.
+ * Source: the append is that of "Optimizing Llama 3.1 405B Inference with
+ * vLLM PagedAttention", section "PagedAttention Mechanics"; the rotation is
+ * the models' (rotary position embedding), which the pages leave to them.
+ *   q             bf16 [num_tokens] rows of [num_q_heads][head_dim]; k, v
+ *                 likewise with num_kv_heads.  q_stride, k_stride, v_stride:
+ *                 elements from one token's row to the next (multiples of 8),
+ *                 so the three may be slices of one projection's output.
+ *   positions     int32 [num_axes][num_tokens], any value (negative too)
+ *   inv_freq      fp64 [rotary_dim / 2] (device): pair i of token t turns by
+ *                 theta = positions[pair_axis[i]][t] * inv_freq[i] radians
+ *   pair_axis     int32 [rotary_dim / 2] (device); NULL: axis 0 for every pair
+ *                 (needed when num_axes > 1).  Several axes (time, height,
+ *                 width, ...) give each pair the position along its own axis.
+ *   rotary_dim    a multiple of 16, at most head_dim; the elements behind it
+ *                 are left as they are.
+ *   adjacent      0: pair i is elements (i, i + rotary_dim / 2);
+ *                 otherwise elements (2i, 2i + 1)
+ *   magnitude     > 0: the rotated elements are multiplied by it
+ *   (x_a, x_b) of a pair becomes magnitude * (x_a cos theta - x_b sin theta,
+ *   x_a sin theta + x_b cos theta), in fp32, rounded once:
+ *   q_out         bf16 [num_tokens][num_q_heads][head_dim], dense; may be q
+ *                 itself when q is dense, and may not overlap it otherwise.
+ *                 num_q_heads 0: no q (q and q_out may be NULL).
+ *   k_cache, v_cache  row slot_mapping[t] gets the rotated k and v as they
+ *                 are (PA_KV_BF16), or e4m3_rn_satfinite(x / scale) of the
+ *                 fp32 rotated k and of v (PA_KV_FP8_E4M3), scale = kv_scale,
+ *                 or k_scales[h] / v_scales[h] when both arrays are given.
+ *   A negative slot writes no k and v for the token (its q is rotated all the
+ *   same); distinct tokens must have distinct slots.  num_axes 1..16.
+ */
+pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const int32_t *positions, int num_axes,
+                         const double *inv_freq, const int32_t *pair_axis, int rotary_dim,
+                         int adjacent, float magnitude, const int32_t *slot_mapping, int num_tokens,
+                         int num_q_heads, void *q_out, void *k_cache, void *v_cache, int num_blocks,
+                         int num_kv_heads, int head_dim, int block_size, pa_kv_dtype kv_dtype,
+                         float kv_scale, const float *k_scales, const float *v_scales,
+                         cudaStream_t stream);
+
+/*
+ * pa_block_summary / pa_sparse_select / pa_sparse_decode / pa_sparse_attend --
+ * decode attention over a chosen part of a long context.  The pages motivate
+ * contexts of 128K tokens ("vLLM PagedAttention Optimization: Complete
+ * Step-by-Step Tuning Guide", Step 1) and attend to all of them; reading only
+ * the pages with the largest bound on q . k is this library's own.
+ *
+ * pa_block_summary: for every slot of slot_mapping that is the LAST row of its
+ *   block (slot % block_size == block_size - 1; others, and negative ones, do
+ *   nothing), int8 bounds of the block's keys as the cache now holds them.
+ *   Call it after the append with the append's slots: a block's bounds are
+ *   made when its last token arrives.  Per block and KV head, over the stored
+ *   values (E4M3: the codes' values, before the scale):
+ *     e = the least exponent in [-60, 40] with max |k| <= 127 * 2^e,
+ *     summary[block][h][0][d] = rint(max_t k[t][d] / 2^e),
+ *     summary[block][h][1][d] = rint(min_t k[t][d] / 2^e)  (held to +-127),
+ *     exponents[block][h] = e;
+ *   a block holding an infinity or NaN gets e = 127 and zeros.
+ *   summary int8 [num_blocks][num_kv_heads][2][head_dim], exponents int8
+ *   [num_blocks][num_kv_heads]; other blocks' entries are left as they are.
+ * pa_sparse_select: row t is one query token with block_tables row t and
+ *   n = context_lens[t] tokens, nb = ceil(n / block_size) logical blocks
+ *   (rows may share a sequence: give each its table row and its own length).
+ *   Per KV head it chooses min(nb, top_k) of them: blocks < sink_blocks,
+ *   blocks >= nb - recent_blocks, and of the others those with the largest
+ *     score(j) = 2^e_j * max_g 2^e_g sum_d max(r_g,d hi_j,d, r_g,d lo_j,d),
+ *   r_g, e_g the query heads of the group in the same int8 form (a query head
+ *   holding an infinity or NaN counts as zero), ties to the lower block; a
+ *   block with e = 127 scores +infinity, one outside the pool -infinity (and
+ *   PA_DEVERR_BAD_BLOCK).  The scores are exact, so the choice is unique.
+ *   The other blocks' bounds must have been made by pa_block_summary.
+ *   selected int32 [num_rows][num_kv_heads][top_k]: ascending logical blocks,
+ *   then -1; counts int32 [num_rows][num_kv_heads].  recent_blocks >= 1,
+ *   sink_blocks + recent_blocks <= top_k, max_blocks_per_seq <= 262144.
+ * pa_sparse_decode: out[t][hq] = bf16_rn of the softmax of softmax_scale *
+ *   q . K over the tokens (position < n) of the first counts[t][h] blocks of
+ *   selected[t][h], applied to V; zeros when there are none.  Any list may be
+ *   given, in any order, without repeated blocks; an entry outside the
+ *   sequence's blocks contributes nothing and sets PA_DEVERR_BAD_BLOCK.
+ *   Cache types and scales as pa_rope_append; softmax_scale > 0.  splits: CTAs
+ *   that share a (row, KV head)'s list, 1, 2, 4 or 8; 0 lets the library
+ *   choose.  One kernel, no workspace.  With an E4M3 cache the query is
+ *   rounded to fp16 as in pa_decode_partitions.
+ * pa_sparse_attend: pa_sparse_select followed by pa_sparse_decode on the same
+ *   stream (two kernels); selected and counts are outputs.
+ */
+pa_status pa_block_summary(const void *k_cache, const int32_t *slot_mapping, int num_tokens,
+                           int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                           pa_kv_dtype kv_dtype, int8_t *summary, int8_t *exponents,
+                           cudaStream_t stream);
+pa_status pa_sparse_select(const void *q, const int8_t *summary, const int8_t *exponents,
+                           const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *context_lens, int num_rows, int num_q_heads,
+                           int num_kv_heads, int head_dim, int num_blocks, int block_size, int top_k,
+                           int sink_blocks, int recent_blocks, int32_t *selected, int32_t *counts,
+                           cudaStream_t stream);
+pa_status pa_sparse_decode(const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *context_lens, int num_rows, int num_q_heads,
+                           int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                           pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
+                           const float *v_scales, float softmax_scale, const int32_t *selected,
+                           const int32_t *counts, int top_k, int splits, void *out,
+                           cudaStream_t stream);
+pa_status pa_sparse_attend(const void *q, const void *k_cache, const void *v_cache,
+                           const int8_t *summary, const int8_t *exponents,
+                           const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *context_lens, int num_rows, int num_q_heads,
+                           int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                           pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
+                           const float *v_scales, float softmax_scale, int top_k, int sink_blocks,
+                           int recent_blocks, int32_t *selected, int32_t *counts, void *out,
+                           cudaStream_t stream);
 
 /*
  * pa_decode_static_workspace -- pa_decode with partition_size > 0, without

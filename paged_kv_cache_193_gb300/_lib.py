@@ -27,9 +27,11 @@ PA_DEVERR_BAD_CONTEXT = 0x2
 PA_DEVERR_TIMEOUT = 0x4
 PA_DEVERR_BAD_SLOT = 0x8
 PA_DEVERR_OUT_OF_BLOCKS = 0x10
+PA_DEVERR_BAD_AXIS = 0x20
 
 # name -> (restype, argtypes); the order matches include/pa.h
 _P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_int64
 SIGNATURES = {
     "pa_slot_mapping": (_I, [_P, _I, _P, _I, _I, _P, _P]),
     "pa_cache_append": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
@@ -56,6 +58,14 @@ SIGNATURES = {
                                _P]),
     "pa_prefill_mma": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F,
                             _P, _P]),
+    "pa_rope_append": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _P, _P, _I, _I, _F, _P, _I, _I, _P, _P, _P, _I,
+                            _I, _I, _I, _I, _F, _P, _P, _P]),
+    "pa_block_summary": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "pa_sparse_select": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "pa_sparse_decode": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _F, _P, _P,
+                              _I, _I, _P, _P]),
+    "pa_sparse_attend": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _F,
+                              _I, _I, _I, _P, _P, _P, _P]),
     "pa_decode_static_workspace": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                         _F, _I, _P, _P]),
     "pa_test_set_wait": (_I, [ctypes.c_uint64, _I]),

@@ -484,6 +484,296 @@ class DecodeStep:
         return self.attend(q, stream)
 
 
+# ---------------------------------------------------------------------------
+# rotate-and-append, page bounds, block-sparse decode
+# ---------------------------------------------------------------------------
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    """All tensors on the current CUDA device (whose stream the call uses)."""
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}; expected {dev}")
+
+
+def _need_shape(t: torch.Tensor, name: str, dtypes, shape) -> None:
+    _need(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from one token's row [heads, head_dim] to the next of a bf16
+    tensor [tokens, heads, head_dim] whose rows are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}; expected bfloat16")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions (got shape {tuple(t.shape)})")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: each token's [heads, head_dim] rows must be dense")
+    return st if T > 1 else H * D
+
+
+def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales, v_scales) -> int:
+    kv_dtype = cache_dtype_of(k_cache)
+    _need(k_cache, "k_cache", _CACHE_DTYPES[kv_dtype], 4)
+    _need_shape(v_cache, "v_cache", _CACHE_DTYPES[kv_dtype], k_cache.shape)
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales must both be given or both be None")
+    if k_scales is not None:
+        _need_shape(k_scales, "k_scales", (torch.float32,), k_cache.shape[1:2])
+        _need_shape(v_scales, "v_scales", (torch.float32,), k_cache.shape[1:2])
+    return kv_dtype
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                v_cache: torch.Tensor, pair_axis: torch.Tensor | None = None, adjacent: bool = False,
+                magnitude: float = 1.0, kv_scale: float = 1.0, k_scales: torch.Tensor | None = None,
+                v_scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor | None:
+    """Rotate q and k of T new tokens by their positions and write k and v
+    into the cache, in one kernel (pa_rope_append).
+
+    ``q`` bf16 [T, Hq, D] (or None), ``k``, ``v`` [T, Hkv, D]: views whose
+    tokens are a stride apart will do (slices of one projection's output).
+    ``positions`` int32 [T], or [axes, T] with ``pair_axis`` int32 [R / 2];
+    ``inv_freq`` float64 [R / 2], R the rotated part of the head dim.
+    ``adjacent`` pairs elements (2i, 2i + 1) instead of (i, i + R / 2).
+    A negative slot writes nothing for its token.  Returns the rotated q,
+    bf16 [T, Hq, D] (``out``; may be a dense ``q`` itself)."""
+    k_stride, v_stride = _token_stride(k, "k"), _token_stride(v, "v")
+    kv_dtype = _caches(k_cache, v_cache, k_scales, v_scales)
+    T, Hkv, D = k.shape
+    NB, Hkv2, B, D2 = k_cache.shape
+    if (Hkv2, D2) != (Hkv, D) or v.shape != k.shape:
+        raise ValueError("inconsistent K/V and cache shapes")
+    _need(positions, "positions", (torch.int32,))
+    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError(f"positions must be [tokens] or [axes, tokens] (got {tuple(positions.shape)})")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    _need(inv_freq, "inv_freq", (torch.float64,), 1)
+    if pair_axis is not None:
+        _need_shape(pair_axis, "pair_axis", (torch.int32,), inv_freq.shape)
+    _need_shape(slot_mapping, "slot_mapping", (torch.int32,), (T,))
+    Hq, q_stride = 0, 0
+    if q is not None:
+        q_stride = _token_stride(q, "q")
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("inconsistent q and k shapes")
+        if out is None:
+            out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        _need_shape(out, "out", (torch.bfloat16,), q.shape)
+    _same_device(k, q=q, v=v, positions=positions, inv_freq=inv_freq, slot_mapping=slot_mapping,
+                 k_cache=k_cache, v_cache=v_cache, pair_axis=pair_axis, k_scales=k_scales,
+                 v_scales=v_scales, out=out)
+    _check(_lib_handle().pa_rope_append(
+        _ptr(q), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, positions.data_ptr(), axes,
+        inv_freq.data_ptr(), _ptr(pair_axis), 2 * inv_freq.shape[0], 1 if adjacent else 0,
+        float(magnitude), slot_mapping.data_ptr(), T, Hq, _ptr(out) if q is not None else None,
+        k_cache.data_ptr(), v_cache.data_ptr(), NB, Hkv, D, B, kv_dtype, float(kv_scale),
+        _ptr(k_scales), _ptr(v_scales), _stream(stream)))
+    return out
+
+
+def alloc_block_summary(k_cache: torch.Tensor):
+    """(summary int8 [NB, Hkv, 2, D], exponents int8 [NB, Hkv]) for a cache,
+    zeroed; pa_block_summary fills in a block when its last token arrives."""
+    NB, Hkv, _, D = k_cache.shape
+    return (torch.zeros(NB, Hkv, 2, D, dtype=torch.int8, device=k_cache.device),
+            torch.zeros(NB, Hkv, dtype=torch.int8, device=k_cache.device))
+
+
+def _summaries(summary, exponents, NB, Hkv, D):
+    _need_shape(summary, "summary", (torch.int8,), (NB, Hkv, 2, D))
+    _need_shape(exponents, "exponents", (torch.int8,), (NB, Hkv))
+
+
+def block_summary(k_cache: torch.Tensor, slot_mapping: torch.Tensor, summary: torch.Tensor,
+                  exponents: torch.Tensor, stream=None) -> None:
+    """int8 bounds of the keys of every block whose last row is among the
+    slots (call it after the append, with the append's slots); in place."""
+    kv_dtype = cache_dtype_of(k_cache)
+    _need(k_cache, "k_cache", _CACHE_DTYPES[kv_dtype], 4)
+    _need(slot_mapping, "slot_mapping", (torch.int32,), 1)
+    NB, Hkv, B, D = k_cache.shape
+    _summaries(summary, exponents, NB, Hkv, D)
+    _same_device(k_cache, slot_mapping=slot_mapping, summary=summary, exponents=exponents)
+    _check(_lib_handle().pa_block_summary(
+        k_cache.data_ptr(), slot_mapping.data_ptr(), slot_mapping.shape[0], NB, Hkv, D, B, kv_dtype,
+        summary.data_ptr(), exponents.data_ptr(), _stream(stream)))
+
+
+def _rows_of(q, block_tables, context_lens):
+    _need(q, "q", (torch.bfloat16,), 3)
+    _need(block_tables, "block_tables", (torch.int32,), 2)
+    S = q.shape[0]
+    if block_tables.shape[0] != S:
+        raise ValueError("block_tables needs one row per query row")
+    _need_shape(context_lens, "context_lens", (torch.int32,), (S,))
+
+
+def _choice(S, Hkv, top_k, selected, counts, device):
+    if selected is None:
+        selected = torch.empty(S, Hkv, top_k, dtype=torch.int32, device=device)
+    if counts is None:
+        counts = torch.empty(S, Hkv, dtype=torch.int32, device=device)
+    _need_shape(selected, "selected", (torch.int32,), (S, Hkv, top_k))
+    _need_shape(counts, "counts", (torch.int32,), (S, Hkv))
+    return selected, counts
+
+
+def sparse_select(q: torch.Tensor, summary: torch.Tensor, exponents: torch.Tensor,
+                  block_tables: torch.Tensor, context_lens: torch.Tensor, block_size: int, top_k: int,
+                  sink_blocks: int = 1, recent_blocks: int = 2, selected: torch.Tensor | None = None,
+                  counts: torch.Tensor | None = None, stream=None):
+    """The ``top_k`` logical blocks each (row, KV head) should attend to: the
+    first ``sink_blocks``, the last ``recent_blocks`` and those with the
+    largest bound of q . k (pa_sparse_select).  Returns (selected int32
+    [S, Hkv, top_k] ascending then -1, counts int32 [S, Hkv])."""
+    _rows_of(q, block_tables, context_lens)
+    _need(summary, "summary", (torch.int8,), 4)
+    S, Hq, D = q.shape
+    NB, Hkv = summary.shape[:2]
+    _summaries(summary, exponents, NB, Hkv, D)
+    selected, counts = _choice(S, Hkv, int(top_k), selected, counts, q.device)
+    _same_device(q, summary=summary, exponents=exponents, block_tables=block_tables,
+                 context_lens=context_lens, selected=selected, counts=counts)
+    _check(_lib_handle().pa_sparse_select(
+        q.data_ptr(), summary.data_ptr(), exponents.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), S, Hq, Hkv, D, NB, int(block_size),
+        int(top_k), int(sink_blocks), int(recent_blocks), selected.data_ptr(), counts.data_ptr(),
+        _stream(stream)))
+    return selected, counts
+
+
+def sparse_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  block_tables: torch.Tensor, context_lens: torch.Tensor, selected: torch.Tensor,
+                  counts: torch.Tensor, softmax_scale: float | None = None, kv_scale: float = 1.0,
+                  k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                  splits: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Decode attention over the first ``counts`` listed logical blocks of
+    each (row, KV head) (pa_sparse_decode); returns bf16 [S, Hq, D]."""
+    _rows_of(q, block_tables, context_lens)
+    kv_dtype = _caches(k_cache, v_cache, k_scales, v_scales)
+    S, Hq, D = q.shape
+    NB, Hkv, B, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("inconsistent q / cache shapes")
+    _need(selected, "selected", (torch.int32,), 3)
+    _choice(S, Hkv, selected.shape[2], selected, counts, q.device)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    _need_shape(out, "out", (torch.bfloat16,), q.shape)
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 context_lens=context_lens, selected=selected, counts=counts, k_scales=k_scales,
+                 v_scales=v_scales, out=out)
+    _check(_lib_handle().pa_sparse_decode(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), S, Hq, Hkv, D, NB, B, kv_dtype,
+        float(kv_scale), _ptr(k_scales), _ptr(v_scales), float(softmax_scale), selected.data_ptr(),
+        counts.data_ptr(), selected.shape[2], int(splits), out.data_ptr(), _stream(stream)))
+    return out
+
+
+def sparse_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, summary: torch.Tensor,
+                  exponents: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                  top_k: int, sink_blocks: int = 1, recent_blocks: int = 2,
+                  softmax_scale: float | None = None, kv_scale: float = 1.0,
+                  k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                  selected: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """sparse_select and sparse_decode in one call (pa_sparse_attend, two
+    kernels); returns bf16 [S, Hq, D] and leaves the choice in ``selected``
+    and ``counts`` when they are given."""
+    _rows_of(q, block_tables, context_lens)
+    kv_dtype = _caches(k_cache, v_cache, k_scales, v_scales)
+    S, Hq, D = q.shape
+    NB, Hkv, B, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("inconsistent q / cache shapes")
+    _summaries(summary, exponents, NB, Hkv, D)
+    selected, counts = _choice(S, Hkv, int(top_k), selected, counts, q.device)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    _need_shape(out, "out", (torch.bfloat16,), q.shape)
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, summary=summary, exponents=exponents,
+                 block_tables=block_tables, context_lens=context_lens, selected=selected,
+                 counts=counts, k_scales=k_scales, v_scales=v_scales, out=out)
+    _check(_lib_handle().pa_sparse_attend(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), summary.data_ptr(),
+        exponents.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), S, Hq, Hkv, D, NB, B, kv_dtype, float(kv_scale), _ptr(k_scales),
+        _ptr(v_scales), float(softmax_scale), int(top_k), int(sink_blocks), int(recent_blocks),
+        selected.data_ptr(), counts.data_ptr(), out.data_ptr(), _stream(stream)))
+    return out
+
+
+class SparseDecodeStep:
+    """One decode step of one attention layer that rotates its own q and k
+    and reads a chosen part of the context: slot mapping, rotate-and-append,
+    bounds of the blocks that the step completes, choice of ``top_k`` blocks
+    per KV head, attention over them.  Every buffer is allocated here; calling
+    it allocates nothing.  ``positions`` (int32 [S] or [axes, S]) is the
+    caller's, read at every call like ``context_lens``.  For a cache that
+    already holds tokens give the ``summary`` and ``exponents`` that describe
+    its full blocks.  Works as a step of ``StepGraph``."""
+
+    def __init__(self, k_cache, v_cache, block_tables, context_lens, positions, inv_freq, num_q_heads,
+                 top_k, sink_blocks=1, recent_blocks=2, softmax_scale=None, kv_scale=1.0, k_scales=None,
+                 v_scales=None, pair_axis=None, adjacent=False, magnitude=1.0, summary=None,
+                 exponents=None):
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.block_tables, self.context_lens, self.positions = block_tables, context_lens, positions
+        self.inv_freq, self.pair_axis = inv_freq, pair_axis
+        self.adjacent, self.magnitude = adjacent, magnitude
+        _, Hkv, self.B, D = k_cache.shape
+        S, dev = block_tables.shape[0], k_cache.device
+        self.top_k, self.sink_blocks, self.recent_blocks = top_k, sink_blocks, recent_blocks
+        self.softmax_scale = softmax_scale
+        self.kv_scale, self.k_scales, self.v_scales = kv_scale, k_scales, v_scales
+        if summary is None:
+            summary, exponents = alloc_block_summary(k_cache)
+        self.summary, self.exponents = summary, exponents
+        self.slots = torch.empty(S, dtype=torch.int32, device=dev)
+        self.q_rotated = torch.empty(S, num_q_heads, D, dtype=torch.bfloat16, device=dev)
+        self.selected = torch.empty(S, Hkv, top_k, dtype=torch.int32, device=dev)
+        self.counts = torch.empty(S, Hkv, dtype=torch.int32, device=dev)
+        self.out = torch.empty(S, num_q_heads, D, dtype=torch.bfloat16, device=dev)
+
+    def launches(self) -> int:
+        """Kernels one call launches."""
+        return 5
+
+    def __call__(self, q, k_new, v_new, stream=None):
+        slot_mapping(self.block_tables, self.context_lens, self.B, out=self.slots, stream=stream)
+        rope_append(q, k_new, v_new, self.positions, self.inv_freq, self.slots, self.k_cache,
+                    self.v_cache, self.pair_axis, self.adjacent, self.magnitude, self.kv_scale,
+                    self.k_scales, self.v_scales, self.q_rotated, stream)
+        block_summary(self.k_cache, self.slots, self.summary, self.exponents, stream)
+        return sparse_attend(self.q_rotated, self.k_cache, self.v_cache, self.summary, self.exponents,
+                             self.block_tables, self.context_lens, self.top_k, self.sink_blocks,
+                             self.recent_blocks, self.softmax_scale, self.kv_scale, self.k_scales,
+                             self.v_scales, self.selected, self.counts, self.out, stream)
+
+
 class StepGraph:
     """Several layers' decode steps captured into one CUDA graph.
 

@@ -1,0 +1,322 @@
+// Rotate-and-append: the position rotation of a batch of new tokens' q and k
+// rows, and the write of their k and v rows into the paged cache, in one
+// kernel ("Optimizing Llama 3.1 405B Inference with vLLM PagedAttention",
+// section "PagedAttention Mechanics": a token's K and V are appended on
+// arrival; the pages leave the rotation to the model).
+//
+// Mathematics: pair i of a row (x_a, x_b) is turned by the angle
+// theta = position * inv_freq[i]:
+//   x'_a = m (x_a cos theta - x_b sin theta)
+//   x'_b = m (x_a sin theta + x_b cos theta)
+// The angle is reduced exactly: inv_freq / 2 pi, taken modulo one turn, is
+// held as a 64-bit fraction F of a turn, and position * F modulo 2^64 is the
+// angle as a fraction of a turn with no rounding in the product, however far
+// the position.  One rounding of F (2^-53 relative) times the position is
+// all that is lost before sine and cosine are taken in fp32.
+//
+// Bound: memory.  Every q, k, v element is read once and written once.
+#include "pa_device.cuh"
+
+namespace pa {
+namespace rope {
+
+struct Args {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const int32_t *positions;              // [axes][num_tokens]
+    const double *inv_freq;                // [rotary_dim / 2]
+    const int32_t *pair_axis;              // [rotary_dim / 2] or null (axis 0)
+    const int32_t *slots;
+    __nv_bfloat16 *q_out;
+    uint8_t *k_cache, *v_cache;
+    int64_t num_slots;
+    int num_tokens, num_axes, num_q_heads, num_kv_heads, block_size;
+    int pairs;       // rotary_dim / 2
+    int tile;        // tokens per CTA
+    int rows_per_y;  // rows (of one token's q, k and v heads) per CTA
+    float magnitude, kv_scale;
+    const float *k_scales, *v_scales;
+    unsigned int *err;
+};
+
+constexpr int kThreads = 256;
+constexpr int kMaxTile = 8;
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(h[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]), pack2<false>(x[4], x[5]),
+                      pack2<false>(x[6], x[7]));
+}
+
+// Eight fp32 values as E4M3 codes of x / scale: one rounding from fp32 (the
+// rotated row is not rounded to bf16 on the way).
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t packed = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 f = make_float2(__fdiv_rn(x[4 * i + 2 * j], scale),
+                                         __fdiv_rn(x[4 * i + 2 * j + 1], scale));
+            packed |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3))
+                      << (16 * j);
+        }
+        w[i] = packed;
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// A thread works on 16 elements of one head's row at a time: with pairs
+// (i, i + R/2) elements 8j .. 8j+7 and their partners, with adjacent pairs
+// elements 16j .. 16j+15; either way pairs 8j .. 8j+7, and two 16-byte loads.
+// Its j is the same for every row it takes.
+template <int D, bool FP8, bool ADJACENT>
+__global__ void __launch_bounds__(kThreads) append_kernel(const Args a) {
+    constexpr int VPR = D / 16;  // threads to a row
+    __shared__ __align__(16) float cs[kMaxTile][D / 2], sn[kMaxTile][D / 2];
+    __shared__ int32_t slot_s[kMaxTile];
+    const int t0 = blockIdx.x * a.tile;
+    const int live = min(a.tile, a.num_tokens - t0);
+
+    for (int i = threadIdx.x; i < live * a.pairs; i += kThreads) {
+        const int tt = i / a.pairs, p = i - tt * a.pairs;
+        int axis = a.pair_axis ? a.pair_axis[p] : 0;
+        if (axis < 0 || axis >= a.num_axes) {
+            set_device_error(a.err, PA_DEVERR_BAD_AXIS);
+            axis = 0;
+        }
+        const int pos = a.positions[static_cast<int64_t>(axis) * a.num_tokens + t0 + tt];
+        const double turns = a.inv_freq[p] * 0.15915494309189533577;  // 1 / 2 pi
+        const uint64_t frac =
+            __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);  // 2^64
+        const uint64_t phase = frac * static_cast<uint64_t>(static_cast<int64_t>(pos));
+        // the upper 32 bits, signed: half turns in [-1, 1)
+        const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
+        float s, c;
+        sincospif(x, &s, &c);
+        cs[tt][p] = c * a.magnitude;
+        sn[tt][p] = s * a.magnitude;
+    }
+    if (threadIdx.x < live) {
+        int32_t slot = a.slots[t0 + threadIdx.x];
+        if (slot >= a.num_slots) {
+            if (blockIdx.y == 0) set_device_error(a.err, PA_DEVERR_BAD_SLOT);
+            slot = -1;
+        }
+        slot_s[threadIdx.x] = slot;
+    }
+    __syncthreads();
+
+    const int j = threadIdx.x % VPR;
+    const int rows = a.num_q_heads + 2 * a.num_kv_heads;
+    const int row0 = blockIdx.y * a.rows_per_y;
+    const int nrows = min(a.rows_per_y, rows - row0);
+    const bool turn = 8 * j < a.pairs;
+    // first elements of the thread's two vectors
+    const int rest = 2 * a.pairs + 16 * (j - a.pairs / 8);
+    const int ea = !turn ? rest : ADJACENT ? 16 * j : 8 * j;
+    const int eb = !turn || ADJACENT ? ea + 8 : a.pairs + 8 * j;
+    for (int i = threadIdx.x / VPR; i < live * nrows; i += kThreads / VPR) {
+        const int tt = i / nrows, row = row0 + i - tt * nrows;
+        const int64_t t = t0 + tt;
+        const bool is_q = row < a.num_q_heads;
+        const bool is_v = row >= a.num_q_heads + a.num_kv_heads;
+        const int h = is_q ? row : row - a.num_q_heads - (is_v ? a.num_kv_heads : 0);
+        const int32_t slot = slot_s[tt];
+        if (!is_q && slot < 0) continue;
+        const __nv_bfloat16 *src = is_q   ? a.q + t * a.q_stride
+                                   : is_v ? a.v + t * a.v_stride
+                                          : a.k + t * a.k_stride;
+        src += static_cast<int64_t>(h) * D;
+        uint4 wa, wb;
+        int da = ea, db = eb;
+        if (is_v) {
+            da = 16 * j;
+            db = da + 8;
+        }
+        wa = *reinterpret_cast<const uint4 *>(src + da);
+        wb = *reinterpret_cast<const uint4 *>(src + db);
+        const int64_t dst =
+            is_q ? (t * a.num_q_heads + h) * D
+                 : ((static_cast<int64_t>(slot / a.block_size) * a.num_kv_heads + h) * a.block_size +
+                    slot % a.block_size) * D;
+        const bool rotate = turn && !is_v;
+        if (!rotate && (!FP8 || is_q)) {  // bits as they are
+            __nv_bfloat16 *to = is_q   ? a.q_out
+                                : is_v ? reinterpret_cast<__nv_bfloat16 *>(a.v_cache)
+                                       : reinterpret_cast<__nv_bfloat16 *>(a.k_cache);
+            *reinterpret_cast<uint4 *>(to + dst + da) = wa;
+            *reinterpret_cast<uint4 *>(to + dst + db) = wb;
+            continue;
+        }
+        float xa[8], xb[8];
+        unpack8(wa, xa);
+        unpack8(wb, xb);
+        if (rotate) {
+            float c[8], s[8];
+#pragma unroll
+            for (int u = 0; u < 8; u += 4) {
+                *reinterpret_cast<float4 *>(c + u) = *reinterpret_cast<const float4 *>(&cs[tt][8 * j + u]);
+                *reinterpret_cast<float4 *>(s + u) = *reinterpret_cast<const float4 *>(&sn[tt][8 * j + u]);
+            }
+            auto rot = [&](float &u, float &w, int i8) {
+                const float p = u, r = w;
+                u = fmaf(p, c[i8], -(r * s[i8]));
+                w = fmaf(p, s[i8], r * c[i8]);
+            };
+            if constexpr (ADJACENT) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    rot(xa[2 * u], xa[2 * u + 1], u);
+                    rot(xb[2 * u], xb[2 * u + 1], 4 + u);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) rot(xa[u], xb[u], u);
+            }
+        }
+        if (is_q) {
+            *reinterpret_cast<uint4 *>(a.q_out + dst + da) = pack8(xa);
+            *reinterpret_cast<uint4 *>(a.q_out + dst + db) = pack8(xb);
+        } else if constexpr (FP8) {
+            const float *scales = is_v ? a.v_scales : a.k_scales;
+            const float scale = scales ? scales[h] : a.kv_scale;
+            uint8_t *to = is_v ? a.v_cache : a.k_cache;
+            *reinterpret_cast<uint2 *>(to + dst + da) = codes8(xa, scale);
+            *reinterpret_cast<uint2 *>(to + dst + db) = codes8(xb, scale);
+        } else {
+            __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.k_cache);
+            *reinterpret_cast<uint4 *>(to + dst + da) = pack8(xa);
+            *reinterpret_cast<uint4 *>(to + dst + db) = pack8(xb);
+        }
+    }
+}
+
+template <int D, bool FP8>
+static void launch(const Args &a, bool adjacent, dim3 grid, cudaStream_t stream) {
+    if (adjacent)
+        append_kernel<D, FP8, true><<<grid, kThreads, 0, stream>>>(a);
+    else
+        append_kernel<D, FP8, false><<<grid, kThreads, 0, stream>>>(a);
+}
+
+static bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + nq && b < a + np;
+}
+
+}  // namespace rope
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                    const void *v, int64_t v_stride, const int32_t *positions,
+                                    int num_axes, const double *inv_freq, const int32_t *pair_axis,
+                                    int rotary_dim, int adjacent, float magnitude,
+                                    const int32_t *slot_mapping, int num_tokens, int num_q_heads,
+                                    void *q_out, void *k_cache, void *v_cache, int num_blocks,
+                                    int num_kv_heads, int head_dim, int block_size,
+                                    pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
+                                    const float *v_scales, cudaStream_t stream) {
+    clear_error();
+    if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_blocks <= 0)
+        return fail(PA_ERR_INVALID_ARG, "bad size (num_tokens=%d, num_q_heads=%d, num_kv_heads=%d, num_blocks=%d)",
+                    num_tokens, num_q_heads, num_kv_heads, num_blocks);
+    if (num_q_heads > 65535 || num_kv_heads > 65535)
+        return fail(PA_ERR_UNSUPPORTED, "more than 65535 heads");
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
+    if (block_size != 16 && block_size != 32)
+        return fail(PA_ERR_UNSUPPORTED, "block_size %d (supported: 16, 32)", block_size);
+    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3)
+        return fail(PA_ERR_UNSUPPORTED, "kv_dtype %d", static_cast<int>(kv_dtype));
+    if (rotary_dim <= 0 || rotary_dim > head_dim)
+        return fail(PA_ERR_INVALID_ARG, "rotary_dim %d outside 1..head_dim %d", rotary_dim, head_dim);
+    if (rotary_dim % 16 != 0)
+        return fail(PA_ERR_UNSUPPORTED, "rotary_dim %d is not a multiple of 16", rotary_dim);
+    if (num_axes < 1 || num_axes > 16)
+        return fail(num_axes < 1 ? PA_ERR_INVALID_ARG : PA_ERR_UNSUPPORTED, "num_axes %d (supported: 1..16)", num_axes);
+    if (num_axes > 1 && !pair_axis)
+        return fail(PA_ERR_INVALID_ARG, "pair_axis is needed with more than one axis");
+    if (!(magnitude > 0.f && magnitude <= 3.4e38f))
+        return fail(PA_ERR_INVALID_ARG, "magnitude must be positive and finite");
+    if ((k_scales == nullptr) != (v_scales == nullptr))
+        return fail(PA_ERR_INVALID_ARG, "k_scales and v_scales must both be given or both be NULL");
+    if (k_scales && kv_dtype != PA_KV_FP8_E4M3)
+        return fail(PA_ERR_INVALID_ARG, "per-head scales need an E4M3 cache");
+    if (kv_dtype == PA_KV_FP8_E4M3 && !k_scales && !(kv_scale > 0.f && kv_scale <= 3.4e38f))
+        return fail(PA_ERR_INVALID_ARG, "fp8 kv_scale must be positive and finite");
+    if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffffLL)
+        return fail(PA_ERR_UNSUPPORTED, "pool of %d blocks exceeds 2^31 slots", num_blocks);
+    if (num_tokens == 0) return PA_OK;
+    if (!k || !v || !positions || !inv_freq || !slot_mapping || !k_cache || !v_cache ||
+        (num_q_heads > 0 && (!q || !q_out)))
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out))))
+        return fail(PA_ERR_INVALID_ARG, "q, k, v, q_out, k_cache and v_cache must be 16-byte aligned");
+    const int64_t qrow = static_cast<int64_t>(num_q_heads) * head_dim;
+    const int64_t krow = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (k_stride % 8 || v_stride % 8 || (num_q_heads > 0 && q_stride % 8))
+        return fail(PA_ERR_INVALID_ARG, "token strides must be multiples of 8 elements");
+    if (num_tokens > 1 && (k_stride < krow || v_stride < krow || (num_q_heads > 0 && q_stride < qrow)))
+        return fail(PA_ERR_INVALID_ARG, "a token stride is smaller than one token's rows");
+    if (num_q_heads > 0 && !(q == q_out && (num_tokens == 1 || q_stride == qrow))) {
+        const size_t span = (static_cast<size_t>(num_tokens - 1) * q_stride + qrow) * 2;
+        if (rope::overlaps(q, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
+            return fail(PA_ERR_INVALID_ARG, "q_out overlaps q but is not q itself");
+    }
+    unsigned int *err = device_error_word();
+    if (!err) return fail(PA_ERR_CUDA, "cannot resolve the device error word");
+
+    rope::Args a;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.pair_axis = pair_axis;
+    a.slots = slot_mapping;
+    a.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    a.k_cache = static_cast<uint8_t *>(k_cache);
+    a.v_cache = static_cast<uint8_t *>(v_cache);
+    a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    a.num_tokens = num_tokens;
+    a.num_axes = num_axes;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.pairs = rotary_dim / 2;
+    a.magnitude = magnitude;
+    a.kv_scale = kv_scale;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.err = err;
+    const int rows = num_q_heads + 2 * num_kv_heads;
+    a.tile = num_tokens >= 8 * 152 * 4 ? 8 : num_tokens >= 4 * 152 * 4 ? 4 : num_tokens >= 2 * 152 * 4 ? 2 : 1;
+    const int at_once = rope::kThreads / (head_dim / 16);  // rows of one pass of the CTA's threads
+    a.rows_per_y = num_tokens <= 152 ? at_once : rows;
+    const dim3 grid((num_tokens + a.tile - 1) / a.tile, (rows + a.rows_per_y - 1) / a.rows_per_y);
+    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
+    if (head_dim == 128)
+        fp8 ? rope::launch<128, true>(a, adjacent != 0, grid, stream)
+            : rope::launch<128, false>(a, adjacent != 0, grid, stream);
+    else
+        fp8 ? rope::launch<64, true>(a, adjacent != 0, grid, stream)
+            : rope::launch<64, false>(a, adjacent != 0, grid, stream);
+    return cuda_check(cudaGetLastError(), "rope append launch");
+}
