@@ -70,33 +70,6 @@ __device__ __forceinline__ uint32_t at(uint32_t base, int t, int b) {
     return base + slab * (BS * C::SLAB) + t * C::SLAB + (phys << 4) + (within & 15);
 }
 
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-// fp32 at shared-memory address `addr` of the cluster's CTA `rank`
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-    float x;
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\t"
-                 "ld.shared::cluster.f32 %0, [r];\n\t}"
-                 : "=f"(x)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
-    return x;
-}
-
 template <int D, int BS, bool FP8, int NT, int NW, int SPW>
 __global__ void __launch_bounds__(NW * 32, (NT == 2 && BS == 16 && !FP8) ? 3 : 2)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
