@@ -493,7 +493,7 @@ pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t
  *   The other blocks' bounds must have been made by pa_block_summary.
  *   selected int32 [num_rows][num_kv_heads][top_k]: ascending logical blocks,
  *   then -1; counts int32 [num_rows][num_kv_heads].  recent_blocks >= 1,
- *   sink_blocks + recent_blocks <= top_k, max_blocks_per_seq <= 262144.
+ *   sink_blocks + recent_blocks <= top_k, max_blocks_per_seq <= 131072.
  * pa_sparse_decode: out[t][hq] = bf16_rn of the softmax of softmax_scale *
  *   q . K over the tokens (position < n) of the first counts[t][h] blocks of
  *   selected[t][h], applied to V; zeros when there are none.  Any list may be
@@ -503,8 +503,10 @@ pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t
  *   that share a (row, KV head)'s list, 1, 2, 4 or 8; 0 lets the library
  *   choose.  One kernel, no workspace.  With an E4M3 cache the query is
  *   rounded to fp16 as in pa_decode_partitions.
- * pa_sparse_attend: pa_sparse_select followed by pa_sparse_decode on the same
- *   stream (two kernels); selected and counts are outputs.
+ * pa_sparse_attend: pa_sparse_select followed by pa_sparse_decode; selected and
+ *   counts are outputs.  One kernel, in which each (row, KV head)'s CTAs choose
+ *   and attend, so that one row's attention hides another's choice; two kernels
+ *   when max_blocks_per_seq > 65536.
  */
 pa_status pa_block_summary(const void *k_cache, const int32_t *slot_mapping, int num_tokens,
                            int num_blocks, int num_kv_heads, int head_dim, int block_size,

@@ -6,6 +6,8 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,7 +76,33 @@ SIGNATURES = {
     "pa_last_error": (ctypes.c_char_p, []),
 }
 
+BINDING_PATH = os.path.join(HERE, "_build", "_pa_binding.so")
+# the calls of the CPython binding, in the order its bind() takes their addresses
+BINDING_CALLS = ("pa_rope_append", "pa_block_summary", "pa_sparse_select", "pa_sparse_decode", "pa_sparse_attend")
+
 _lib = None
+_binding = None
+
+
+def binding():
+    """The CPython binding, calling into the library that load() gives.  Like
+    load(), raises ImportError when it has not been built."""
+    global _binding
+    if _binding is None:
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(
+                f"{BINDING_PATH} not found: build the CUDA library first "
+                "(python -c 'import __graft_entry__ as g; g.build()')")
+        import torch  # noqa: F401  (the module links against its libraries)
+        loader = importlib.machinery.ExtensionFileLoader("_pa_binding", BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_pa_binding", BINDING_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        lib = load()
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in BINDING_CALLS))
+        _binding = module
+    return _binding
+
 
 
 def load(path: str | None = None) -> ctypes.CDLL:

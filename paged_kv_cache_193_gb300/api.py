@@ -488,56 +488,6 @@ class DecodeStep:
 # rotate-and-append, page bounds, block-sparse decode
 # ---------------------------------------------------------------------------
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    """All tensors on the current CUDA device (whose stream the call uses)."""
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}; expected {dev}")
-
-
-def _need_shape(t: torch.Tensor, name: str, dtypes, shape) -> None:
-    _need(t, name, dtypes)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-
-
-def _token_stride(t: torch.Tensor, name: str) -> int:
-    """Elements from one token's row [heads, head_dim] to the next of a bf16
-    tensor [tokens, heads, head_dim] whose rows are dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} has dtype {t.dtype}; expected bfloat16")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dimensions (got shape {tuple(t.shape)})")
-    T, H, D = t.shape
-    st, sh, sd = t.stride()
-    if (D > 1 and sd != 1) or (H > 1 and sh != D):
-        raise ValueError(f"{name}: each token's [heads, head_dim] rows must be dense")
-    return st if T > 1 else H * D
-
-
-def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales, v_scales) -> int:
-    kv_dtype = cache_dtype_of(k_cache)
-    _need(k_cache, "k_cache", _CACHE_DTYPES[kv_dtype], 4)
-    _need_shape(v_cache, "v_cache", _CACHE_DTYPES[kv_dtype], k_cache.shape)
-    if (k_scales is None) != (v_scales is None):
-        raise ValueError("k_scales and v_scales must both be given or both be None")
-    if k_scales is not None:
-        _need_shape(k_scales, "k_scales", (torch.float32,), k_cache.shape[1:2])
-        _need_shape(v_scales, "v_scales", (torch.float32,), k_cache.shape[1:2])
-    return kv_dtype
-
-
-def _ptr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
-
-
 def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
                 inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
                 v_cache: torch.Tensor, pair_axis: torch.Tensor | None = None, adjacent: bool = False,
@@ -554,85 +504,37 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positi
     ``adjacent`` pairs elements (2i, 2i + 1) instead of (i, i + R / 2).
     A negative slot writes nothing for its token.  Returns the rotated q,
     bf16 [T, Hq, D] (``out``; may be a dense ``q`` itself)."""
-    k_stride, v_stride = _token_stride(k, "k"), _token_stride(v, "v")
-    kv_dtype = _caches(k_cache, v_cache, k_scales, v_scales)
-    T, Hkv, D = k.shape
-    NB, Hkv2, B, D2 = k_cache.shape
-    if (Hkv2, D2) != (Hkv, D) or v.shape != k.shape:
-        raise ValueError("inconsistent K/V and cache shapes")
-    _need(positions, "positions", (torch.int32,))
-    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
-        raise ValueError(f"positions must be [tokens] or [axes, tokens] (got {tuple(positions.shape)})")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    _need(inv_freq, "inv_freq", (torch.float64,), 1)
-    if pair_axis is not None:
-        _need_shape(pair_axis, "pair_axis", (torch.int32,), inv_freq.shape)
-    _need_shape(slot_mapping, "slot_mapping", (torch.int32,), (T,))
-    Hq, q_stride = 0, 0
-    if q is not None:
-        q_stride = _token_stride(q, "q")
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D:
-            raise ValueError("inconsistent q and k shapes")
-        if out is None:
-            out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-        _need_shape(out, "out", (torch.bfloat16,), q.shape)
-    _same_device(k, q=q, v=v, positions=positions, inv_freq=inv_freq, slot_mapping=slot_mapping,
-                 k_cache=k_cache, v_cache=v_cache, pair_axis=pair_axis, k_scales=k_scales,
-                 v_scales=v_scales, out=out)
-    _check(_lib_handle().pa_rope_append(
-        _ptr(q), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, positions.data_ptr(), axes,
-        inv_freq.data_ptr(), _ptr(pair_axis), 2 * inv_freq.shape[0], 1 if adjacent else 0,
-        float(magnitude), slot_mapping.data_ptr(), T, Hq, _ptr(out) if q is not None else None,
-        k_cache.data_ptr(), v_cache.data_ptr(), NB, Hkv, D, B, kv_dtype, float(kv_scale),
-        _ptr(k_scales), _ptr(v_scales), _stream(stream)))
-    return out
+    if out is None and isinstance(q, torch.Tensor):
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    status = _lib.binding().rope_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, pair_axis,
+                                        adjacent, magnitude, kv_scale, k_scales, v_scales, out, stream)
+    if status is not None:
+        _check(status)
+    return None if q is None else out
 
 
 def alloc_block_summary(k_cache: torch.Tensor):
     """(summary int8 [NB, Hkv, 2, D], exponents int8 [NB, Hkv]) for a cache,
-    zeroed; pa_block_summary fills in a block when its last token arrives."""
+    zeroed; block_summary fills in a block when its last token arrives."""
     NB, Hkv, _, D = k_cache.shape
     return (torch.zeros(NB, Hkv, 2, D, dtype=torch.int8, device=k_cache.device),
             torch.zeros(NB, Hkv, dtype=torch.int8, device=k_cache.device))
-
-
-def _summaries(summary, exponents, NB, Hkv, D):
-    _need_shape(summary, "summary", (torch.int8,), (NB, Hkv, 2, D))
-    _need_shape(exponents, "exponents", (torch.int8,), (NB, Hkv))
 
 
 def block_summary(k_cache: torch.Tensor, slot_mapping: torch.Tensor, summary: torch.Tensor,
                   exponents: torch.Tensor, stream=None) -> None:
     """int8 bounds of the keys of every block whose last row is among the
     slots (call it after the append, with the append's slots); in place."""
-    kv_dtype = cache_dtype_of(k_cache)
-    _need(k_cache, "k_cache", _CACHE_DTYPES[kv_dtype], 4)
-    _need(slot_mapping, "slot_mapping", (torch.int32,), 1)
-    NB, Hkv, B, D = k_cache.shape
-    _summaries(summary, exponents, NB, Hkv, D)
-    _same_device(k_cache, slot_mapping=slot_mapping, summary=summary, exponents=exponents)
-    _check(_lib_handle().pa_block_summary(
-        k_cache.data_ptr(), slot_mapping.data_ptr(), slot_mapping.shape[0], NB, Hkv, D, B, kv_dtype,
-        summary.data_ptr(), exponents.data_ptr(), _stream(stream)))
+    status = _lib.binding().block_summary(k_cache, slot_mapping, summary, exponents, stream)
+    if status is not None:
+        _check(status)
 
 
-def _rows_of(q, block_tables, context_lens):
-    _need(q, "q", (torch.bfloat16,), 3)
-    _need(block_tables, "block_tables", (torch.int32,), 2)
-    S = q.shape[0]
-    if block_tables.shape[0] != S:
-        raise ValueError("block_tables needs one row per query row")
-    _need_shape(context_lens, "context_lens", (torch.int32,), (S,))
-
-
-def _choice(S, Hkv, top_k, selected, counts, device):
+def _choice(q, Hkv, top_k, selected, counts):
     if selected is None:
-        selected = torch.empty(S, Hkv, top_k, dtype=torch.int32, device=device)
+        selected = torch.empty(q.shape[0], Hkv, top_k, dtype=torch.int32, device=q.device)
     if counts is None:
-        counts = torch.empty(S, Hkv, dtype=torch.int32, device=device)
-    _need_shape(selected, "selected", (torch.int32,), (S, Hkv, top_k))
-    _need_shape(counts, "counts", (torch.int32,), (S, Hkv))
+        counts = torch.empty(q.shape[0], Hkv, dtype=torch.int32, device=q.device)
     return selected, counts
 
 
@@ -644,19 +546,12 @@ def sparse_select(q: torch.Tensor, summary: torch.Tensor, exponents: torch.Tenso
     first ``sink_blocks``, the last ``recent_blocks`` and those with the
     largest bound of q . k (pa_sparse_select).  Returns (selected int32
     [S, Hkv, top_k] ascending then -1, counts int32 [S, Hkv])."""
-    _rows_of(q, block_tables, context_lens)
-    _need(summary, "summary", (torch.int8,), 4)
-    S, Hq, D = q.shape
-    NB, Hkv = summary.shape[:2]
-    _summaries(summary, exponents, NB, Hkv, D)
-    selected, counts = _choice(S, Hkv, int(top_k), selected, counts, q.device)
-    _same_device(q, summary=summary, exponents=exponents, block_tables=block_tables,
-                 context_lens=context_lens, selected=selected, counts=counts)
-    _check(_lib_handle().pa_sparse_select(
-        q.data_ptr(), summary.data_ptr(), exponents.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), S, Hq, Hkv, D, NB, int(block_size),
-        int(top_k), int(sink_blocks), int(recent_blocks), selected.data_ptr(), counts.data_ptr(),
-        _stream(stream)))
+    if selected is None or counts is None:
+        selected, counts = _choice(q, summary.shape[1], top_k, selected, counts)
+    status = _lib.binding().sparse_select(q, summary, exponents, block_tables, context_lens, block_size, top_k,
+                                          sink_blocks, recent_blocks, selected, counts, stream)
+    if status is not None:
+        _check(status)
     return selected, counts
 
 
@@ -667,27 +562,14 @@ def sparse_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   splits: int = 0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Decode attention over the first ``counts`` listed logical blocks of
     each (row, KV head) (pa_sparse_decode); returns bf16 [S, Hq, D]."""
-    _rows_of(q, block_tables, context_lens)
-    kv_dtype = _caches(k_cache, v_cache, k_scales, v_scales)
-    S, Hq, D = q.shape
-    NB, Hkv, B, D2 = k_cache.shape
-    if D2 != D:
-        raise ValueError("inconsistent q / cache shapes")
-    _need(selected, "selected", (torch.int32,), 3)
-    _choice(S, Hkv, selected.shape[2], selected, counts, q.device)
     if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(D)
+        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
         out = torch.empty_like(q)
-    _need_shape(out, "out", (torch.bfloat16,), q.shape)
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 context_lens=context_lens, selected=selected, counts=counts, k_scales=k_scales,
-                 v_scales=v_scales, out=out)
-    _check(_lib_handle().pa_sparse_decode(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), S, Hq, Hkv, D, NB, B, kv_dtype,
-        float(kv_scale), _ptr(k_scales), _ptr(v_scales), float(softmax_scale), selected.data_ptr(),
-        counts.data_ptr(), selected.shape[2], int(splits), out.data_ptr(), _stream(stream)))
+    status = _lib.binding().sparse_decode(q, k_cache, v_cache, block_tables, context_lens, selected, counts,
+                                          softmax_scale, kv_scale, k_scales, v_scales, splits, out, stream)
+    if status is not None:
+        _check(status)
     return out
 
 
@@ -698,31 +580,20 @@ def sparse_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
                   selected: torch.Tensor | None = None, counts: torch.Tensor | None = None,
                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """sparse_select and sparse_decode in one call (pa_sparse_attend, two
-    kernels); returns bf16 [S, Hq, D] and leaves the choice in ``selected``
-    and ``counts`` when they are given."""
-    _rows_of(q, block_tables, context_lens)
-    kv_dtype = _caches(k_cache, v_cache, k_scales, v_scales)
-    S, Hq, D = q.shape
-    NB, Hkv, B, D2 = k_cache.shape
-    if D2 != D:
-        raise ValueError("inconsistent q / cache shapes")
-    _summaries(summary, exponents, NB, Hkv, D)
-    selected, counts = _choice(S, Hkv, int(top_k), selected, counts, q.device)
+    """sparse_select and sparse_decode in one call (pa_sparse_attend);
+    returns bf16 [S, Hq, D] and leaves the choice in ``selected`` and
+    ``counts`` when they are given."""
+    if selected is None or counts is None:
+        selected, counts = _choice(q, k_cache.shape[1], top_k, selected, counts)
     if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(D)
+        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
         out = torch.empty_like(q)
-    _need_shape(out, "out", (torch.bfloat16,), q.shape)
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, summary=summary, exponents=exponents,
-                 block_tables=block_tables, context_lens=context_lens, selected=selected,
-                 counts=counts, k_scales=k_scales, v_scales=v_scales, out=out)
-    _check(_lib_handle().pa_sparse_attend(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), summary.data_ptr(),
-        exponents.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), S, Hq, Hkv, D, NB, B, kv_dtype, float(kv_scale), _ptr(k_scales),
-        _ptr(v_scales), float(softmax_scale), int(top_k), int(sink_blocks), int(recent_blocks),
-        selected.data_ptr(), counts.data_ptr(), out.data_ptr(), _stream(stream)))
+    status = _lib.binding().sparse_attend(q, k_cache, v_cache, summary, exponents, block_tables, context_lens, top_k,
+                                          sink_blocks, recent_blocks, softmax_scale, kv_scale, k_scales, v_scales,
+                                          selected, counts, out, stream)
+    if status is not None:
+        _check(status)
     return out
 
 
@@ -760,7 +631,7 @@ class SparseDecodeStep:
 
     def launches(self) -> int:
         """Kernels one call launches."""
-        return 5
+        return 4 if self.block_tables.shape[1] <= 65536 else 5
 
     def __call__(self, q, k_new, v_new, stream=None):
         slot_mapping(self.block_tables, self.context_lens, self.B, out=self.slots, stream=stream)

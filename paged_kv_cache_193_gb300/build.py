@@ -3,6 +3,9 @@
 Each ``csrc/*.cu`` file is compiled in parallel with nvcc, then linked into a
 shared library with the CUDA runtime linked statically, so the library only
 needs the driver at run time.  Output: ``paged_kv_cache_193_gb300/_build/libpa.so``.
+Beside it ``csrc/binding.cpp`` becomes ``_pa_binding.so``, the CPython binding
+of the calls whose kernels are shorter than a check of their arguments in
+Python.
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpa.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(OUT_DIR, "_pa_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,6 +58,28 @@ def compile_flags(verbose_ptxas: bool = False) -> list[str]:
     return flags
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the CPython binding if its source is newer; return its path."""
+    newest = max(os.path.getmtime(f) for f in [BINDING_SRC, *_headers(), __file__])
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    lib = os.path.join(root, "lib")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = None,
           defines: tuple[str, ...] = ()) -> str:
     """Compile and link if any source is newer than the library; return its
@@ -59,6 +87,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = No
     variant of the library elsewhere, for launch-shape tuning."""
     lib = out or LIB
     if not force and not defines and out is None and not _stale():
+        build_binding()
         return LIB
     obj_dir = os.path.join(os.path.dirname(lib), os.path.basename(lib) + ".objs") if out else OUT_DIR
     os.makedirs(obj_dir, exist_ok=True)
@@ -74,8 +103,11 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = No
         return obj, r.stderr
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding, force) if out is None else None
         results = list(ex.map(one, srcs))
+        if binding is not None:
+            binding.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)

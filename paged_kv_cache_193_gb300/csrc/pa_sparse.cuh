@@ -15,10 +15,12 @@ constexpr int kMinExp = -60, kMaxExp = 40;
 // Marks a page whose keys hold an infinity or NaN: its score is +infinity.
 constexpr int kOddExp = 127;
 
+constexpr int kSms = 152;
+
 // Longest block-table row of the choice: a cluster of eight CTAs keeps one
-// 32-bit key per page, 128 KB to a CTA.
-constexpr int kMaxTableBlocks = 8 * 32768;
-constexpr int kMaxSelectSmem = 32768 * 4;
+// 32-bit key per page, 64 KB to a CTA beside its copies in flight.
+constexpr int kMaxKeys = 16384;
+constexpr int kMaxTableBlocks = 8 * kMaxKeys;
 
 // ---- thread-block clusters and distributed shared memory ----------------------
 
@@ -92,11 +94,5 @@ inline pa_status raise_smem_limit(const void *kernel, int bytes, std::atomic<uin
 
 pa_status check_select(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
                        int block_size, int max_blocks, int top_k, int sink, int recent);
-pa_status run_select(const void *q, const int8_t *summary, const int8_t *exponents,
-                     const int32_t *block_tables, int max_blocks, const int32_t *context_lens,
-                     int num_rows, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
-                     int block_size, int top_k, int sink, int recent, int32_t *selected,
-                     int32_t *counts, cudaStream_t stream);
-
 }  // namespace sparse
 }  // namespace pa

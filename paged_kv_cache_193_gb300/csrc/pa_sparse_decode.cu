@@ -1,588 +1,9 @@
-// Decode attention over chosen pages: for each (row, KV head) the softmax of
-// softmax_scale * q . K[t] over the tokens of the listed logical pages, applied
-// to V ("vLLM PagedAttention: Memory Optimization & High-Throughput LLM
-// Inference Tuning", section 2, walks every page; here only those of a list
-// are walked).
-//
-// One cluster of CTAs per (row, KV head), the list dealt out over the
-// cluster's warps.  A warp keeps several pages in flight: TMA tile loads of
-// the K and V page into a ring stage of its own, S^T = K Q^T as m16n8k16
-// products with the query group (padded to 8 or 16) as N, one pass of online
-// softmax, O^T += V^T P^T.  The CTA's warps, then the cluster's CTAs over
-// distributed shared memory, join their (max, sum, accumulator) triples, so
-// there is no workspace and no second kernel however few rows there are.
-#include <cudaTypedefs.h>
-
-#include "pa_sparse.cuh"
+// Entry points of the block-sparse decode: attention over a given list, and
+// the choice and the attention in one kernel.
+#include "pa_sparse_attend.cuh"
 
 namespace pa {
 namespace sparse {
-
-struct Args {
-    const __nv_bfloat16 *q;
-    const int32_t *block_tables;
-    const int32_t *context_lens;
-    const int32_t *selected;  // [num_rows][num_kv_heads][top_k] logical pages
-    const int32_t *counts;    // [num_rows][num_kv_heads]
-    __nv_bfloat16 *out;
-    int max_blocks, num_blocks, num_q_heads, num_kv_heads, group, top_k;
-    float softmax_log2;  // softmax_scale * log2(e): scores in base-2 units
-    float kv_scale;
-    const float *k_scales, *v_scales;
-    unsigned int *err;
-    uint64_t wait_limit_ns;
-    int stall_first_wait;
-};
-
-// limit of the drain of copies in flight after a wait gave up
-constexpr uint64_t kDrainNs = 2000000000ull;
-
-template <int D, int BS, bool FP8, int NT, int NW, int SPW>
-struct Shape {
-    static constexpr int ELEM = FP8 ? 1 : 2;
-    static constexpr int ROWB = D * ELEM;                  // bytes of a token's row
-    static constexpr int SLAB = ROWB >= 128 ? 128 : ROWB;  // TMA box width = swizzle span
-    static constexpr int NSLAB = ROWB / SLAB;
-    static constexpr int PAGE = BS * ROWB;
-    static constexpr int PPI = (FP8 && BS == 16) ? 2 : 1;  // pages per step of a warp
-    static constexpr int STAGE = 2 * PPI * PAGE;           // K pages, then V pages
-    static constexpr int NSTAGE = NW * SPW;
-    static constexpr int RING = NSTAGE * STAGE;
-    static constexpr int NP = 8 * NT;  // group padded to the product's N
-    static constexpr int OSTR = D + 4;
-    // the join: a partial output per warp, (reference, sum) per warp and head,
-    // then the CTA's own partial and (reference, sum)
-    static constexpr int JOIN = (NW * NP * OSTR + 2 * NW * NP + NP * D + 2 * NP) * 4;
-    static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + 1024;  // + base alignment
-    static constexpr int MT = BS / 16;   // 16-token tiles of a page
-    static constexpr int MI = PPI * MT;  // and of a step
-    static constexpr int KSTEPS = D / 16;
-    static constexpr int DT = D / 16;
-    static constexpr int CPT = D / 64;  // E4M3: 16-byte pieces per thread and row
-};
-
-// Address of byte b of token row t in a page tile as the TMA's swizzle lays
-// it down.
-template <class C, int BS>
-__device__ __forceinline__ uint32_t at(uint32_t base, int t, int b) {
-    const int slab = b / C::SLAB, within = b % C::SLAB, chunk = within >> 4;
-    const int phys = C::SLAB == 128 ? (chunk ^ (t & 7)) : (chunk ^ ((t >> 1) & 3));
-    return base + slab * (BS * C::SLAB) + t * C::SLAB + (phys << 4) + (within & 15);
-}
-
-template <int D, int BS, bool FP8, int NT, int NW, int SPW>
-__global__ void __launch_bounds__(NW * 32, (NT == 2 && BS == 16 && !FP8) ? 3 : 2)
-    attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const Args a) {
-    using C = Shape<D, BS, FP8, NT, NW, SPW>;
-    constexpr int PPI = C::PPI, MI = C::MI;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[C::NSTAGE];
-    __shared__ __align__(8) uint64_t stall_bar;  // never completed (wait-limit test hook)
-
-    const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t ring = (raw + 1023u) & ~1023u;
-    float *join = reinterpret_cast<float *>(smem_raw + (ring - raw));
-    const uint32_t rank = cluster_rank(), ranks = cluster_size();
-    const int h = blockIdx.y, s = blockIdx.z;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int r = lane >> 2, c = lane & 3;
-
-    const float k_scale = FP8 ? (a.k_scales ? __ldg(a.k_scales + h) : a.kv_scale) : 1.f;
-    const float v_scale = FP8 ? (a.v_scales ? __ldg(a.v_scales + h) : a.kv_scale) : 1.f;
-    const float score_scale = a.softmax_log2 * k_scale;
-
-    if (tid == 0) {
-#pragma unroll
-        for (int i = 0; i < C::NSTAGE; ++i) mbar_init(smem_addr(&bars[i]), 1);
-        mbar_init(smem_addr(&stall_bar), 1);
-        fence_barrier_init();
-        prefetch_tensormap(&tmK);
-        prefetch_tensormap(&tmV);
-    }
-
-    // query fragments (B operand of S^T = K Q^T), resident in registers
-    uint32_t qf[C::KSTEPS][NT][2];
-    {
-        const __nv_bfloat16 *qh = a.q + (static_cast<int64_t>(s) * a.num_q_heads + h * a.group) * D;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int g = nt * 8 + r;
-            const bool live = g < a.group;
-            const __nv_bfloat16 *qg = qh + g * D;
-#pragma unroll
-            for (int kk = 0; kk < C::KSTEPS; ++kk) {
-                if constexpr (!FP8) {
-                    qf[kk][nt][0] = live ? __ldg(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 2 * c)) : 0u;
-                    qf[kk][nt][1] = live ? __ldg(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 8 + 2 * c)) : 0u;
-                } else {
-                    // permuted order, as the K bytes below: this thread's dims
-                    // are c*16*CPT + 4*kk + {0,1,2,3}
-                    const uint2 w = live ? __ldg(reinterpret_cast<const uint2 *>(qg + c * 16 * C::CPT + 4 * kk))
-                                         : make_uint2(0u, 0u);
-                    const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.x));
-                    const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.y));
-                    qf[kk][nt][0] = pack2<true>(f0.x, f0.y);
-                    qf[kk][nt][1] = pack2<true>(f1.x, f1.y);
-                }
-            }
-        }
-    }
-    int n = a.context_lens[s];
-    if (n > a.max_blocks * BS) {
-        if (tid == 0 && rank == 0 && h == 0) set_device_error(a.err, PA_DEVERR_BAD_CONTEXT);
-        n = a.max_blocks * BS;
-    }
-    const int nb = n > 0 ? (n + BS - 1) / BS : 0;
-    __syncthreads();
-    // the list comes from the kernel before this one on the stream
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // ---- this warp's entries of the list ----------------------------------------
-    const int64_t list_row = static_cast<int64_t>(s) * a.num_kv_heads + h;
-    const int listed = min(max(a.counts[list_row], 0), a.top_k);
-    const int step = NW * static_cast<int>(ranks);
-    const int first = static_cast<int>(rank) * NW + warp;
-    const int32_t *list = a.selected + list_row * a.top_k + first;
-    const int32_t *table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
-    const int my_pages = listed > first ? (listed - first + step - 1) / step : 0;
-    const int my_steps = (my_pages + PPI - 1) / PPI;
-    const uint64_t policy = l2_evict_first_policy();
-    const int rows_total = a.num_blocks * a.num_kv_heads * BS;
-
-    // First tensor row of the warp's k-th page; rows_total (outside: the copy
-    // fills zeros) for an entry that is no page of the sequence or pool.
-    auto first_row = [&](int k) -> int {
-        if (k >= my_pages) return rows_total;
-        const int j = list[static_cast<int64_t>(k) * step];
-        if (j < 0 || j >= nb) {
-            set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
-            return rows_total;
-        }
-        const int b = __ldg(table + j);
-        if (b < 0 || b >= a.num_blocks) {
-            set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
-            return rows_total;
-        }
-        return (b * a.num_kv_heads + h) * BS;
-    };
-    int y_cur = first_row(lane), y_next = first_row(32 + lane), chunk = 0;
-    auto page_row = [&](int k) -> int {  // called by all lanes with k = 0, 1, 2, ...
-        if ((k >> 5) != chunk) {
-            y_cur = y_next;
-            chunk = k >> 5;
-            y_next = first_row((chunk + 1) * 32 + lane);
-        }
-        return __shfl_sync(0xffffffffu, y_cur, k & 31);
-    };
-    auto fetch = [&](int it) {
-        int ys[PPI];
-#pragma unroll
-        for (int p = 0; p < PPI; ++p) ys[p] = page_row(PPI * it + p);
-        const int live = min(PPI, my_pages - PPI * it);
-        if (lane >= live) return;
-        const int st = warp * SPW + it % SPW;
-        const uint32_t bar = smem_addr(&bars[st]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, live * 2 * C::PAGE);
-        const uint32_t kdst = ring + st * C::STAGE + lane * C::PAGE;
-        const uint32_t vdst = kdst + PPI * C::PAGE;
-        int y = ys[0];
-#pragma unroll
-        for (int p = 1; p < PPI; ++p)
-            if (lane == p) y = ys[p];
-#pragma unroll
-        for (int sl = 0; sl < C::NSLAB; ++sl) {
-            tma_load_2d(kdst + sl * (BS * C::SLAB), &tmK, sl * (C::SLAB / C::ELEM), y, bar, policy);
-            tma_load_2d(vdst + sl * (BS * C::SLAB), &tmV, sl * (C::SLAB / C::ELEM), y, bar, policy);
-        }
-    };
-    const int prolog = my_steps < SPW ? my_steps : SPW;
-    for (int it = 0; it < prolog; ++it) fetch(it);
-
-    float o[C::DT][NT][4];
-#pragma unroll
-    for (int dt = 0; dt < C::DT; ++dt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[dt][nt][e] = 0.f;
-    // probabilities are taken against m_ref, which moves only when a tile's
-    // maximum exceeds it by more than kLazy (base-2 units): they stay below
-    // 2^kLazy and the accumulator is rescaled rarely
-    constexpr float kLazy = 8.f;
-    float m_ref[NT][2], l_run[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            m_ref[nt][j] = -INFINITY;
-            l_run[nt][j] = 0.f;
-        }
-    // Token (within its 16-token tile) of MMA row r, and of row r + 8: the
-    // E4M3 V fragments pair tokens 4c, 4c+1 and 4c+2, 4c+3, and the scores
-    // take the same order.
-    const int tok_r = FP8 ? (r >> 1) * 4 + (r & 1) : r;
-    const int tok_dh = FP8 ? 2 : 8;
-
-    bool ok = true;
-    int it_fail = 0;
-    if (a.stall_first_wait && my_steps > 0)
-        ok = mbar_wait_bounded(smem_addr(&stall_bar), 0, a.wait_limit_ns);
-    for (int it = 0; ok && it < my_steps; ++it) {
-        const int st = warp * SPW + it % SPW;
-        // tokens of the step's pages (a list entry read again: it is cached)
-        int valid[PPI];
-        bool any = false;
-#pragma unroll
-        for (int p = 0; p < PPI; ++p) {
-            const int k = PPI * it + p;
-            int j = k < my_pages ? list[static_cast<int64_t>(k) * step] : -1;
-            valid[p] = j >= 0 && j < nb ? min(BS, n - j * BS) : 0;
-            any |= valid[p] > 0;
-        }
-        if (!mbar_wait_bounded(smem_addr(&bars[st]), (it / SPW) & 1, a.wait_limit_ns)) {
-            ok = false;
-            it_fail = it;
-            break;
-        }
-        const uint32_t kbase = ring + st * C::STAGE;
-        const uint32_t vbase = kbase + PPI * C::PAGE;
-        if (any) {
-            bool partial = false;
-#pragma unroll
-            for (int p = 0; p < PPI; ++p) partial |= valid[p] < BS;
-            if (partial) {
-                // rows behind the context hold anything: zero V so that a
-                // probability of 0 times them is 0
-                constexpr int CH = C::NSLAB * (C::SLAB / 16);
-#pragma unroll
-                for (int p = 0; p < PPI; ++p) {
-                    const uint32_t vb = vbase + p * C::PAGE;
-                    for (int i = lane; i < (BS - valid[p]) * CH; i += 32) {
-                        const int row = valid[p] + i / CH, rem = i % CH;
-                        sts128_zero(vb + (rem / (C::SLAB / 16)) * (BS * C::SLAB) + row * C::SLAB +
-                                    (rem % (C::SLAB / 16)) * 16);
-                    }
-                }
-                fence_proxy_async_smem();  // before the stage's next copy
-                __syncwarp();
-            }
-
-            float sc[MI][NT][4];
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[mi][nt][e] = 0.f;
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    const uint32_t kb = kbase + (mi / C::MT) * C::PAGE;
-                    const int t = (mi % C::MT) * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-                    for (int kk = 0; kk < C::KSTEPS; ++kk) {
-                        uint32_t a0, a1, a2, a3;
-                        ldsm_x4(at<C, BS>(kb, t, (kk * 16 + (lane >> 4) * 8) * 2), a0, a1, a2, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<false>(sc[mi][nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    const uint32_t kb = kbase + (mi / C::MT) * C::PAGE;
-                    const int t0 = (mi % C::MT) * 16 + tok_r, t1 = t0 + tok_dh;
-                    uint4 ra[C::CPT], rb[C::CPT];
-#pragma unroll
-                    for (int j = 0; j < C::CPT; ++j) {
-                        ra[j] = lds128(at<C, BS>(kb, t0, (c * C::CPT + j) * 16));
-                        rb[j] = lds128(at<C, BS>(kb, t1, (c * C::CPT + j) * 16));
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < C::KSTEPS; ++kk) {
-                        const uint4 &A = ra[kk / 4];
-                        const uint4 &B = rb[kk / 4];
-                        const uint32_t wa = (kk % 4 == 0) ? A.x : (kk % 4 == 1) ? A.y : (kk % 4 == 2) ? A.z : A.w;
-                        const uint32_t wb = (kk % 4 == 0) ? B.x : (kk % 4 == 1) ? B.y : (kk % 4 == 2) ? B.z : B.w;
-                        uint32_t a0, a1, a2, a3;
-                        e4m3x4_to_f16x2x2(wa, a0, a2);
-                        e4m3x4_to_f16x2x2(wb, a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<true>(sc[mi][nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
-                    }
-                }
-            }
-
-            // online softmax over the step's tokens, per query head
-            float mx[NT][2];
-            bool grow = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int mi = 0; mi < MI; ++mi) {
-                        const int lim = valid[mi / C::MT] - (mi % C::MT) * 16;
-#pragma unroll
-                        for (int hi = 0; hi < 2; ++hi) {
-                            float x = sc[mi][nt][hi * 2 + j] * score_scale;
-                            x = tok_r + hi * tok_dh < lim ? x : -INFINITY;
-                            sc[mi][nt][hi * 2 + j] = x;
-                            m = fmaxf(m, x);
-                        }
-                    }
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    mx[nt][j] = m;
-                    grow |= m > m_ref[nt][j] + kLazy;
-                }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float m_new = fmaxf(m_ref[nt][j], mx[nt][j]);
-                        const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_ref[nt][j] - m_new);
-                        m_ref[nt][j] = m_new;
-                        l_run[nt][j] *= alpha;
-#pragma unroll
-                        for (int dt = 0; dt < C::DT; ++dt) {
-                            o[dt][nt][j] *= alpha;
-                            o[dt][nt][j + 2] *= alpha;
-                        }
-                    }
-            }
-            uint32_t pb[MI][NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    // no finite score so far: any reference will do for the zeros
-                    const float ref = m_ref[nt][j] == -INFINITY ? 0.f : m_ref[nt][j];
-                    float sum = 0.f;
-#pragma unroll
-                    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                        for (int hi = 0; hi < 2; ++hi) {
-                            const float pr = fast_exp2(sc[mi][nt][hi * 2 + j] - ref);
-                            sc[mi][nt][hi * 2 + j] = pr;
-                            sum += pr;
-                        }
-                    l_run[nt][j] += sum;
-                }
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    pb[mi][nt][0] = movmatrix_trans(pack2<FP8>(sc[mi][nt][0], sc[mi][nt][1]));
-                    pb[mi][nt][1] = movmatrix_trans(pack2<FP8>(sc[mi][nt][2], sc[mi][nt][3]));
-                }
-            }
-
-            // O^T += V^T P^T
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    const uint32_t vb = vbase + (mi / C::MT) * C::PAGE;
-                    const int t = (mi % C::MT) * 16 + (lane & 7) + (lane >> 4) * 8;
-#pragma unroll
-                    for (int dt = 0; dt < C::DT; ++dt) {
-                        uint32_t a0, a1, a2, a3;
-                        ldsm_x4_trans(at<C, BS>(vb, t, (dt * 16 + ((lane >> 3) & 1) * 8) * 2), a0, a1, a2, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<false>(o[dt][nt], a0, a1, a2, a3, pb[mi][nt][0], pb[mi][nt][1]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    const uint32_t vb = vbase + (mi / C::MT) * C::PAGE;
-                    const int t = (mi % C::MT) * 16 + (lane & 15);
-#pragma unroll
-                    for (int cp = 0; cp < D / 32; ++cp) {
-                        uint32_t w0, w1, w2, w3, a0, a1, a2, a3;
-                        ldsm_x2_trans_b8(at<C, BS>(vb, t, (2 * cp + (lane >> 4)) * 16), w0, w1, w2, w3);
-                        e4m3x4_to_f16x2x2(w0, a0, a2);
-                        e4m3x4_to_f16x2x2(w1, a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<true>(o[2 * cp][nt], a0, a1, a2, a3, pb[mi][nt][0], pb[mi][nt][1]);
-                        e4m3x4_to_f16x2x2(w2, a0, a2);
-                        e4m3x4_to_f16x2x2(w3, a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<true>(o[2 * cp + 1][nt], a0, a1, a2, a3, pb[mi][nt][0], pb[mi][nt][1]);
-                    }
-                }
-            }
-        }
-        __syncwarp();
-        if (it + SPW < my_steps) fetch(it + SPW);
-    }
-    if (!ok) {
-        // a copy never arrived: flag it, wait (bounded) for the copies still in
-        // flight into this warp's stages, and go on with nothing
-        if (lane == 0) set_device_error(a.err, PA_DEVERR_TIMEOUT);
-        const int issued = min(my_steps, it_fail + SPW);
-        for (int it = it_fail; it < issued; ++it)
-            mbar_wait_bounded(smem_addr(&bars[warp * SPW + it % SPW]), (it / SPW) & 1, kDrainNs);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m_ref[nt][0] = m_ref[nt][1] = -INFINITY;
-            l_run[nt][0] = l_run[nt][1] = 0.f;
-        }
-    }
-
-    // ---- join the warps ---------------------------------------------------------
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float l = l_run[nt][j];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            l_run[nt][j] = l;
-        }
-    __syncthreads();  // every warp is done with the page ring
-    float *osm = join;                        // [NW][NP][OSTR]
-    float *msm = osm + NW * C::NP * C::OSTR;  // [NW][NP] reference
-    float *lsm = msm + NW * C::NP;            // [NW][NP] sum
-    float *csm = lsm + NW * C::NP;            // [NP][D] the CTA's accumulator
-    float *mc = csm + C::NP * D;              // [NP] its reference
-    float *lc = mc + C::NP;                   // [NP] its sum
-#pragma unroll
-    for (int dt = 0; dt < C::DT; ++dt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int g = nt * 8 + 2 * c + (e & 1);
-                const int d = dt * 16 + r + (e >> 1) * 8;
-                osm[(warp * C::NP + g) * C::OSTR + d] = o[dt][nt][e];
-            }
-    if (r == 0) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int g = nt * 8 + 2 * c + j;
-                msm[warp * C::NP + g] = m_ref[nt][j];
-                lsm[warp * C::NP + g] = l_run[nt][j];
-            }
-    }
-    __syncthreads();
-    // A part that saw no token has reference -infinity and sum 0, and is left
-    // out; one with a NaN keeps it (its weight is not skipped).
-    auto weight = [](float m, float top) { return m == -INFINITY ? 0.f : fast_exp2(m - top); };
-    for (int i = tid; i < a.group * D; i += NW * 32) {
-        const int g = i / D, d = i % D;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) top = fmaxf(top, msm[w * C::NP + g]);
-        float acc = 0.f, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float f = weight(msm[w * C::NP + g], top);
-            if (msm[w * C::NP + g] != -INFINITY || lsm[w * C::NP + g] != 0.f) {
-                acc += f * osm[(w * C::NP + g) * C::OSTR + d];
-                sum += f * lsm[w * C::NP + g];
-            }
-        }
-        csm[i] = acc;
-        if (d == 0) {
-            mc[g] = top;
-            lc[g] = sum;
-        }
-    }
-    if (ranks > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
-    }
-
-    // ---- join the CTAs: each writes its share of the output -----------------------
-    const int64_t out0 = (static_cast<int64_t>(s) * a.num_q_heads + h * a.group) * D;
-    const int pairs = a.group * D / 2;
-    for (int i = static_cast<int>(rank) * NW * 32 + tid; i < pairs; i += static_cast<int>(ranks) * NW * 32) {
-        const int g = 2 * i / D;
-        float top = -INFINITY;
-        for (uint32_t k = 0; k < ranks; ++k) top = fmaxf(top, ld_cluster(smem_addr(mc + g), k));
-        float v0 = 0.f, v1 = 0.f, sum = 0.f;
-        for (uint32_t k = 0; k < ranks; ++k) {
-            const float m = ld_cluster(smem_addr(mc + g), k), l = ld_cluster(smem_addr(lc + g), k);
-            if (m == -INFINITY && l == 0.f) continue;
-            const float f = weight(m, top);
-            sum += f * l;
-            v0 += f * ld_cluster(smem_addr(csm + 2 * i), k);
-            v1 += f * ld_cluster(smem_addr(csm + 2 * i + 1), k);
-        }
-        const float inv = sum != 0.f ? v_scale / sum : 0.f;
-        *reinterpret_cast<__nv_bfloat162 *>(a.out + out0 + 2 * i) = __floats2bfloat162_rn(v0 * inv, v1 * inv);
-    }
-    if (ranks > 1) {  // nobody leaves while another may still read its part
-        cluster_arrive();
-        cluster_wait();
-    }
-}
-
-// ---------------------------------------------------------------------------
-// host side
-// ---------------------------------------------------------------------------
-
-constexpr int kWarps = 4;
-
-// Page ring per CTA: 64 KB (three CTAs per SM), and 96 KB where a group above
-// 8 needs so many registers that only two fit.
-template <int D, int BS, bool FP8, int NT>
-constexpr int stages_per_warp() {
-    constexpr int ppi = (FP8 && BS == 16) ? 2 : 1;
-    constexpr int stage = 2 * ppi * BS * D * (FP8 ? 1 : 2);
-    constexpr bool wide = D == 128 && NT == 2 && !(BS == 16 && !FP8);
-    constexpr int spw = (wide ? 96 : 64) * 1024 / (kWarps * stage);
-    return spw < 1 ? 1 : spw;
-}
-
-template <int D, int BS, bool FP8, int NT>
-static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int num_rows,
-                               int splits, bool dependent, cudaStream_t stream) {
-    constexpr int SPW = stages_per_warp<D, BS, FP8, NT>();
-    using C = Shape<D, BS, FP8, NT, kWarps, SPW>;
-    auto kern = attend_kernel<D, BS, FP8, NT, kWarps, SPW>;
-    static std::atomic<uint64_t> raised{0};
-    pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM, raised);
-    if (st != PA_OK) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(splits, a.num_kv_heads, num_rows);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 2 : 1;
-    return cuda_check(cudaLaunchKernelEx(&cfg, kern, tk, tv, a), "sparse decode launch");
-}
-
-template <int D, int BS>
-static pa_status launch_shape(bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
-                              int num_rows, int splits, bool dependent, cudaStream_t stream) {
-    if (fp8)
-        return a.group <= 8 ? launch_attend<D, BS, true, 1>(tk, tv, a, num_rows, splits, dependent, stream)
-                            : launch_attend<D, BS, true, 2>(tk, tv, a, num_rows, splits, dependent, stream);
-    return a.group <= 8 ? launch_attend<D, BS, false, 1>(tk, tv, a, num_rows, splits, dependent, stream)
-                        : launch_attend<D, BS, false, 2>(tk, tv, a, num_rows, splits, dependent, stream);
-}
 
 struct Call {
     const void *q, *k_cache, *v_cache;
@@ -621,7 +42,19 @@ static pa_status check_pointers(const Call &c) {
     return PA_OK;
 }
 
-static pa_status run_attend(const Call &c, bool dependent, cudaStream_t stream) {
+// CTAs to a (row, KV head)'s list: the most whose clusters are all resident at
+// once (an eighth of the CTAs' places is kept back: clusters of three, six or
+// eight leave some of a GPC's places empty) and whose warps have a page each.
+static int splits_for(int64_t rows, int top_k, int resident) {
+    int splits = 1;
+    for (int s : {2, 3, 4, 6, 8})
+        if (rows * s <= resident * kSms * 7 / 8 && top_k >= kWarps * s) splits = s;
+    return splits;
+}
+
+// `select`: choose the pages in the same kernel; otherwise the list is there,
+// or comes from the kernel before this one (`dependent`).
+static pa_status run_attend(const Call &c, const SelectArgs *select, bool dependent, cudaStream_t stream) {
     const bool fp8 = c.kv_dtype == PA_KV_FP8_E4M3;
     const int64_t pool_rows = static_cast<int64_t>(c.num_blocks) * c.num_kv_heads * c.block_size;
     CUtensorMap tk, tv;
@@ -651,17 +84,18 @@ static pa_status run_attend(const Call &c, bool dependent, cudaStream_t stream) 
     a.err = err;
     a.wait_limit_ns = wait_limit_ns();
     a.stall_first_wait = stall_first_wait();
-    int splits = c.splits;
-    if (splits == 0) {
-        const int64_t rows = static_cast<int64_t>(c.num_rows) * c.num_kv_heads;
-        splits = 1;
-        while (splits < 8 && rows * splits < 2 * 152 && c.top_k > 2 * kWarps * splits) splits *= 2;
+    const int64_t rows = static_cast<int64_t>(c.num_rows) * c.num_kv_heads;
+    // CTAs to an SM (see the ring's size)
+    const bool wide = c.head_dim == 128 && a.group > 8 && !(c.block_size == 16 && !fp8);
+    const int resident = wide ? 2 : 3;
+    if (select) {
+        a.select = *select;
+        int splits = splits_for(rows, c.top_k, resident);
+        while (c.max_blocks > kFusedKeys * splits) ++splits;  // at most 8: checked by the caller
+        return launch_chosen(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, stream);
     }
-    if (c.head_dim == 128)
-        return c.block_size == 16 ? launch_shape<128, 16>(fp8, tk, tv, a, c.num_rows, splits, dependent, stream)
-                                  : launch_shape<128, 32>(fp8, tk, tv, a, c.num_rows, splits, dependent, stream);
-    return c.block_size == 16 ? launch_shape<64, 16>(fp8, tk, tv, a, c.num_rows, splits, dependent, stream)
-                              : launch_shape<64, 32>(fp8, tk, tv, a, c.num_rows, splits, dependent, stream);
+    const int splits = c.splits ? c.splits : splits_for(rows, c.top_k, resident);
+    return launch_any<false>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, dependent, stream);
 }
 
 }  // namespace sparse
@@ -690,7 +124,7 @@ pa_status pa_sparse_decode(const void *q, const void *k_cache, const void *v_cac
     if (st != PA_OK) return st;
     if (num_rows == 0) return PA_OK;
     st = check_pointers(c);
-    return st == PA_OK ? run_attend(c, false, stream) : st;
+    return st == PA_OK ? run_attend(c, nullptr, false, stream) : st;
 }
 
 pa_status pa_sparse_attend(const void *q, const void *k_cache, const void *v_cache,
@@ -715,10 +149,12 @@ pa_status pa_sparse_attend(const void *q, const void *k_cache, const void *v_cac
     if (st != PA_OK) return st;
     if (!summary || !exponents) return fail(PA_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(summary)) return fail(PA_ERR_INVALID_ARG, "summary must be 16-byte aligned");
-    st = run_select(q, summary, exponents, block_tables, max_blocks_per_seq, context_lens, num_rows,
-                    num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, top_k, sink_blocks,
-                    recent_blocks, selected, counts, stream);
-    return st == PA_OK ? run_attend(c, true, stream) : st;
+    const SelectArgs sel = select_args(q, summary, exponents, block_tables, max_blocks_per_seq, context_lens,
+                                       num_q_heads, num_kv_heads, num_blocks, block_size, top_k, sink_blocks,
+                                       recent_blocks, selected, counts);
+    if (max_blocks_per_seq <= 8 * kFusedKeys) return run_attend(c, &sel, false, stream);
+    st = run_select(sel, num_rows, head_dim, stream);
+    return st == PA_OK ? run_attend(c, nullptr, true, stream) : st;
 }
 
 }  // extern "C"

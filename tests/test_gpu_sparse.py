@@ -227,6 +227,65 @@ def test_choice_among_many_ties(api, cuda_device, D, Hq, S, pages):
     assert api.device_errors() == 0
 
 
+@pytest.mark.parametrize("D,G,S,pages,top_k,sink,recent", [
+    # candidates up to and just past the numbers that are ranked directly (256 alone, 500 in a cluster)
+    (64, 2, 304, 259, 20, 1, 2), (64, 2, 304, 260, 20, 1, 2), (128, 1, 2, 503, 90, 1, 2), (128, 1, 2, 504, 90, 1, 2),
+    (128, 9, 3, 257, 40, 0, 1), (64, 16, 1, 513, 200, 0, 1),
+    # one candidate more than is wanted, and lists longer than the candidates
+    (128, 4, 1, 65, 64, 1, 2), (64, 1, 5, 130, 129, 60, 68), (128, 2, 2, 900, 700, 300, 350), (64, 3, 320, 900, 700, 300, 350),
+    # a few pages to a warp of the last CTA, and none
+    (128, 4, 1, 1029, 100, 1, 2), (64, 4, 3, 2081, 33, 1, 1), (64, 4, 60, 700, 33, 1, 1),
+])
+def test_choice_at_its_borders(api, cuda_device, D, G, S, pages, top_k, sink, recent):
+    """Alone and followed by the attention, bit for bit; scores of any value, then few values."""
+    g = torch.Generator().manual_seed(pages + top_k)
+    NB, Hkv, B = 400, 2, 16
+    kc, vc = (torch.randn(NB, Hkv, B, D, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(S, G * Hkv, D, generator=g).to(torch.bfloat16)
+    tables = torch.randint(0, NB, (S, pages), generator=g).to(torch.int32)
+    lens = torch.full((S,), pages * B, dtype=torch.int32) - torch.randint(0, B, (S,), generator=g).to(torch.int32)
+    dev = [t.to(cuda_device) for t in (q, kc, vc, tables, lens)]
+    rows = sorted({0, S // 2, S - 1})
+    for few_values in (False, True):
+        s = torch.randint(-127, 128, (NB, Hkv, 2, D), generator=g).to(torch.int8).sort(dim=2, descending=True).values
+        e = torch.randint(-9, -6, (NB, Hkv), generator=g).to(torch.int8)
+        if few_values:
+            s[:, :, :, 1:] = 0
+            s[:, :, :, 0] = s[:, :, :, 0].sign()
+            e[:] = -7
+        se, ee = s.to(cuda_device), e.to(cuda_device)
+        sel, cnt = api.sparse_select(dev[0], se, ee, dev[3], dev[4], B, top_k, sink, recent)
+        sel2, cnt2 = torch.zeros_like(sel), torch.zeros_like(cnt)
+        out = api.sparse_attend(*dev[:3], se, ee, *dev[3:], top_k, sink, recent, selected=sel2, counts=cnt2)
+        assert torch.equal(sel, sel2) and torch.equal(cnt, cnt2)
+        want_sel, want_cnt = R.select(f64(q)[rows], s.numpy(), e.numpy(), tables.numpy()[rows], lens.numpy()[rows], B, top_k, sink, recent)
+        assert np.array_equal(sel.cpu().numpy()[rows], want_sel) and np.array_equal(cnt.cpu().numpy()[rows], want_cnt)
+        alone = api.sparse_decode(*dev[:3], *dev[3:], sel, cnt)
+        assert torch.equal(out, alone)
+    assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_largest_whole_sums(api, cuda_device, D):
+    """Queries and bounds at +-127 throughout: sums of up to 127 * 127 * D that differ by single units."""
+    g = torch.Generator().manual_seed(D)
+    NB, S = 90, 4
+    s = torch.full((NB, 1, 2, D), 127, dtype=torch.int8)
+    s[:, :, 1] = -127
+    s[torch.arange(NB), 0, 0, torch.randint(0, D, (NB,), generator=g)] -= torch.randint(0, 3, (NB,), generator=g).to(torch.int8)
+    s[torch.arange(NB), 0, 1, torch.randint(0, D, (NB,), generator=g)] += torch.randint(0, 3, (NB,), generator=g).to(torch.int8)
+    e = torch.zeros(NB, 1, dtype=torch.int8)
+    q = torch.full((S, 9, D), 127.0)
+    q[1] = -127
+    q[2] = torch.randint(0, 2, (9, D), generator=g) * 254.0 - 127
+    q[3, :, ::2] = -127
+    q = (q + torch.randint(-1, 1, q.shape, generator=g) * q.sign()).to(torch.bfloat16)
+    tables, lens = torch.arange(NB).to(torch.int32)[None].repeat(S, 1), torch.full((S,), NB * 16, dtype=torch.int32)
+    sel, _ = api.sparse_select(*(t.to(cuda_device) for t in (q, s, e, tables, lens)), 16, 30, 0, 1)
+    want, _ = R.select(f64(q), s.numpy(), e.numpy(), tables.numpy(), lens.numpy(), 16, 30, 0, 1)
+    assert np.array_equal(sel.cpu().numpy(), want)
+
+
 def test_choice_with_extreme_bounds_and_queries(api, cuda_device):
     """Exponents at both ends, the largest whole numbers, zero and non-finite queries."""
     g = torch.Generator().manual_seed(12)
@@ -466,6 +525,6 @@ def test_decode_loop(api, cuda_device, fp8):
 def test_decode_loop_captured(api, cuda_device):
     def captured(step, io):
         graph = api.StepGraph([step], [io])
-        assert graph.launches() == 5
+        assert graph.launches() == 4
         return graph.replay
     _decode_loop(api, cuda_device, captured, 20)

@@ -86,7 +86,7 @@ def _select(lib, fn="select", **kw):
 @pytest.mark.parametrize("fn", ["select", "decode", "attend"])
 @pytest.mark.parametrize("kw,status", [
     (dict(S=-1), 1), (dict(Hkv=3), 1), (dict(Hq=64, Hkv=2), 2), (dict(D=96), 2), (dict(B=8), 2), (dict(NB=0), 1), (dict(mb=0), 1),
-    (dict(S=70000), 2), (dict(NB=1 << 27), 2), (dict(k=0), 1), (dict(mb=1 << 28), 1), (dict(mb=(1 << 18) + 1), 2),
+    (dict(S=70000), 2), (dict(NB=1 << 27), 2), (dict(k=0), 1), (dict(mb=1 << 28), 1), (dict(mb=(1 << 17) + 1), 2),
     (dict(q=None), 1), (dict(bt=None), 1), (dict(cl=None), 1), (dict(sel=None), 1), (dict(cnt=None), 1), (dict(q=ODD), 1),
 ])
 def test_sparse_entry_points_reject_on_host(lib, fn, kw, status):
@@ -121,82 +121,115 @@ def test_no_rows_is_a_no_op(lib, fn):
     assert _select(lib, fn, S=0, q=None, sel=None, out=None) == 0
 
 
-# ---- the Python binding --------------------------------------------------------
+# ---- the Python binding: host tensors meet every check but the device's, which comes last ----
 
-@pytest.fixture
-def on_gpu(monkeypatch, lib):
-    """Host tensors that say they are on cuda:0, to reach the checks behind the device's."""
-    monkeypatch.setattr(torch.Tensor, "device", property(lambda self: torch.device("cuda", 0)))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+bf = torch.bfloat16
 
 
-def _args(T=3, Hq=4, Hkv=2, D=64, NB=4, B=16):
-    bf = torch.bfloat16
-    cache = torch.zeros(NB, Hkv, B, D, dtype=bf)
-    return dict(q=torch.zeros(T, Hq, D, dtype=bf), k=torch.zeros(T, Hkv, D, dtype=bf), v=torch.zeros(T, Hkv, D, dtype=bf),
-                positions=torch.zeros(T, dtype=torch.int32), inv_freq=torch.ones(D // 2, dtype=torch.float64),
-                slot_mapping=torch.zeros(T, dtype=torch.int32), k_cache=cache, v_cache=cache.clone(),
-                out=torch.zeros(T, Hq, D, dtype=bf))
+def z(*shape, dtype=torch.int32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _append_args():
+    return dict(q=z(3, 4, 64, dtype=bf), k=z(3, 2, 64, dtype=bf), v=z(3, 2, 64, dtype=bf), positions=z(3),
+                inv_freq=torch.ones(32, dtype=torch.float64), slot_mapping=z(3), k_cache=z(4, 2, 16, 64, dtype=bf),
+                v_cache=z(4, 2, 16, 64, dtype=bf), out=z(3, 4, 64, dtype=bf))
 
 
 @pytest.mark.parametrize("change,err,match", [
-    (dict(q=torch.zeros(3, 4, 128, dtype=torch.bfloat16)), ValueError, "inconsistent q and k"),
-    (dict(q=torch.zeros(3, 4, 64)), TypeError, "bfloat16"),
-    (dict(k=torch.zeros(3, 64, 2, dtype=torch.bfloat16).transpose(1, 2)), ValueError, "dense"),
-    (dict(v=torch.zeros(4, 2, 64, dtype=torch.bfloat16)), ValueError, "inconsistent K/V"),
-    (dict(positions=torch.zeros(4, dtype=torch.int32)), ValueError, "positions"),
-    (dict(positions=torch.zeros(3, dtype=torch.int64)), TypeError, "positions"),
+    (dict(q=z(3, 4, 128, dtype=bf)), ValueError, "inconsistent q and k"),
+    (dict(q=z(2, 4, 64, dtype=bf)), ValueError, "inconsistent q and k"),
+    (dict(q=z(3, 4, 64, dtype=torch.float32)), TypeError, "q has dtype"),
+    (dict(q=[1.0]), TypeError, "q must be a torch.Tensor"),
+    (dict(k=z(3, 64, 2, dtype=bf).transpose(1, 2)), ValueError, "dense"),
+    (dict(k=z(3, 128, dtype=bf)), ValueError, "3 dimensions"),
+    (dict(v=z(4, 2, 64, dtype=bf)), ValueError, "inconsistent K/V"),
+    (dict(k=None), TypeError, "k must be a torch.Tensor"),
+    (dict(positions=z(4)), ValueError, "positions"),
+    (dict(positions=z(2, 3, 1)), ValueError, "positions"),
+    (dict(positions=z(3, dtype=torch.int64)), TypeError, "positions"),
+    (dict(positions=z(3, 2).t()), ValueError, "contiguous"),
     (dict(inv_freq=torch.ones(32)), TypeError, "inv_freq"),
-    (dict(pair_axis=torch.zeros(31, dtype=torch.int32)), ValueError, "pair_axis"),
-    (dict(slot_mapping=torch.zeros(2, dtype=torch.int32)), ValueError, "slot_mapping"),
+    (dict(inv_freq=torch.ones(2, 16, dtype=torch.float64)), ValueError, "inv_freq"),
+    (dict(pair_axis=z(31)), ValueError, "pair_axis"),
+    (dict(slot_mapping=z(2)), ValueError, "slot_mapping"),
     (dict(k_scales=torch.ones(2)), ValueError, "both"),
-    (dict(out=torch.zeros(3, 4, 32, dtype=torch.bfloat16)), ValueError, "out"),
-    (dict(v_cache=torch.zeros(4, 2, 16, 32, dtype=torch.bfloat16)), ValueError, "v_cache"),
+    (dict(k_scales=torch.ones(3), v_scales=torch.ones(3)), ValueError, "k_scales"),
+    (dict(out=z(3, 4, 32, dtype=bf)), ValueError, "out"),
+    (dict(out=z(3, 4, 64, dtype=torch.float16)), TypeError, "out"),
+    (dict(v_cache=z(4, 2, 16, 32, dtype=bf)), ValueError, "v_cache"),
+    (dict(v_cache=z(4, 2, 16, 64, dtype=torch.uint8)), ValueError, "v_cache"),
+    (dict(k_cache=z(4, 2, 16, 64, dtype=torch.float32)), TypeError, "k_cache"),
+    (dict(k_cache=z(4, 3, 16, 64, dtype=bf), v_cache=z(4, 3, 16, 64, dtype=bf)), ValueError, "inconsistent K/V and cache"),
+    (dict(magnitude="much"), TypeError, None),
+    ({}, ValueError, "CUDA tensor"),
 ])
-def test_rope_append_binding_refuses(on_gpu, change, err, match):
+def test_rope_append_binding_refuses(lib, change, err, match):
     with pytest.raises(err, match=match):
-        api.rope_append(**{**_args(), **change})
+        api.rope_append(**{**_append_args(), **change})
 
 
-def test_rope_append_binding_refuses_a_library_error(on_gpu):
-    a = _args()
-    a["inv_freq"] = torch.ones(12, dtype=torch.float64)  # 24 elements: not a multiple of 16
-    with pytest.raises(api.PagedAttentionError, match="multiple of 16"):
-        api.rope_append(**a, stream=type("S", (), {"cuda_stream": 0}))
+def _summary_args():
+    return dict(k_cache=z(4, 2, 16, 64, dtype=bf), slot_mapping=z(3), summary=z(4, 2, 2, 64, dtype=torch.int8),
+                exponents=z(4, 2, dtype=torch.int8))
 
 
-def test_tensors_of_another_device_are_refused(on_gpu, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    with pytest.raises(ValueError, match="current device"):
-        api.rope_append(**_args())
-    with pytest.raises(ValueError, match="current device"):
-        api.block_summary(_args()["k_cache"], torch.zeros(3, dtype=torch.int32), torch.zeros(4, 2, 2, 64, dtype=torch.int8),
-                          torch.zeros(4, 2, dtype=torch.int8))
-
-
-def test_host_tensors_are_refused(lib):
-    with pytest.raises(ValueError, match="CUDA tensor"):
-        api.rope_append(**_args())
-    a = _args()
-    with pytest.raises(ValueError, match="CUDA tensor"):
-        api.block_summary(a["k_cache"], a["slot_mapping"], *api.alloc_block_summary(a["k_cache"]))
-
-
-@pytest.mark.parametrize("change,match", [
-    (dict(summary=torch.zeros(4, 2, 2, 32, dtype=torch.int8)), "summary"),
-    (dict(exponents=torch.zeros(4, 3, dtype=torch.int8)), "exponents"),
-    (dict(context_lens=torch.zeros(2, dtype=torch.int32)), "context_lens"),
-    (dict(block_tables=torch.zeros(2, 8, dtype=torch.int32)), "block_tables"),
-    (dict(selected=torch.zeros(3, 2, 5, dtype=torch.int32)), "selected"),
-    (dict(counts=torch.zeros(3, 1, dtype=torch.int32)), "counts"),
-    (dict(v_scales=torch.ones(2)), "both"),
-    (dict(out=torch.zeros(3, 2, 64, dtype=torch.bfloat16)), "out"),
+@pytest.mark.parametrize("change,err,match", [
+    (dict(summary=z(4, 2, 64, dtype=torch.int8)), ValueError, "summary"),
+    (dict(summary=z(4, 2, 2, 64, dtype=torch.uint8)), TypeError, "summary"),
+    (dict(exponents=z(4, 3, dtype=torch.int8)), ValueError, "exponents"),
+    (dict(slot_mapping=z(3, 1)), ValueError, "slot_mapping"),
+    (dict(k_cache=z(4, 2, 64, dtype=bf)), ValueError, "k_cache"),
+    ({}, ValueError, "CUDA tensor"),
 ])
-def test_sparse_attend_binding_refuses(on_gpu, change, match):
-    a = _args()
-    args = dict(q=a["q"], k_cache=a["k_cache"], v_cache=a["v_cache"], summary=torch.zeros(4, 2, 2, 64, dtype=torch.int8),
-                exponents=torch.zeros(4, 2, dtype=torch.int8), block_tables=torch.zeros(3, 8, dtype=torch.int32),
-                context_lens=torch.ones(3, dtype=torch.int32), top_k=4, selected=torch.zeros(3, 2, 4, dtype=torch.int32),
-                counts=torch.zeros(3, 2, dtype=torch.int32))
-    with pytest.raises(ValueError, match=match):
-        api.sparse_attend(**{**args, **change})
+def test_block_summary_binding_refuses(lib, change, err, match):
+    with pytest.raises(err, match=match):
+        api.block_summary(**{**_summary_args(), **change})
+
+
+def test_alloc_block_summary():
+    s, e = api.alloc_block_summary(z(4, 2, 16, 64, dtype=bf))
+    assert s.shape == (4, 2, 2, 64) and e.shape == (4, 2) and s.dtype == e.dtype == torch.int8
+
+
+def _sparse_args(fn):
+    a = dict(q=z(3, 4, 64, dtype=bf), block_tables=z(3, 8), context_lens=z(3), selected=z(3, 2, 4), counts=z(3, 2))
+    if fn != "select":
+        a.update(k_cache=z(4, 2, 16, 64, dtype=bf), v_cache=z(4, 2, 16, 64, dtype=bf), out=z(3, 4, 64, dtype=bf))
+    if fn != "decode":
+        a.update(summary=z(4, 2, 2, 64, dtype=torch.int8), exponents=z(4, 2, dtype=torch.int8), top_k=4)
+    if fn == "select":
+        a["block_size"] = 16
+    return a
+
+
+@pytest.mark.parametrize("fns,change,err,match", [
+    ("select decode attend", dict(q=z(3, 4, 64, dtype=torch.float16)), TypeError, "q has dtype"),
+    ("select decode attend", dict(q=z(3, 256, dtype=bf)), (ValueError, IndexError), None),
+    ("select decode attend", dict(block_tables=z(2, 8)), ValueError, "block_tables"),
+    ("select decode attend", dict(block_tables=z(3, 8, dtype=torch.int64)), TypeError, "block_tables"),
+    ("select decode attend", dict(context_lens=z(2)), ValueError, "context_lens"),
+    ("select decode attend", dict(counts=z(3, 1)), ValueError, "counts"),
+    ("select decode attend", dict(selected=z(3, 3, 4)), ValueError, "selected"),
+    ("select attend", dict(selected=z(3, 2, 5)), ValueError, "selected"),
+    ("select attend", dict(summary=z(4, 2, 2, 32, dtype=torch.int8)), ValueError, "summary"),
+    ("select attend", dict(exponents=z(4, 2)), TypeError, "exponents"),
+    ("select attend", dict(top_k=2 ** 40), ValueError, "top_k is out of range"),
+    ("select attend", dict(top_k=4.5), TypeError, None),
+    ("decode attend", dict(v_scales=torch.ones(2)), ValueError, "both"),
+    ("decode attend", dict(out=z(3, 2, 64, dtype=bf)), ValueError, "out"),
+    ("decode attend", dict(k_cache=z(4, 2, 16, 128, dtype=bf), v_cache=z(4, 2, 16, 128, dtype=bf)), ValueError, "inconsistent"),
+    ("select decode attend", {}, ValueError, "CUDA tensor"),
+])
+def test_sparse_binding_refuses(lib, fns, change, err, match):
+    for fn in fns.split():
+        with pytest.raises(err, match=match):
+            getattr(api, "sparse_" + fn)(**{**_sparse_args(fn), **change})
+
+
+def test_binding_fails_loudly_when_it_is_not_built(monkeypatch, tmp_path):
+    from paged_kv_cache_193_gb300 import _lib
+    monkeypatch.setattr(_lib, "_binding", None)
+    monkeypatch.setattr(_lib, "BINDING_PATH", str(tmp_path / "missing.so"))
+    with pytest.raises(ImportError, match="build"):
+        _lib.binding()
