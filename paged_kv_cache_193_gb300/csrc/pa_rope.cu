@@ -15,6 +15,8 @@
 // all that is lost before sine and cosine are taken in fp32.
 //
 // Bound: memory.  Every q, k, v element is read once and written once.
+#include <algorithm>
+
 #include "pa_device.cuh"
 
 namespace pa {
@@ -57,6 +59,22 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                       pack2<false>(x[6], x[7]));
 }
 
+// f / 2 pi modulo one turn, as a 64-bit fraction of a turn, from the bits of f
+// (the fp64 unit is some sixty times slower than the integer one here): the
+// significand times 2 / pi, of which the upper 64 bits are kept, shifted by the
+// exponent.  Off by less than 2^-64 turns plus 2^-61 of f; 0 for what is not
+// finite and from 2^65 on.
+__device__ __forceinline__ uint64_t turn_fraction(double f) {
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+    const int exponent = static_cast<int>(bits >> 52 & 0x7ff) - 1023;  // f = 1.m * 2^exponent
+    const uint64_t significand = (bits | 1ull << 52) << 11;            // 1.m * 2^63
+    // 2 / pi * 2^64, rounded; the product is 1.m * 2 / pi * 2^63
+    const uint64_t part = __umul64hi(significand, 0xa2f9836e4e44152aull);
+    const int shift = exponent - 1;  // to f / 2 pi * 2^64
+    const uint64_t turn = shift <= -64 || shift >= 64 ? 0 : shift >= 0 ? part << shift : part >> -shift;
+    return bits >> 63 ? 0ull - turn : turn;
+}
+
 // Eight fp32 values as E4M3 codes of x / scale: one rounding from fp32 (the
 // rotated row is not rounded to bf16 on the way).
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
@@ -81,7 +99,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
 // elements 16j .. 16j+15; either way pairs 8j .. 8j+7, and two 16-byte loads.
 // Its j is the same for every row it takes.
 template <int D, bool FP8, bool ADJACENT>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(const Args a) {
     constexpr int VPR = D / 16;  // threads to a row
     __shared__ __align__(16) float cs[kMaxTile][D / 2], sn[kMaxTile][D / 2];
     __shared__ int32_t slot_s[kMaxTile];
@@ -96,9 +114,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Args a) {
             axis = 0;
         }
         const int pos = a.positions[static_cast<int64_t>(axis) * a.num_tokens + t0 + tt];
-        const double turns = a.inv_freq[p] * 0.15915494309189533577;  // 1 / 2 pi
-        const uint64_t frac =
-            __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);  // 2^64
+        const uint64_t frac = turn_fraction(a.inv_freq[p]);
         const uint64_t phase = frac * static_cast<uint64_t>(static_cast<int64_t>(pos));
         // the upper 32 bits, signed: half turns in [-1, 1)
         const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
@@ -129,32 +145,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Args a) {
     for (int i = threadIdx.x / VPR; i < live * nrows; i += kThreads / VPR) {
         const int tt = i / nrows, row = row0 + i - tt * nrows;
         const int64_t t = t0 + tt;
-        const bool is_q = row < a.num_q_heads;
-        const bool is_v = row >= a.num_q_heads + a.num_kv_heads;
-        const int h = is_q ? row : row - a.num_q_heads - (is_v ? a.num_kv_heads : 0);
+        const bool is_q = row < a.num_q_heads, is_v = row >= a.num_q_heads + a.num_kv_heads;
+        const int h = row - (is_q ? 0 : is_v ? a.num_q_heads + a.num_kv_heads : a.num_q_heads);
         const int32_t slot = slot_s[tt];
         if (!is_q && slot < 0) continue;
-        const __nv_bfloat16 *src = is_q   ? a.q + t * a.q_stride
-                                   : is_v ? a.v + t * a.v_stride
-                                          : a.k + t * a.k_stride;
-        src += static_cast<int64_t>(h) * D;
-        uint4 wa, wb;
-        int da = ea, db = eb;
-        if (is_v) {
-            da = 16 * j;
-            db = da + 8;
-        }
-        wa = *reinterpret_cast<const uint4 *>(src + da);
-        wb = *reinterpret_cast<const uint4 *>(src + db);
+        const __nv_bfloat16 *src = (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) +
+                                   static_cast<int64_t>(h) * D;
+        const int da = is_v ? 16 * j : ea, db = is_v ? da + 8 : eb;
+        const uint4 wa = *reinterpret_cast<const uint4 *>(src + da);
+        const uint4 wb = *reinterpret_cast<const uint4 *>(src + db);
         const int64_t dst =
             is_q ? (t * a.num_q_heads + h) * D
                  : ((static_cast<int64_t>(slot / a.block_size) * a.num_kv_heads + h) * a.block_size +
                     slot % a.block_size) * D;
         const bool rotate = turn && !is_v;
         if (!rotate && (!FP8 || is_q)) {  // bits as they are
-            __nv_bfloat16 *to = is_q   ? a.q_out
-                                : is_v ? reinterpret_cast<__nv_bfloat16 *>(a.v_cache)
-                                       : reinterpret_cast<__nv_bfloat16 *>(a.k_cache);
+            __nv_bfloat16 *to = is_q ? a.q_out : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache);
             *reinterpret_cast<uint4 *>(to + dst + da) = wa;
             *reinterpret_cast<uint4 *>(to + dst + db) = wb;
             continue;
@@ -307,9 +313,14 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
     a.v_scales = v_scales;
     a.err = err;
     const int rows = num_q_heads + 2 * num_kv_heads;
-    a.tile = num_tokens >= 8 * 152 * 4 ? 8 : num_tokens >= 4 * 152 * 4 ? 4 : num_tokens >= 2 * 152 * 4 ? 2 : 1;
+    // Tokens to a CTA: up to some 24,000 elements, so that the angles of its
+    // tokens are a small part of its work, but two CTAs to an SM.
+    a.tile = 1;
+    while (a.tile < rope::kMaxTile && 2 * a.tile * rows * head_dim <= 24576 && num_tokens >= 2 * a.tile * 2 * 152) a.tile *= 2;
     const int at_once = rope::kThreads / (head_dim / 16);  // rows of one pass of the CTA's threads
-    a.rows_per_y = num_tokens <= 152 ? at_once : rows;
+    // With few tokens a token's rows are shared out too, up to four CTAs to an SM.
+    const int shares = std::max(1, std::min((rows + at_once - 1) / at_once, 4 * 152 / num_tokens));
+    a.rows_per_y = (rows + shares - 1) / shares;
     const dim3 grid((num_tokens + a.tile - 1) / a.tile, (rows + a.rows_per_y - 1) / a.rows_per_y);
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
     if (head_dim == 128)

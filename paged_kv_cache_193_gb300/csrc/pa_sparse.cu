@@ -31,98 +31,114 @@ struct SummaryArgs {
     unsigned int *err;
 };
 
-// A CTA looks at 32 slots; each of its warps takes (completed page, head)
+constexpr int kSummarySlots = 16;  // looked at by a CTA
+constexpr int kSummaryWarps = 8;
+
+// A CTA looks at 16 slots; each of its warps takes (completed page, head)
 // items in turn.  A lane reads 16-byte pieces of the page's rows, all before
-// the first is used.
+// the first is used, and keeps their largest and least as packed bf16; lanes
+// that hold the same head dims then join theirs, the lower half of the warp
+// the largest and the upper half the least.  An E4M3 code in the upper byte of
+// a bf16 is finite and keeps the codes' order (both are sign and magnitude),
+// so codes are compared as they are; the code of NaN comes out as the largest
+// or the least, and bf16 NaNs pass through their maximum and minimum.
+//
+// Bound: latency (the slots, then the page, then the joins) up to some
+// thousand pages, the memory above.
 template <int D, int BS, bool FP8>
-__global__ void __launch_bounds__(256) summary_kernel(const SummaryArgs a) {
+__global__ void __launch_bounds__(kSummaryWarps * 32) summary_kernel(const SummaryArgs a) {
+    using T = __nv_bfloat162;
     constexpr int ELEM = FP8 ? 1 : 2;
-    constexpr int EPL = 16 / ELEM;       // elements of a lane's piece
-    constexpr int LPR = D / EPL;         // lanes to a row
-    constexpr int RPL = 32 / LPR;        // rows per load of the warp
+    constexpr int EPL = 16 / ELEM;  // elements of a lane's piece
+    constexpr int LPR = D / EPL;    // lanes to a row
+    constexpr int RPL = 32 / LPR;   // rows per load of the warp
     constexpr int LOADS = BS / RPL;
+    constexpr int PAIRS = EPL / 2;
+    auto pair = [](uint32_t w) { return *reinterpret_cast<const T *>(&w); };
+    auto bits = [](const T &x) { return *reinterpret_cast<const uint32_t *>(&x); };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int token = blockIdx.x * 32 + lane;
-    int32_t slot = token < a.num_tokens ? a.slots[token] : -1;
+    const int token = blockIdx.x * kSummarySlots + lane;
+    int32_t slot = lane < kSummarySlots && token < a.num_tokens ? a.slots[token] : -1;
     if (slot >= a.num_slots) {
         if (warp == 0) set_device_error(a.err, PA_DEVERR_BAD_SLOT);
         slot = -1;
     }
-    uint32_t ends = __ballot_sync(0xffffffffu, slot >= 0 && slot % BS == BS - 1);
+    const uint32_t ends = __ballot_sync(0xffffffffu, slot >= 0 && slot % BS == BS - 1);
     const int items = __popc(ends) * a.num_kv_heads;
-    for (int it = warp; it < items; it += 8) {
+    for (int it = warp; it < items; it += kSummaryWarps) {
         const int nth = it / a.num_kv_heads, h = it - nth * a.num_kv_heads;
-        const int from = __fns(ends, 0, nth + 1);
-        const int64_t blk = __shfl_sync(0xffffffffu, slot, from) / BS;
+        uint32_t rest = ends;
+        for (int k = 0; k < nth; ++k) rest &= rest - 1;
+        const int64_t blk = __shfl_sync(0xffffffffu, slot, __ffs(rest) - 1) / BS;
         const int64_t row = blk * a.num_kv_heads + h;
         const uint8_t *src = a.k_cache + row * (BS * D * ELEM) + lane * 16;
         uint4 w[LOADS];
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + i * 512);
-        float hi[EPL], lo[EPL];
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-            hi[e] = -INFINITY;
-            lo[e] = INFINITY;
-        }
-        bool odd = false;  // an infinity or NaN among the keys
+        T hi[PAIRS], lo[PAIRS];  // E4M3: bytes 0 and 2 of a word, then 1 and 3
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                if constexpr (FP8) {
-                    uint32_t l2, h2;
-                    e4m3x4_to_f16x2x2(u[p], l2, h2);
-                    const float2 f0 = __half22float2(*reinterpret_cast<__half2 *>(&l2));
-                    const float2 f1 = __half22float2(*reinterpret_cast<__half2 *>(&h2));
-                    const float x[4] = {f0.x, f0.y, f1.x, f1.y};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        odd |= !(fabsf(x[e]) < INFINITY);
-                        hi[4 * p + e] = fmaxf(hi[4 * p + e], x[e]);
-                        lo[4 * p + e] = fminf(lo[4 * p + e], x[e]);
-                    }
-                } else {
-                    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[p]));
-                    odd |= !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
-                    hi[2 * p] = fmaxf(hi[2 * p], f.x);
-                    lo[2 * p] = fminf(lo[2 * p], f.x);
-                    hi[2 * p + 1] = fmaxf(hi[2 * p + 1], f.y);
-                    lo[2 * p + 1] = fminf(lo[2 * p + 1], f.y);
-                }
+            for (int k = 0; k < PAIRS; ++k) {
+                const uint32_t v = !FP8 ? u[k % 4] : (k & 1 ? u[k / 2] : u[k / 2 % 4] << 8) & 0xff00ff00u;
+                const T x = pair(v);
+                hi[k] = i == 0 ? x : __hmax2_nan(hi[k], x);
+                lo[k] = i == 0 ? x : __hmin2_nan(lo[k], x);
             }
         }
+        // lower half: the largest; upper half: the least
+        T ext[PAIRS];
         float amax = 0.f;
+        bool odd = false;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) {
+        for (int k = 0; k < PAIRS; ++k) {
+            const bool low = lane < 16;
+            T x = low ? hi[k] : lo[k];
 #pragma unroll
-            for (int m = LPR; m < 32; m <<= 1) {
-                hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], m));
-                lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], m));
+            for (int m = 16; m >= LPR; m >>= 1) {
+                const T o = pair(__shfl_xor_sync(0xffffffffu, m == 16 ? bits(low ? lo[k] : hi[k]) : bits(x), m));
+                x = low ? __hmax2_nan(x, o) : __hmin2_nan(x, o);
             }
-            amax = fmaxf(amax, fmaxf(fabsf(hi[e]), fabsf(lo[e])));
+            ext[k] = x;
+        }
+        float2 val[PAIRS];
+#pragma unroll
+        for (int k = 0; k < PAIRS; ++k) {
+            if constexpr (FP8) {
+                const uint32_t b = bits(ext[k]);
+                uint32_t f, none;
+                e4m3x4_to_f16x2x2((b >> 8 & 0xffu) | (b >> 16 & 0xff00u), f, none);
+                val[k] = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+            } else {
+                val[k] = __bfloat1622float2(ext[k]);
+            }
+            odd |= !(fabsf(val[k].x) < INFINITY) || !(fabsf(val[k].y) < INFINITY);
+            amax = fmaxf(amax, fmaxf(fabsf(val[k].x), fabsf(val[k].y)));
         }
 #pragma unroll
-        for (int m = 1; m < LPR; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        for (int m = 1; m < 32; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
         odd = __any_sync(0xffffffffu, odd);
         const int ex = odd ? kOddExp : shared_exponent(amax);
-        const float inv = odd ? 0.f : power_of_two(-ex);
-        if (lane < 2 * LPR) {  // the first lanes write the largest, the next the least
-            int8_t *dst = a.summary + row * (2 * D) + lane * EPL;
+        const float inv = power_of_two(odd ? 0 : -ex);
+        if ((lane & 15) < LPR) {
             uint32_t out[EPL / 4];
 #pragma unroll
-            for (int e = 0; e < EPL; e += 4) {
+            for (int k = 0; k < EPL / 4; ++k) {
+                // elements 4k .. 4k + 3
+                const float2 p = val[2 * k], r = val[2 * k + 1];
+                const int x[4] = {to_int8(p.x, inv), to_int8(FP8 ? r.x : p.y, inv), to_int8(FP8 ? p.y : r.x, inv),
+                                  to_int8(r.y, inv)};
                 uint32_t v = 0;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const float x = lane < LPR ? hi[e + b] : lo[e + b];
-                    v |= static_cast<uint32_t>((odd ? 0 : to_int8(x, inv)) & 0xff) << (8 * b);
-                }
-                out[e / 4] = v;
+                for (int b = 0; b < 4; ++b) v |= (static_cast<uint32_t>(x[b]) & 0xffu) << (8 * b);
+                out[k] = odd ? 0u : v;
             }
-#pragma unroll
-            for (int e = 0; e < EPL / 4; ++e) reinterpret_cast<uint32_t *>(dst)[e] = out[e];
+            int8_t *dst = a.summary + row * (2 * D) + (lane < 16 ? 0 : D) + (lane & 15) * EPL;
+            if constexpr (EPL == 16)
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+            else
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
         }
         if (lane == 0) a.exponents[row] = static_cast<int8_t>(ex);
     }
@@ -238,9 +254,9 @@ pa_status run_select(const SelectArgs &a, int num_rows, int head_dim, cudaStream
 template <int D, int BS>
 static void launch_summary(const SummaryArgs &a, bool fp8, unsigned grid, cudaStream_t stream) {
     if (fp8)
-        summary_kernel<D, BS, true><<<grid, 256, 0, stream>>>(a);
+        summary_kernel<D, BS, true><<<grid, kSummaryWarps * 32, 0, stream>>>(a);
     else
-        summary_kernel<D, BS, false><<<grid, 256, 0, stream>>>(a);
+        summary_kernel<D, BS, false><<<grid, kSummaryWarps * 32, 0, stream>>>(a);
 }
 
 }  // namespace sparse
@@ -284,7 +300,7 @@ pa_status pa_block_summary(const void *k_cache, const int32_t *slot_mapping, int
     a.num_kv_heads = num_kv_heads;
     a.err = err;
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
-    const unsigned grid = (static_cast<unsigned>(num_tokens) + 31) / 32;
+    const unsigned grid = (static_cast<unsigned>(num_tokens) + kSummarySlots - 1) / kSummarySlots;
     if (head_dim == 128)
         block_size == 16 ? launch_summary<128, 16>(a, fp8, grid, stream)
                          : launch_summary<128, 32>(a, fp8, grid, stream);
