@@ -505,8 +505,7 @@ pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t
  *   rounded to fp16 as in pa_decode_partitions.
  * pa_sparse_attend: pa_sparse_select followed by pa_sparse_decode; selected and
  *   counts are outputs.  One kernel, in which each (row, KV head)'s CTAs choose
- *   and attend, so that one row's attention hides another's choice; two kernels
- *   when max_blocks_per_seq > 65536.
+ *   and attend, so that one row's attention hides another's choice.
  */
 pa_status pa_block_summary(const void *k_cache, const int32_t *slot_mapping, int num_tokens,
                            int num_blocks, int num_kv_heads, int head_dim, int block_size,

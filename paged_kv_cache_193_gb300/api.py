@@ -631,7 +631,7 @@ class SparseDecodeStep:
 
     def launches(self) -> int:
         """Kernels one call launches."""
-        return 4 if self.block_tables.shape[1] <= 65536 else 5
+        return 4
 
     def __call__(self, q, k_new, v_new, stream=None):
         slot_mapping(self.block_tables, self.context_lens, self.B, out=self.slots, stream=stream)

@@ -152,25 +152,25 @@ template <int D, int NT, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads, (NT == 2 ? 384 : 512) / kSelThreads) select_kernel(const SelectArgs a) {
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) Choice<D, NT, kSelThreads> sh;
-    choose<D, NT, kSelThreads>(a, dyn, reinterpret_cast<uint32_t *>(dyn + copy_bytes<D, kSelThreads>()), sh,
+    choose<D, NT, kSelThreads>(a, dyn, reinterpret_cast<uint32_t *>(dyn + copy_bytes(kSelThreads, D, a.stages)), sh,
                                static_cast<int>(cluster_rank()), static_cast<int>(cluster_size()), blockIdx.y, blockIdx.z);
 }
 
 template <int D, int NT, int kSelThreads>
-static pa_status launch_threads(const SelectArgs &a, int num_rows, cudaStream_t stream) {
+static pa_status launch_threads(SelectArgs a, int num_rows, cudaStream_t stream) {
+    a.stages = kMaxStages;
     const int64_t rows = static_cast<int64_t>(num_rows) * a.num_kv_heads;
     int ranks = 1;
     while (ranks < 8 && ((rows * ranks < kSms && a.max_blocks > 512 * ranks) || a.max_blocks > kMaxKeys * ranks)) ranks *= 2;
-    constexpr int kCopies = copy_bytes<D, kSelThreads>();
-    const int share = ((a.max_blocks + ranks - 1) / ranks + 31) & ~31;
     auto kern = select_kernel<D, NT, kSelThreads>;
     static std::atomic<uint64_t> raised{0};
-    pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), kCopies + kMaxKeys * 4 + 16, raised);
+    const int copies = copy_bytes(kSelThreads, D, kMaxStages);
+    pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), copies + key_bytes(kMaxKeys, 1), raised);
     if (st != PA_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ranks, a.num_kv_heads, num_rows);
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = kCopies + static_cast<size_t>(share + 4) * 4;
+    cfg.dynamicSmemBytes = copies + key_bytes(a.max_blocks, ranks);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

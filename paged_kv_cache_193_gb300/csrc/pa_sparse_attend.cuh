@@ -15,6 +15,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "pa_sparse_select.cuh"
 
 namespace pa {
@@ -35,12 +37,17 @@ struct Args {
     uint64_t wait_limit_ns;
     int stall_first_wait;
     SelectArgs select;  // of the kernel that chooses the pages itself
+    int longest_first;  // its clusters take the rows by length
 };
 
-// Candidate pages that a CTA of the choosing kernel can hold keys of.
-constexpr int kFusedKeys = 8192;
 pa_status launch_chosen(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
                         int num_rows, int splits, cudaStream_t stream);
+
+// CTAs to an SM, as the registers and the ring allow.
+constexpr int resident_ctas(int head_dim, int block_size, bool fp8, int group) {
+    if (head_dim == 64) return group > 8 || (block_size == 32 && !fp8) ? 3 : 4;
+    return group > 8 && !(block_size == 16 && !fp8) ? 2 : 3;
+}
 
 // limit of the drain of copies in flight after a wait gave up
 constexpr uint64_t kDrainNs = 2000000000ull;
@@ -62,10 +69,6 @@ struct Shape {
     // then the CTA's own partial and (reference, sum)
     static constexpr int JOIN = (NW * NP * OSTR + 2 * NW * NP + NP * D + 2 * NP) * 4;
     static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + 1024;  // + base alignment
-    // the choice before the ring is filled: copies of bounds, then keys; the
-    // 64 bytes behind the ring let eight CTAs hold 2^16 keys
-    static constexpr int COPIES = copy_bytes<D, NW * 32>();
-    static_assert((RING + 64 - COPIES) / 4 - 4 >= 8192, "room for the keys");
     static constexpr int MT = BS / 16;   // 16-token tiles of a page
     static constexpr int MI = PPI * MT;  // and of a step
     static constexpr int KSTEPS = D / 16;
@@ -82,9 +85,27 @@ __device__ __forceinline__ uint32_t at(uint32_t base, int t, int b) {
     return base + slab * (BS * C::SLAB) + t * C::SLAB + (phys << 4) + (within & 15);
 }
 
+// The row of the z-th longest context of `n` (at most kMaxSorted), the first of
+// equals first; `room` is 4 n + 4 bytes of shared memory.
+constexpr int kMaxSorted = 128;
+__device__ __forceinline__ int longest_row(const int32_t *lens, int n, int z, void *room) {
+    int32_t *len = static_cast<int32_t *>(room);
+    const int i = threadIdx.x;
+    const int32_t mine = i < n ? lens[i] : 0;
+    if (i < n) len[i] = mine;
+    __syncthreads();
+    int before = 0;
+    for (int j = 0; j < n; ++j) before += len[j] > mine || (len[j] == mine && j < i);
+    if (i < n && before == z) len[n] = i;
+    __syncthreads();
+    const int row = len[n];
+    __syncthreads();  // the room is used again
+    return row;
+}
+
 // CHOOSE: the cluster first chooses the row's pages, in the ring's memory.
 template <int D, int BS, bool FP8, int NT, int NW, int SPW, bool CHOOSE>
-__global__ void __launch_bounds__(NW * 32, (NT == 2 && BS == 16 && !FP8) ? 3 : 2)
+__global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8))
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const Args a) {
     using C = Shape<D, BS, FP8, NT, NW, SPW>;
@@ -97,9 +118,12 @@ __global__ void __launch_bounds__(NW * 32, (NT == 2 && BS == 16 && !FP8) ? 3 : 2
     const uint32_t ring = (raw + 1023u) & ~1023u;
     float *join = reinterpret_cast<float *>(smem_raw + (ring - raw));
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
-    const int h = blockIdx.y, s = blockIdx.z;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, c = lane & 3;
+    const int h = blockIdx.y;
+    int s = blockIdx.z;
+    if constexpr (CHOOSE)
+        if (a.longest_first) s = longest_row(a.context_lens, gridDim.z, s, join);
 
     const float k_scale = FP8 ? (a.k_scales ? __ldg(a.k_scales + h) : a.kv_scale) : 1.f;
     const float v_scale = FP8 ? (a.v_scales ? __ldg(a.v_scales + h) : a.kv_scale) : 1.f;
@@ -118,7 +142,7 @@ __global__ void __launch_bounds__(NW * 32, (NT == 2 && BS == 16 && !FP8) ? 3 : 2
     if constexpr (CHOOSE) {
         __shared__ __align__(16) Choice<D, NT, NW * 32> sh;
         uint8_t *mem = smem_raw + (ring - raw);
-        chosen = choose<D, NT, NW * 32>(a.select, mem, reinterpret_cast<uint32_t *>(mem + C::COPIES), sh,
+        chosen = choose<D, NT, NW * 32>(a.select, mem, reinterpret_cast<uint32_t *>(mem + copy_bytes(NW * 32, D, a.select.stages)), sh,
                                         static_cast<int>(rank), static_cast<int>(ranks), h, s);
         fence_proxy_async_smem();  // this memory is next written by page copies
     }
@@ -158,8 +182,6 @@ __global__ void __launch_bounds__(NW * 32, (NT == 2 && BS == 16 && !FP8) ? 3 : 2
     const int nb = n > 0 ? (n + BS - 1) / BS : 0;
     __syncthreads();
     if constexpr (!CHOOSE) {
-        // the list may come from the kernel before this one on the stream
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         const int64_t row = static_cast<int64_t>(s) * a.num_kv_heads + h;
         chosen = Chosen{min(max(a.counts[row], 0), a.top_k), a.selected + row * a.top_k};
     }
@@ -607,63 +629,71 @@ __global__ void __launch_bounds__(NW * 32, (NT == 2 && BS == 16 && !FP8) ? 3 : 2
 
 constexpr int kWarps = 4;
 
-// Page ring per CTA: 64 KB (three CTAs per SM), and 96 KB where a group above
-// 8 needs so many registers that only two fit.
+// Page ring per CTA.  Head dim 128: 64 KB, so that three CTAs fit on an SM, and
+// 96 KB where a group above 8 needs so many registers that only two fit.  Head
+// dim 64: two steps to a warp, 32 KB mostly: four CTAs up to 8 query heads.
 template <int D, int BS, bool FP8, int NT>
 constexpr int stages_per_warp() {
+    if (D == 64) return 2;
     constexpr int ppi = (FP8 && BS == 16) ? 2 : 1;
     constexpr int stage = 2 * ppi * BS * D * (FP8 ? 1 : 2);
-    constexpr bool wide = D == 128 && NT == 2 && !(BS == 16 && !FP8);
-    constexpr int spw = (wide ? 96 : 64) * 1024 / (kWarps * stage);
-    return spw < 1 ? 1 : spw;
+    constexpr bool wide = NT == 2 && !(BS == 16 && !FP8);
+    return (wide ? 96 : 64) * 1024 / (kWarps * stage) < 1 ? 1 : (wide ? 96 : 64) * 1024 / (kWarps * stage);
 }
 
 template <int D, int BS, bool FP8, int NT, bool CHOOSE>
-static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int num_rows,
-                               int splits, bool dependent, cudaStream_t stream) {
+static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a0, int num_rows,
+                               int splits, cudaStream_t stream) {
     constexpr int SPW = stages_per_warp<D, BS, FP8, NT>();
     using C = Shape<D, BS, FP8, NT, kWarps, SPW>;
-    constexpr int kSmem = C::SMEM + (CHOOSE ? 64 : 0);
+    // The choice works where the ring will be: copies of bounds, then keys.  Long
+    // shares take more shared memory than the ring.
+    Args a = a0;
+    int smem = C::SMEM;
+    if constexpr (CHOOSE) {
+        const int keys = key_bytes(a.select.max_blocks, splits);
+        a.select.stages = copy_bytes(kWarps * 32, D, kMaxStages) + keys <= C::SMEM - 1024 ? kMaxStages : 2;
+        smem = std::max(smem, 1024 + copy_bytes(kWarps * 32, D, a.select.stages) + keys);
+    }
+    constexpr int kMostSmem = CHOOSE ? std::max(C::SMEM, 1024 + copy_bytes(kWarps * 32, D, 2) + (kMaxKeys + 4) * 4) : C::SMEM;
     auto kern = attend_kernel<D, BS, FP8, NT, kWarps, SPW, CHOOSE>;
     static std::atomic<uint64_t> raised{0};
-    pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), kSmem, raised);
+    pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), kMostSmem, raised);
     if (st != PA_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, a.num_kv_heads, num_rows);
     cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = splits;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 2 : 1;
+    cfg.numAttrs = 1;
     return cuda_check(cudaLaunchKernelEx(&cfg, kern, tk, tv, a), "sparse decode launch");
 }
 
 template <int D, int BS, bool CHOOSE>
 static pa_status launch_shape(bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
-                              int num_rows, int splits, bool dependent, cudaStream_t stream) {
+                              int num_rows, int splits, cudaStream_t stream) {
     if (fp8)
-        return a.group <= 8 ? launch_attend<D, BS, true, 1, CHOOSE>(tk, tv, a, num_rows, splits, dependent, stream)
-                            : launch_attend<D, BS, true, 2, CHOOSE>(tk, tv, a, num_rows, splits, dependent, stream);
-    return a.group <= 8 ? launch_attend<D, BS, false, 1, CHOOSE>(tk, tv, a, num_rows, splits, dependent, stream)
-                        : launch_attend<D, BS, false, 2, CHOOSE>(tk, tv, a, num_rows, splits, dependent, stream);
+        return a.group <= 8 ? launch_attend<D, BS, true, 1, CHOOSE>(tk, tv, a, num_rows, splits, stream)
+                            : launch_attend<D, BS, true, 2, CHOOSE>(tk, tv, a, num_rows, splits, stream);
+    return a.group <= 8 ? launch_attend<D, BS, false, 1, CHOOSE>(tk, tv, a, num_rows, splits, stream)
+                        : launch_attend<D, BS, false, 2, CHOOSE>(tk, tv, a, num_rows, splits, stream);
 }
 
 
 template <bool CHOOSE>
 static pa_status launch_any(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv,
-                            const Args &a, int num_rows, int splits, bool dependent, cudaStream_t stream) {
+                            const Args &a, int num_rows, int splits, cudaStream_t stream) {
     if (head_dim == 128)
-        return block_size == 16 ? launch_shape<128, 16, CHOOSE>(fp8, tk, tv, a, num_rows, splits, dependent, stream)
-                                : launch_shape<128, 32, CHOOSE>(fp8, tk, tv, a, num_rows, splits, dependent, stream);
-    return block_size == 16 ? launch_shape<64, 16, CHOOSE>(fp8, tk, tv, a, num_rows, splits, dependent, stream)
-                            : launch_shape<64, 32, CHOOSE>(fp8, tk, tv, a, num_rows, splits, dependent, stream);
+        return block_size == 16 ? launch_shape<128, 16, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream)
+                                : launch_shape<128, 32, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream);
+    return block_size == 16 ? launch_shape<64, 16, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream)
+                            : launch_shape<64, 32, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream);
 }
 
 }  // namespace sparse

@@ -52,9 +52,8 @@ static int splits_for(int64_t rows, int top_k, int resident) {
     return splits;
 }
 
-// `select`: choose the pages in the same kernel; otherwise the list is there,
-// or comes from the kernel before this one (`dependent`).
-static pa_status run_attend(const Call &c, const SelectArgs *select, bool dependent, cudaStream_t stream) {
+// `select`: choose the pages in the same kernel; otherwise the list is there.
+static pa_status run_attend(const Call &c, const SelectArgs *select, cudaStream_t stream) {
     const bool fp8 = c.kv_dtype == PA_KV_FP8_E4M3;
     const int64_t pool_rows = static_cast<int64_t>(c.num_blocks) * c.num_kv_heads * c.block_size;
     CUtensorMap tk, tv;
@@ -85,17 +84,18 @@ static pa_status run_attend(const Call &c, const SelectArgs *select, bool depend
     a.wait_limit_ns = wait_limit_ns();
     a.stall_first_wait = stall_first_wait();
     const int64_t rows = static_cast<int64_t>(c.num_rows) * c.num_kv_heads;
-    // CTAs to an SM (see the ring's size)
-    const bool wide = c.head_dim == 128 && a.group > 8 && !(c.block_size == 16 && !fp8);
-    const int resident = wide ? 2 : 3;
+    const int resident = resident_ctas(c.head_dim, c.block_size, fp8, a.group);
     if (select) {
         a.select = *select;
+        a.longest_first = 0;
         int splits = splits_for(rows, c.top_k, resident);
-        while (c.max_blocks > kFusedKeys * splits) ++splits;  // at most 8: checked by the caller
+        while (c.max_blocks > kMaxKeys * splits) ++splits;  // at most 8, by the limit on the table
+        // With more CTAs than places, and rows that few threads can sort
+        a.longest_first = c.num_rows > 1 && c.num_rows <= kMaxSorted && rows * splits > resident * kSms;
         return launch_chosen(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, stream);
     }
     const int splits = c.splits ? c.splits : splits_for(rows, c.top_k, resident);
-    return launch_any<false>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, dependent, stream);
+    return launch_any<false>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, stream);
 }
 
 }  // namespace sparse
@@ -124,7 +124,7 @@ pa_status pa_sparse_decode(const void *q, const void *k_cache, const void *v_cac
     if (st != PA_OK) return st;
     if (num_rows == 0) return PA_OK;
     st = check_pointers(c);
-    return st == PA_OK ? run_attend(c, nullptr, false, stream) : st;
+    return st == PA_OK ? run_attend(c, nullptr, stream) : st;
 }
 
 pa_status pa_sparse_attend(const void *q, const void *k_cache, const void *v_cache,
@@ -152,9 +152,7 @@ pa_status pa_sparse_attend(const void *q, const void *k_cache, const void *v_cac
     const SelectArgs sel = select_args(q, summary, exponents, block_tables, max_blocks_per_seq, context_lens,
                                        num_q_heads, num_kv_heads, num_blocks, block_size, top_k, sink_blocks,
                                        recent_blocks, selected, counts);
-    if (max_blocks_per_seq <= 8 * kFusedKeys) return run_attend(c, &sel, false, stream);
-    st = run_select(sel, num_rows, head_dim, stream);
-    return st == PA_OK ? run_attend(c, nullptr, true, stream) : st;
+    return run_attend(c, &sel, stream);
 }
 
 }  // extern "C"

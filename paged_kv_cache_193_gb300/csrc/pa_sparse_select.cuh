@@ -35,6 +35,7 @@ struct SelectArgs {
     int32_t *counts;    // [num_rows][num_kv_heads]
     int max_blocks, num_blocks, num_kv_heads, group, block_size;
     int top_k, sink, recent;
+    int stages;  // of the warps' rings of copies: 2 or 3
     unsigned int *err;
 };
 
@@ -53,7 +54,11 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Four signed bytes of a word as fp16 pairs, even = bytes 0 and 2, odd = bytes
 // 1 and 3: 0x6400 | (x + 128) is the fp16 value kOffset + x, exactly.
@@ -95,10 +100,9 @@ struct alignas(16) Choice {
     uint32_t bits[16];  // pages taken, of few
 };
 
-// Candidates that are ranked one against another with no histogram: up to
-// kFewAlone when a CTA has the row to itself, kFewShared in a cluster (whose
-// histograms cost five cluster-wide barriers).
-constexpr int kFewAlone = 256, kFewShared = 500;
+// Up to this many candidates, no more than one to a thread, are ranked one
+// against another with no histogram: a cluster's histograms cost five barriers.
+constexpr int kFew = 500;
 
 // What a row attends to: `count` logical pages, listed, or the first ones when
 // `list` is null.
@@ -107,9 +111,15 @@ struct Chosen {
     const int32_t *list;
 };
 
-// Bytes of a CTA's copies in flight: 32 pages' bounds for each of its warps.
-template <int D, int kSelThreads>
-constexpr int copy_bytes() { return kSelThreads / 32 * 32 * 2 * D; }
+// A warp takes 16 pages' bounds at a time through a ring of `stages` such steps
+// of its own.
+constexpr int kStepPages = 16;
+constexpr int kMaxStages = 3;
+__host__ __device__ constexpr int copy_bytes(int threads, int head_dim, int stages) {
+    return threads / 32 * stages * kStepPages * 2 * head_dim;
+}
+// Bytes of keys that a CTA needs when `ranks` share a row.
+inline int key_bytes(int max_blocks, int ranks) { return ((((max_blocks + ranks - 1) / ranks + 31) & ~31) + 4) * 4; }
 
 // The cluster's choice for row t and KV head h, written to a.selected and
 // a.counts, and returned.
@@ -128,9 +138,7 @@ constexpr int copy_bytes() { return kSelThreads / 32 * 32 * 2 * D; }
 // last page to be taken, and, once few keys are left in the bin, their ranks
 // among one another; of few candidates, their ranks at once.
 //
-// `copies` is copy_bytes() of shared memory (16-byte aligned), `keys` room for
-// the CTA's share of the candidates (ceil(max_blocks / ranks), rounded up to
-// 32) and four more.  Every thread of the cluster calls it; on return the
+// `copies` is copy_bytes() of shared memory (16-byte aligned), `keys` key_bytes().  Every thread of the cluster calls it; on return the
 // listed pages are visible to all of them.
 template <int D, int NT, int kSelThreads>
 __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, uint32_t *keys, Choice<D, NT, kSelThreads> &sh,
@@ -164,7 +172,10 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
     // with one CTA to the row its first pages are known before the length is
     const int32_t *table = a.block_tables + static_cast<int64_t>(t) * a.max_blocks + a.sink;
     int32_t next_blk = -1;
-    if (ranks == 1 && a.sink + warp * 32 + lane < a.max_blocks) next_blk = __ldg(table + warp * 32 + lane);
+    {
+        const int at = warp * kStepPages + lane % kStepPages;
+        if (ranks == 1 && a.sink + at < a.max_blocks) next_blk = __ldg(table + at);
+    }
     int n = a.context_lens[t];
     if (n > a.max_blocks * a.block_size) {
         if (tid == 0 && rank == 0 && h == 0) set_device_error(a.err, PA_DEVERR_BAD_CONTEXT);
@@ -192,42 +203,48 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
     const int per = ((ncand + ranks - 1) / ranks + 31) & ~31;
     const int c0 = min(ncand, rank * per), c1 = min(ncand, c0 + per);
     const int have = c1 - c0;
-    const bool few = ncand <= (ranks > 1 ? kFewShared : kFewAlone) && a.top_k <= kBins;
-    // the table entries of this warp's next 32 pages
-    if (ranks > 1 && warp * 32 + lane < have) next_blk = __ldg(table + c0 + warp * 32 + lane);
-
-    // A warp takes 32 pages at a time: their bounds are copied into its part of
-    // `copies`, 16 bytes a lane; piece x of page p lies at x ^ 4 (p & 1), so that
-    // eight lanes' reads below meet eight bank groups.  Other warps' copies are
-    // in flight while one computes: a second set of copies per warp measured
-    // no faster (64 sequences of 4K-32K tokens: 47 against 46 us).
+    const bool few = per <= kSelThreads && ncand <= kFew && a.top_k <= kBins;
+    // The warp's i-th step is pages (i * warps + warp) * STEP and on of the
+    // share.  Their bounds are copied 16 bytes a lane, stages - 1 steps ahead;
+    // piece x of page p lies at x ^ 4 (p & 1), so that eight lanes' reads below
+    // meet eight bank groups.
     constexpr int PAGE = 2 * D;
-    constexpr int LPP = PAGE / 16;  // lanes to a page
-    constexpr int PPC = 32 / LPP;   // pages per copy instruction
-    const uint8_t *stage = copies + warp * (32 * PAGE);
-    const uint32_t stage_at = smem_addr(stage);
-    int next_exps = 0;  // the exponent of the lane's page
-    auto copy = [&](int first) {
-        int32_t blk = next_blk;
-        const int after = first + 32 * kSelWarps + lane;
-        next_blk = after < have ? __ldg(table + c0 + after) : -1;
-        const bool bad = blk < 0 || blk >= a.num_blocks;
-        if (bad) {
-            if (first + lane < have) set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
-            blk = 0;
-        }
-        const int32_t row = blk * a.num_kv_heads + h;  // below 2^27: the pool's limit
+    constexpr int STEP = kStepPages;
+    constexpr int LPP = PAGE / 16;     // lanes to a page
+    constexpr int PPC = 32 / LPP;      // pages per copy instruction
+    const int own = lane % STEP;       // the step's page that the lane looks up
+    const int steps = have > warp * STEP ? (have - warp * STEP + STEP * kSelWarps - 1) / (STEP * kSelWarps) : 0;
+    if (ranks > 1 && warp * STEP + own < have) next_blk = __ldg(table + c0 + warp * STEP + own);
+    const uint8_t *ring = copies + warp * a.stages * STEP * PAGE;
+    const uint32_t ring_at = smem_addr(ring);
+    int put = 0;
+    int exps0 = 0, exps1 = 0, exps2 = 0;  // exponents of the lane's pages, by age
+    auto copy = [&](int i) {
+        exps2 = exps1;
+        exps1 = exps0;
+        if (i < steps) {
+            const int at = (i * kSelWarps + warp) * STEP + own;
+            int32_t blk = next_blk;
+            next_blk = at + STEP * kSelWarps < have ? __ldg(table + c0 + at + STEP * kSelWarps) : -1;
+            const bool bad = blk < 0 || blk >= a.num_blocks;
+            if (bad) {
+                if (at < have) set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
+                blk = 0;
+            }
+            const int32_t row = blk * a.num_kv_heads + h;  // below 2^27: the pool's limit
+            const uint32_t dst = ring_at + put * STEP * PAGE;
+            put = put + 1 == a.stages ? 0 : put + 1;
 #pragma unroll
-        for (int k = 0; k < 32; k += PPC) {
-            const int p = k + lane / LPP, x = lane % LPP;
-            const int32_t prow = __shfl_sync(0xffffffffu, row, p);
-            cp_async16(stage_at + p * PAGE + ((x ^ ((p & 1) << 2)) << 4),
-                       a.summary + static_cast<int64_t>(prow) * PAGE + x * 16);
+            for (int k = 0; k < STEP; k += PPC) {
+                const int p = k + lane / LPP, x = lane % LPP;
+                const int32_t prow = __shfl_sync(0xffffffffu, row, p);
+                cp_async16(dst + p * PAGE + ((x ^ ((p & 1) << 2)) << 4),
+                           a.summary + static_cast<int64_t>(prow) * PAGE + x * 16);
+            }
+            exps0 = bad ? kBadExp : a.exponents[row];
         }
-        next_exps = bad ? kBadExp : a.exponents[row];
+        cp_async_commit();
     };
-    if (warp * 32 < have) copy(warp * 32);
-
     if (tid == 0) {
         sh.range[0] = 0xffffffffu;
         sh.range[1] = 0;
@@ -280,6 +297,7 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
             if (tid % 8 == 0) sh.sum[g][tid % TPH / 8] = static_cast<float>(total);
         }
     }
+    for (int i = 0; i < a.stages - 1; ++i) copy(i);
     __syncthreads();
     // B fragments: lane (r, c) holds pieces c, c + 4, ... of head r
     uint32_t qf[NT][PIECES][4][2];
@@ -305,76 +323,73 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
     // ---- scores of this CTA's share of the candidates -------------------------
     if (few && ranks > 1) cluster_wait();
     uint32_t kmin = 0xffffffffu, kmax = 0;
-    for (int first = warp * 32; first < have; first += 32 * kSelWarps) {
-        cp_async_wait_all();
+    int get = 0;
+    for (int it = 0; it < steps; ++it) {
+        copy(it + a.stages - 1);
+        if (a.stages == 3)
+            cp_async_wait<2>();
+        else
+            cp_async_wait<1>();
         __syncwarp();
-        const int exps = next_exps;
-        // both halves of the 32 pages and each 64 head dims have sums of their
-        // own: chains of eight products in place of one of 32
-        float acc[2][NT][SETS][4];
+        const int exps = a.stages == 3 ? exps2 : exps1;
+        const uint8_t *stage = ring + get * STEP * PAGE;
+        get = get + 1 == a.stages ? 0 : get + 1;
+        // each 64 head dims have sums of their own: two chains of eight products
+        float acc[NT][SETS][4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < SETS; ++k)
 #pragma unroll
-                for (int k = 0; k < SETS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[half][nt][k][e] = start[nt][k][e & 1];
+                for (int e = 0; e < 4; ++e) acc[nt][k][e] = start[nt][k][e & 1];
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             const int x = ((c + 4 * i) ^ ((r & 1) << 2)) << 4;
-            uint4 w[4];
+            const uint4 w0 = *reinterpret_cast<const uint4 *>(stage + r * PAGE + x);
+            const uint4 w1 = *reinterpret_cast<const uint4 *>(stage + (r + 8) * PAGE + x);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint4 *>(stage + (8 * k + r) * PAGE + x);
+            for (int j = 0; j < 4; ++j) {
+                auto word = [&](const uint4 &u) { return j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w; };
+                uint32_t a0, a1, a2, a3;
+                int8x4_offset_f16(word(w0), a0, a2);
+                int8x4_offset_f16(word(w1), a1, a3);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16816<true>(acc[nt][i % SETS], a0, a1, a2, a3, qf[nt][i][j][0], qf[nt][i][j][1]);
+            }
+        }
+        auto dot = [&](int nt, int e) {
+            float x = acc[nt][0][e];
+            if constexpr (SETS == 2) x += acc[nt][1][e];
+            return x;
+        };
+        float s0 = -INFINITY, s1 = -INFINITY;  // pages r and r + 8
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    auto word = [&](const uint4 &u) { return j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w; };
-                    uint32_t a0, a1, a2, a3;
-                    int8x4_offset_f16(word(w[2 * half]), a0, a2);
-                    int8x4_offset_f16(word(w[2 * half + 1]), a1, a3);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<true>(acc[half][nt][i % SETS], a0, a1, a2, a3, qf[nt][i][j][0], qf[nt][i][j][1]);
+            for (int j = 0; j < 2; ++j)
+                if (nt * 8 + 2 * c + j < a.group) {
+                    s0 = fmaxf(s0, dot(nt, j) * unit[nt][j]);
+                    s1 = fmaxf(s1, dot(nt, 2 + j) * unit[nt][j]);
                 }
+#pragma unroll
+        for (int m = 1; m < 4; m <<= 1) {
+            s0 = fmaxf(s0, __shfl_xor_sync(0xffffffffu, s0, m));
+            s1 = fmaxf(s1, __shfl_xor_sync(0xffffffffu, s1, m));
         }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            auto dot = [&](int nt, int e) {
-                float x = acc[half][nt][0][e];
-                if constexpr (SETS == 2) x += acc[half][nt][1][e];
-                return x;
-            };
-            float s0 = -INFINITY, s1 = -INFINITY;  // pages r and r + 8
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (nt * 8 + 2 * c + j < a.group) {
-                        s0 = fmaxf(s0, dot(nt, j) * unit[nt][j]);
-                        s1 = fmaxf(s1, dot(nt, 2 + j) * unit[nt][j]);
-                    }
-#pragma unroll
-            for (int m = 1; m < 4; m <<= 1) {
-                s0 = fmaxf(s0, __shfl_xor_sync(0xffffffffu, s0, m));
-                s1 = fmaxf(s1, __shfl_xor_sync(0xffffffffu, s1, m));
-            }
-            const int page = 16 * half + r + 8 * (c & 1);
-            const int ex = __shfl_sync(0xffffffffu, exps, page);
-            const int i = first + page;  // of the CTA's share
-            if (c < 2 && i < have) {
-                const float score = ex == kBadExp ? -INFINITY : ex == kOddExp ? INFINITY : (c ? s1 : s0) * power_of_two(ex);
-                const uint32_t key = order_key(score + 0.f);  // no negative zero
-                keys[i] = key;
-                if (few && ranks > 1)
-                    for (int k = 0; k < ranks; ++k) st_cluster_u32(smem_addr(&sh.hist[0][c0 + i]), k, key);
-                kmin = min(kmin, key);
-                kmax = max(kmax, key);
-            }
+        const int page = r + 8 * (c & 1);
+        const int ex = __shfl_sync(0xffffffffu, exps, page);
+        const int i = (it * kSelWarps + warp) * STEP + page;  // of the CTA's share
+        if (c < 2 && i < have) {
+            const float score = ex == kBadExp ? -INFINITY : ex == kOddExp ? INFINITY : (c ? s1 : s0) * power_of_two(ex);
+            const uint32_t key = order_key(score + 0.f);  // no negative zero
+            keys[i] = key;
+            if (few && ranks > 1)
+                for (int k = 0; k < ranks; ++k) st_cluster_u32(smem_addr(&sh.hist[0][c0 + i]), k, key);
+            kmin = min(kmin, key);
+            kmax = max(kmax, key);
         }
-        __syncwarp();  // the copies may be overwritten
-        if (first + 32 * kSelWarps < have) copy(first + 32 * kSelWarps);
+        __syncwarp();  // the step's place in the ring is free
     }
     if (few) {
         // Every CTA has all keys (its own, or every CTA's in sh.hist[0]) and

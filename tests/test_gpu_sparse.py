@@ -228,8 +228,8 @@ def test_choice_among_many_ties(api, cuda_device, D, Hq, S, pages):
 
 
 @pytest.mark.parametrize("D,G,S,pages,top_k,sink,recent", [
-    # candidates up to and just past the numbers that are ranked directly (256 alone, 500 in a cluster)
-    (64, 2, 304, 259, 20, 1, 2), (64, 2, 304, 260, 20, 1, 2), (128, 1, 2, 503, 90, 1, 2), (128, 1, 2, 504, 90, 1, 2),
+    # candidates up to and just past the numbers that are ranked directly (one to a thread, 500 in a cluster)
+    (64, 2, 304, 131, 20, 1, 2), (64, 2, 304, 132, 20, 1, 2), (64, 2, 304, 259, 20, 1, 2), (64, 2, 304, 260, 20, 1, 2), (128, 1, 2, 503, 90, 1, 2), (128, 1, 2, 504, 90, 1, 2),
     (128, 9, 3, 257, 40, 0, 1), (64, 16, 1, 513, 200, 0, 1),
     # one candidate more than is wanted, and lists longer than the candidates
     (128, 4, 1, 65, 64, 1, 2), (64, 1, 5, 130, 129, 60, 68), (128, 2, 2, 900, 700, 300, 350), (64, 3, 320, 900, 700, 300, 350),
