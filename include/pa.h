@@ -493,7 +493,8 @@ pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t
  *   The other blocks' bounds must have been made by pa_block_summary.
  *   selected int32 [num_rows][num_kv_heads][top_k]: ascending logical blocks,
  *   then -1; counts int32 [num_rows][num_kv_heads].  recent_blocks >= 1,
- *   sink_blocks + recent_blocks <= top_k, max_blocks_per_seq <= 131072.
+ *   sink_blocks + recent_blocks <= top_k; top_k and max_blocks_per_seq
+ *   <= 131072.
  * pa_sparse_decode: out[t][hq] = bf16_rn of the softmax of softmax_scale *
  *   q . K over the tokens (position < n) of the first counts[t][h] blocks of
  *   selected[t][h], applied to V; zeros when there are none.  Any list may be

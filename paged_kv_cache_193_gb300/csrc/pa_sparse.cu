@@ -216,6 +216,8 @@ pa_status check_select(int num_rows, int num_q_heads, int num_kv_heads, int head
                     "filled is always read, so recent_blocks is 1 or more", top_k, sink, recent);
     if (static_cast<int64_t>(sink) + recent > top_k)
         return fail(PA_ERR_INVALID_ARG, "sink_blocks %d + recent_blocks %d exceed top_k %d", sink, recent, top_k);
+    if (top_k > kMaxTableBlocks)
+        return fail(PA_ERR_UNSUPPORTED, "top_k %d (supported: up to %d)", top_k, kMaxTableBlocks);
     if (max_blocks > kMaxTableBlocks)
         return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq %d (supported: up to %d)", max_blocks, kMaxTableBlocks);
     return PA_OK;

@@ -45,8 +45,9 @@ pa_status launch_chosen(int head_dim, int block_size, bool fp8, const CUtensorMa
 
 // CTAs to an SM, as the registers and the ring allow.
 constexpr int resident_ctas(int head_dim, int block_size, bool fp8, int group) {
-    if (head_dim == 64) return group > 8 || (block_size == 32 && !fp8) ? 3 : 4;
-    return group > 8 && !(block_size == 16 && !fp8) ? 2 : 3;
+    const bool big = block_size == 32 && !fp8;  // pages twice the others' size
+    if (group <= 8) return big ? 3 : 4;
+    return head_dim == 64 || (block_size == 16 && !fp8) ? 3 : 2;
 }
 
 // limit of the drain of copies in flight after a wait gave up
@@ -629,16 +630,20 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8))
 
 constexpr int kWarps = 4;
 
-// Page ring per CTA.  Head dim 128: 64 KB, so that three CTAs fit on an SM, and
-// 96 KB where a group above 8 needs so many registers that only two fit.  Head
-// dim 64: two steps to a warp, 32 KB mostly: four CTAs up to 8 query heads.
+// Steps of a warp's ring.  Up to 8 query heads at head dim 128 one step, 32 KB
+// to a CTA and four CTAs to an SM, against two steps and three CTAs: 113 and 117
+// us over 64 sequences of 4K-32K tokens, 60 and 63 with E4M3 pages (512 clusters
+// of one CTA: four to an SM have places for all of them).  Groups above 8 need
+// so many registers that fewer CTAs fit, and take the memory: 64 KB for three
+// CTAs, 96 KB for two.  Head dim 64: two steps, 32 KB mostly.
 template <int D, int BS, bool FP8, int NT>
 constexpr int stages_per_warp() {
     if (D == 64) return 2;
+    if (NT == 1) return 1;
     constexpr int ppi = (FP8 && BS == 16) ? 2 : 1;
     constexpr int stage = 2 * ppi * BS * D * (FP8 ? 1 : 2);
-    constexpr bool wide = NT == 2 && !(BS == 16 && !FP8);
-    return (wide ? 96 : 64) * 1024 / (kWarps * stage) < 1 ? 1 : (wide ? 96 : 64) * 1024 / (kWarps * stage);
+    constexpr int spw = (BS == 16 && !FP8 ? 64 : 96) * 1024 / (kWarps * stage);
+    return spw < 1 ? 1 : spw;
 }
 
 template <int D, int BS, bool FP8, int NT, bool CHOOSE>

@@ -392,6 +392,32 @@ def test_choice_flags_bad_table_entries_and_contexts(api, cuda_device):
     assert out.isfinite().all()
 
 
+@pytest.mark.parametrize("S", [40, 75, 110, 150, 240, 300, 700])
+def test_every_number_of_ctas_to_a_row(api, cuda_device, S):
+    """Row counts for which a row gets 8, 6, 4, 3, 2 and 1 CTAs, and for which the rows are taken by length or not."""
+    rng = np.random.default_rng(S)
+    case = Case(cuda_device, [int(n) for n in rng.integers(0, 330, S)], 2, 1, D=64, seed=S)
+    s, e = case.summaries(api)
+    top_k = 34 if S < 100 else 16
+    sel, cnt, out = case.attend(api, s, e, top_k)
+    want_sel, want_cnt = R.select(f64(case.q), s.cpu().numpy(), e.cpu().numpy(), case.tables, case.lens, 16, top_k, 1, 2)
+    assert np.array_equal(sel, want_sel) and np.array_equal(cnt, want_cnt)
+    case.check(out, sel, cnt)
+    assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("Hkv", [5, 9])
+def test_rows_taken_by_length(api, cuda_device, Hkv):
+    """More clusters than places with 128 rows or fewer: the rows are taken longest first, equal ones in their order."""
+    lens = ([700, 16, 700, 0, 33] * 26)[:128]
+    case = Case(cuda_device, lens, Hkv, Hkv, D=64)
+    s, e = case.summaries(api)
+    sel, cnt, out = case.attend(api, s, e, 8)
+    want_sel, want_cnt = R.select(f64(case.q), s.cpu().numpy(), e.cpu().numpy(), case.tables, case.lens, 16, 8, 1, 2)
+    assert np.array_equal(sel, want_sel) and np.array_equal(cnt, want_cnt)
+    case.check(out, sel, cnt)
+
+
 def test_rows_may_share_a_sequence(api, cuda_device):
     """Several query tokens of one sequence, each with its own length."""
     case = Case(cuda_device, [613], 8, 2)
