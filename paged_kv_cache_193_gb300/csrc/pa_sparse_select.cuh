@@ -447,10 +447,9 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
 
     // ---- the key of the last page taken ---------------------------------------
     uint32_t low = sh.range[0], high = sh.range[1];
-    for (int k = 1; k < ranks; ++k) {
-        const uint32_t other = static_cast<uint32_t>((rank + k) % ranks);
-        low = min(low, ld_cluster_u32(smem_addr(&sh.range[0]), other));
-        high = max(high, ld_cluster_u32(smem_addr(&sh.range[1]), other));
+    if (ranks > 1) {  // a lane for each CTA
+        low = __reduce_min_sync(0xffffffffu, lane < ranks ? ld_cluster_u32(smem_addr(&sh.range[0]), lane) : 0xffffffffu);
+        high = __reduce_max_sync(0xffffffffu, lane < ranks ? ld_cluster_u32(smem_addr(&sh.range[1]), lane) : 0u);
     }
     uint32_t span = high - low;  // keys looked at: low .. low + span
     int shift = max(0, 32 - __clz(span) - kBinBits);
@@ -469,12 +468,19 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
         // four bins to a thread, from the top
         const uint32_t at = smem_addr(hs) + (kSelThreads - 1 - tid) * 16;
         uint4 v = make_uint4(0, 0, 0, 0);
-        for (int k = 0; k < ranks; ++k) {
-            const uint4 o = ranks > 1 ? ld_cluster_v4(at, k) : lds128(at);
-            v.x += o.x;
-            v.y += o.y;
-            v.z += o.z;
-            v.w += o.w;
+        if (ranks > 1) {
+            uint4 o[8];  // all in flight together
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = k < ranks ? ld_cluster_v4(at, k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v.x += o[k].x;
+                v.y += o[k].y;
+                v.z += o[k].z;
+                v.w += o[k].w;
+            }
+        } else {
+            v = lds128(at);
         }
         const uint32_t sum = v.x + v.y + v.z + v.w;
         uint32_t before = sum;
@@ -591,10 +597,8 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
             sh.taken[1] = se;
         }
         sync_all();
-        for (int k = 0; k < rank; ++k) {
-            xa += ld_cluster_u32(smem_addr(&sh.taken[0]), k);
-            xe += ld_cluster_u32(smem_addr(&sh.taken[1]), k);
-        }
+        xa = __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster_u32(smem_addr(&sh.taken[0]), lane) : 0u);
+        xe = __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster_u32(smem_addr(&sh.taken[1]), lane) : 0u);
     }
 #pragma unroll
     for (int w = 0; w < kSelWarps; ++w)

@@ -87,7 +87,6 @@ def _select(lib, fn="select", **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(S=-1), 1), (dict(Hkv=3), 1), (dict(Hq=64, Hkv=2), 2), (dict(D=96), 2), (dict(B=8), 2), (dict(NB=0), 1), (dict(mb=0), 1),
     (dict(S=70000), 2), (dict(NB=1 << 27), 2), (dict(k=0), 1), (dict(mb=1 << 28), 1), (dict(mb=(1 << 17) + 1), 2), (dict(k=(1 << 17) + 1), 2), (dict(k=2 ** 31 - 1), 2),
-   
     (dict(q=None), 1), (dict(bt=None), 1), (dict(cl=None), 1), (dict(sel=None), 1), (dict(cnt=None), 1), (dict(q=ODD), 1),
 ])
 def test_sparse_entry_points_reject_on_host(lib, fn, kw, status):
