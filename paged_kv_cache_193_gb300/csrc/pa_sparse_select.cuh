@@ -398,36 +398,56 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
         // were taken go to every CTA.
         uint32_t *all = ranks > 1 ? sh.hist[0] : keys;
         if (tid < 3) all[ncand + tid] = 0u;  // to a multiple of four, below every score's key
+        sh.ranked[tid] = 0;
         sync_all();
-        for (int b = 0; b < have; b += kSelThreads) {
-            const int i = c0 + b + tid;
-            const uint32_t key = b + tid < have ? all[i] : 0u;
+        // `split` threads to a page, each with its part of the keys
+        const int split = have <= kSelThreads / 4 ? 4 : have <= kSelThreads / 2 ? 2 : 1;
+        const int mine = tid % (kSelThreads / split), part = tid / (kSelThreads / split);
+        const int self = c0 + mine;
+        if (mine < have) {
+            const uint32_t key = all[self];
             uint32_t place = 0;
-            if (b + warp * 32 < have)
-                for (int j = 0; j < ncand; j += 4) {
-                    const uint4 k4 = *reinterpret_cast<const uint4 *>(all + j);
-                    place += k4.x > key || (k4.x == key && j < i);
-                    place += k4.y > key || (k4.y == key && j + 1 < i);
-                    place += k4.z > key || (k4.z == key && j + 2 < i);
-                    place += k4.w > key || (k4.w == key && j + 3 < i);
-                }
-            const uint32_t votes = __ballot_sync(0xffffffffu, b + tid < have && place < static_cast<uint32_t>(want));
-            if (b + warp * 32 < have && lane < ranks) {
+#pragma unroll 4
+            for (int j = 4 * part; j < ncand; j += 4 * split) {
+                const uint4 k4 = *reinterpret_cast<const uint4 *>(all + j);
+                place += k4.x > key || (k4.x == key && j < self);
+                place += k4.y > key || (k4.y == key && j + 1 < self);
+                place += k4.z > key || (k4.z == key && j + 2 < self);
+                place += k4.w > key || (k4.w == key && j + 3 < self);
+            }
+            if (split > 1) atomicAdd(&sh.ranked[mine], place);
+            else sh.ranked[mine] = place;
+        }
+        __syncthreads();
+        if (warp * 32 < have) {
+            const bool is = warp * 32 + lane < have && sh.ranked[warp * 32 + lane] < static_cast<uint32_t>(want);
+            const uint32_t votes = __ballot_sync(0xffffffffu, is);
+            if (lane < ranks) {
                 if (ranks > 1)
-                    st_cluster_u32(smem_addr(&sh.bits[i / 32]), lane, votes);
+                    st_cluster_u32(smem_addr(&sh.bits[c0 / 32 + warp]), lane, votes);
                 else
-                    sh.bits[i / 32] = votes;
+                    sh.bits[warp] = votes;
             }
         }
         sync_all();
+        // each page's place in the list: those taken in the words before its own
         int32_t *list = reinterpret_cast<int32_t *>(sh.hist[1]);
-        for (int i = tid; i < ncand; i += kSelThreads) {
-            const uint32_t word = sh.bits[i / 32];
-            if (word >> (i & 31) & 1u) {
-                int at = a.sink + __popc(word & ((1u << (i & 31)) - 1u));
-                for (int w = 0; w < i / 32; ++w) at += __popc(sh.bits[w]);
-                list[at] = a.sink + i;
-                if (rank == 0) out[at] = a.sink + i;
+        const int words = (ncand + 31) / 32;
+        const int in_word = lane < words ? __popc(sh.bits[lane]) : 0;
+        int upto = in_word;
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += o;
+        }
+        for (int w = warp; w < words; w += kSelWarps) {
+            const uint32_t word = sh.bits[w];
+            const int before = __shfl_sync(0xffffffffu, upto - in_word, w);
+            if (word >> lane & 1u) {
+                const int at = a.sink + before + __popc(word & ((1u << lane) - 1u));
+                const int page = a.sink + 32 * w + lane;
+                list[at] = page;
+                if (rank == 0) out[at] = page;
             }
         }
         for (int i = tid; i < a.sink; i += kSelThreads) list[i] = i;
