@@ -16,6 +16,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_sparse_select.cuh"
 
@@ -41,9 +42,10 @@ struct Args {
 };
 
 pa_status launch_chosen(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
-                        int num_rows, int splits, cudaStream_t stream);
+                        int num_rows, int splits, int warps, cudaStream_t stream);
 
-// CTAs to an SM, as the registers and the ring allow.
+// CTAs of four warps to an SM, as the registers and the ring allow; half as
+// many of eight warps.
 constexpr int resident_ctas(int head_dim, int block_size, bool fp8, int group) {
     const bool big = block_size == 32 && !fp8;  // pages twice the others' size
     if (group <= 8) return big ? 3 : 4;
@@ -106,7 +108,7 @@ __device__ __forceinline__ int longest_row(const int32_t *lens, int n, int z, vo
 
 // CHOOSE: the cluster first chooses the row's pages, in the ring's memory.
 template <int D, int BS, bool FP8, int NT, int NW, int SPW, bool CHOOSE>
-__global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8))
+__global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4 / NW)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const Args a) {
     using C = Shape<D, BS, FP8, NT, NW, SPW>;
@@ -628,8 +630,6 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8))
 // host side
 // ---------------------------------------------------------------------------
 
-constexpr int kWarps = 4;
-
 // Steps of a warp's ring.  Up to 8 query heads at head dim 128 one step, 32 KB
 // to a CTA and four CTAs to an SM, against two steps and three CTAs: 113 and 117
 // us over 64 sequences of 4K-32K tokens, 60 and 63 with E4M3 pages (512 clusters
@@ -642,32 +642,32 @@ constexpr int stages_per_warp() {
     if (NT == 1) return 1;
     constexpr int ppi = (FP8 && BS == 16) ? 2 : 1;
     constexpr int stage = 2 * ppi * BS * D * (FP8 ? 1 : 2);
-    constexpr int spw = (BS == 16 && !FP8 ? 64 : 96) * 1024 / (kWarps * stage);
+    constexpr int spw = (BS == 16 && !FP8 ? 64 : 96) * 1024 / (4 * stage);
     return spw < 1 ? 1 : spw;
 }
 
-template <int D, int BS, bool FP8, int NT, bool CHOOSE>
+template <int D, int BS, bool FP8, int NT, int NW, bool CHOOSE>
 static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a0, int num_rows,
                                int splits, cudaStream_t stream) {
     constexpr int SPW = stages_per_warp<D, BS, FP8, NT>();
-    using C = Shape<D, BS, FP8, NT, kWarps, SPW>;
+    using C = Shape<D, BS, FP8, NT, NW, SPW>;
     // The choice works where the ring will be: copies of bounds, then keys.  Long
     // shares take more shared memory than the ring.
     Args a = a0;
     int smem = C::SMEM;
     if constexpr (CHOOSE) {
         const int keys = key_bytes(a.select.max_blocks, splits);
-        a.select.stages = copy_bytes(kWarps * 32, D, kMaxStages) + keys <= C::SMEM - 1024 ? kMaxStages : 2;
-        smem = std::max(smem, 1024 + copy_bytes(kWarps * 32, D, a.select.stages) + keys);
+        a.select.stages = copy_bytes(NW * 32, D, kMaxStages) + keys <= C::SMEM - 1024 ? kMaxStages : 2;
+        smem = std::max(smem, 1024 + copy_bytes(NW * 32, D, a.select.stages) + keys);
     }
-    constexpr int kMostSmem = CHOOSE ? std::max(C::SMEM, 1024 + copy_bytes(kWarps * 32, D, 2) + (kMaxKeys + 4) * 4) : C::SMEM;
-    auto kern = attend_kernel<D, BS, FP8, NT, kWarps, SPW, CHOOSE>;
+    constexpr int kMostSmem = CHOOSE ? std::max(C::SMEM, 1024 + copy_bytes(NW * 32, D, 2) + (kMaxKeys + 4) * 4) : C::SMEM;
+    auto kern = attend_kernel<D, BS, FP8, NT, NW, SPW, CHOOSE>;
     static std::atomic<uint64_t> raised{0};
     pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), kMostSmem, raised);
     if (st != PA_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, a.num_kv_heads, num_rows);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -680,25 +680,29 @@ static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, con
     return cuda_check(cudaLaunchKernelEx(&cfg, kern, tk, tv, a), "sparse decode launch");
 }
 
-template <int D, int BS, bool CHOOSE>
-static pa_status launch_shape(bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
-                              int num_rows, int splits, cudaStream_t stream) {
-    if (fp8)
-        return a.group <= 8 ? launch_attend<D, BS, true, 1, CHOOSE>(tk, tv, a, num_rows, splits, stream)
-                            : launch_attend<D, BS, true, 2, CHOOSE>(tk, tv, a, num_rows, splits, stream);
-    return a.group <= 8 ? launch_attend<D, BS, false, 1, CHOOSE>(tk, tv, a, num_rows, splits, stream)
-                        : launch_attend<D, BS, false, 2, CHOOSE>(tk, tv, a, num_rows, splits, stream);
+// Eight warps to a CTA: only for the kernel that chooses, up to 8 query heads.
+template <int D, int BS, bool FP8, bool CHOOSE>
+static pa_status launch_group(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int num_rows, int splits,
+                              int warps, cudaStream_t stream) {
+    if (a.group > 8) return launch_attend<D, BS, FP8, 2, 4, CHOOSE>(tk, tv, a, num_rows, splits, stream);
+    if constexpr (CHOOSE)
+        if (warps == 8) return launch_attend<D, BS, FP8, 1, 8, CHOOSE>(tk, tv, a, num_rows, splits, stream);
+    return launch_attend<D, BS, FP8, 1, 4, CHOOSE>(tk, tv, a, num_rows, splits, stream);
 }
-
 
 template <bool CHOOSE>
 static pa_status launch_any(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv,
-                            const Args &a, int num_rows, int splits, cudaStream_t stream) {
-    if (head_dim == 128)
-        return block_size == 16 ? launch_shape<128, 16, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream)
-                                : launch_shape<128, 32, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream);
-    return block_size == 16 ? launch_shape<64, 16, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream)
-                            : launch_shape<64, 32, CHOOSE>(fp8, tk, tv, a, num_rows, splits, stream);
+                            const Args &a, int num_rows, int splits, int warps, cudaStream_t stream) {
+    auto shape = [&](auto d, auto bs) {
+        return fp8 ? launch_group<d.value, bs.value, true, CHOOSE>(tk, tv, a, num_rows, splits, warps, stream)
+                   : launch_group<d.value, bs.value, false, CHOOSE>(tk, tv, a, num_rows, splits, warps, stream);
+    };
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    using I16 = std::integral_constant<int, 16>;
+    using I32 = std::integral_constant<int, 32>;
+    if (head_dim == 128) return block_size == 16 ? shape(I128{}, I16{}) : shape(I128{}, I32{});
+    return block_size == 16 ? shape(I64{}, I16{}) : shape(I64{}, I32{});
 }
 
 }  // namespace sparse

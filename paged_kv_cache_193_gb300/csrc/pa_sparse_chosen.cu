@@ -6,8 +6,8 @@ namespace pa {
 namespace sparse {
 
 pa_status launch_chosen(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
-                        int num_rows, int splits, cudaStream_t stream) {
-    return launch_any<true>(head_dim, block_size, fp8, tk, tv, a, num_rows, splits, stream);
+                        int num_rows, int splits, int warps, cudaStream_t stream) {
+    return launch_any<true>(head_dim, block_size, fp8, tk, tv, a, num_rows, splits, warps, stream);
 }
 
 }  // namespace sparse

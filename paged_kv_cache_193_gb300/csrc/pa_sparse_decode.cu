@@ -42,14 +42,49 @@ static pa_status check_pointers(const Call &c) {
     return PA_OK;
 }
 
-// CTAs to a (row, KV head)'s list: the most whose clusters are all resident at
-// once (an eighth of the CTAs' places is kept back: clusters of three, six or
-// eight leave some of a GPC's places empty) and whose warps have a page each.
-static int splits_for(int64_t rows, int top_k, int resident) {
+// How a (row, KV head)'s pages are shared out.
+struct Launch {
+    int warps;   // to a CTA
+    int splits;  // CTAs to a cluster
+    bool longest_first;
+};
+
+// Four warps to a CTA: the most CTAs whose clusters are all resident at once and
+// whose warps have a page each.  An eighth of the CTAs' places is kept back:
+// clusters of three, six or eight leave some of a GPC's places empty (8 rows of
+// 8 heads, 16 queries each, 128K tokens: 62 us with 6, 68 with 4, 87 with 8).
+static int splits_of_four_warps(int64_t rows, int pages, int resident) {
     int splits = 1;
     for (int s : {2, 3, 4, 6, 8})
-        if (rows * s <= resident * kSms * 7 / 8 && top_k >= kWarps * s) splits = s;
+        if (rows * s <= resident * kSms * 7 / 8 && pages >= 4 * s) splits = s;
     return splits;
+}
+
+// The kernel that chooses takes CTAs of eight warps while a CTA for every row
+// and KV head is resident (up to 8 query heads): half the cluster for the same
+// warps, and most of a choice's steps are waits for the whole cluster.
+// Measured, 4 against 8 warps, each at its best: 8 rows of 128K tokens 30 and 24
+// us, 64 of 128K 58 and 56, 256 of 1K-8K 33 and 30, 272 at head dim 64 16 and 14.
+// Clusters of three and six of them, and of eight beyond half of the places,
+// measured slower than the next smaller size (32 of 8K: 18 us with 8, 15 with 4).
+static Launch chosen_launch(const Call &c, int group, int resident) {
+    const int64_t rows = static_cast<int64_t>(c.num_rows) * c.num_kv_heads;
+    Launch l{4, 1, false};
+    int places = resident;
+    if (group <= 8 && rows <= resident / 2 * kSms) {
+        l.warps = 8;
+        places = resident / 2;
+        const int pages = std::max(c.top_k, c.max_blocks / 4);
+        for (int s : {2, 4, 8})
+            if (rows * s <= (s == 8 ? places * kSms / 2 : places * kSms * 7 / 8) && pages >= 8 * s) l.splits = s;
+    } else {
+        l.splits = splits_of_four_warps(rows, c.top_k, resident);
+    }
+    while (c.max_blocks > kMaxKeys * l.splits) ++l.splits;  // at most 8, by the limit on the table
+    // With more CTAs than places, and rows that few threads can sort, the longest
+    // go first (64 rows of 8 heads, 4K-32K tokens: 118 us, 130 in their order).
+    l.longest_first = c.num_rows > 1 && c.num_rows <= kMaxSorted && rows * l.splits > places * kSms;
+    return l;
 }
 
 // `select`: choose the pages in the same kernel; otherwise the list is there.
@@ -87,15 +122,12 @@ static pa_status run_attend(const Call &c, const SelectArgs *select, cudaStream_
     const int resident = resident_ctas(c.head_dim, c.block_size, fp8, a.group);
     if (select) {
         a.select = *select;
-        a.longest_first = 0;
-        int splits = splits_for(rows, c.top_k, resident);
-        while (c.max_blocks > kMaxKeys * splits) ++splits;  // at most 8, by the limit on the table
-        // With more CTAs than places, and rows that few threads can sort
-        a.longest_first = c.num_rows > 1 && c.num_rows <= kMaxSorted && rows * splits > resident * kSms;
-        return launch_chosen(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, stream);
+        const Launch l = chosen_launch(c, a.group, resident);
+        a.longest_first = l.longest_first;
+        return launch_chosen(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, l.splits, l.warps, stream);
     }
-    const int splits = c.splits ? c.splits : splits_for(rows, c.top_k, resident);
-    return launch_any<false>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, stream);
+    const int splits = c.splits ? c.splits : splits_of_four_warps(rows, c.top_k, resident);
+    return launch_any<false>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, 4, stream);
 }
 
 }  // namespace sparse
