@@ -138,8 +138,9 @@ inline int key_bytes(int max_blocks, int ranks) { return ((((max_blocks + ranks 
 // last page to be taken, and, once few keys are left in the bin, their ranks
 // among one another; of few candidates, their ranks at once.
 //
-// `copies` is copy_bytes() of shared memory (16-byte aligned), `keys` key_bytes().  Every thread of the cluster calls it; on return the
-// listed pages are visible to all of them.
+// `copies` is copy_bytes() of shared memory (16-byte aligned), `keys`
+// key_bytes().  Every thread of the cluster calls it; on return the listed pages
+// are visible to all of them.
 template <int D, int NT, int kSelThreads>
 __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, uint32_t *keys, Choice<D, NT, kSelThreads> &sh,
                                          int rank, int ranks, int h, int t) {

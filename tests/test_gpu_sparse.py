@@ -496,6 +496,40 @@ def test_a_long_table(api, cuda_device):
     assert (np.abs(f64(out) - ref) <= bound).all()
 
 
+def test_a_cache_past_32_bits(api, cuda_device):
+    """Pages whose bytes and elements lie past 2^32, at the end of an 8.6 GB E4M3 cache."""
+    NB, Hkv, B, D = 2 ** 18, 16, 16, 128
+    assert NB * Hkv * B * D > 2 ** 32
+    g = torch.Generator().manual_seed(31)
+    kc, vc = (torch.zeros(NB, Hkv, B, D, dtype=torch.uint8, device=cuda_device) for _ in range(2))
+    s, e = api.alloc_block_summary(kc)
+    n = 10 * B
+    blocks = torch.tensor([NB - 1, 5, NB - 3, NB - 2, 9, NB - 200, 0, NB - 77, NB - 4, NB - 5], dtype=torch.int32)
+    slots = (blocks[:, None] * B + torch.arange(B)).flatten().to(torch.int32).to(cuda_device)
+    q, k, v = (torch.randn(n, h, D, generator=g).to(torch.bfloat16).to(cuda_device) for h in (Hkv, Hkv, Hkv))
+    pos = torch.arange(n, dtype=torch.int32, device=cuda_device)
+    freq = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).to(cuda_device)
+    rq = api.rope_append(q, k, v, pos, freq, slots, kc, vc, kv_scale=1 / 32)
+    api.block_summary(kc, slots, s, e)
+    used = blocks.long().to(cuda_device)
+    small = [t[used].clone() for t in (kc, vc, s, e)]
+    # the same tokens in a cache of ten pages
+    k2, v2 = torch.zeros_like(small[0]), torch.zeros_like(small[1])
+    s2, e2 = api.alloc_block_summary(k2)
+    slots2 = torch.arange(n, dtype=torch.int32, device=cuda_device)
+    assert torch.equal(rq, api.rope_append(q, k, v, pos, freq, slots2, k2, v2, kv_scale=1 / 32))
+    api.block_summary(k2, slots2, s2, e2)
+    for big, want in zip(small, (k2, v2, s2, e2)):
+        assert torch.equal(big, want)
+    assert int((kc[NB - 300:] != 0).any(-1).any(-1).any(-1).sum()) == 7
+    lens = torch.tensor([n], dtype=torch.int32, device=cuda_device)
+    last = rq[-1:].contiguous()
+    far = api.sparse_attend(last, kc, vc, s, e, blocks[None].to(cuda_device), lens, 6, kv_scale=1 / 32)
+    near = api.sparse_attend(last, k2, v2, s2, e2, torch.arange(10, dtype=torch.int32, device=cuda_device)[None], lens, 6,
+                             kv_scale=1 / 32)
+    assert torch.equal(far, near) and far.isfinite().all() and api.device_errors() == 0
+
+
 # ---- the operators as they are used together ------------------------------------
 
 def _decode_loop(api, device, step_of, steps, S=3, Hq=8, Hkv=2, D=128, B=16, top_k=6, fp8=False):
