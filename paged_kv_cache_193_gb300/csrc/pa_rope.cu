@@ -17,7 +17,7 @@
 // Bound: memory.  Every q, k, v element is read once and written once.
 #include <algorithm>
 
-#include "pa_device.cuh"
+#include "pa_launch.cuh"
 
 namespace pa {
 namespace rope {
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const Args a) {
     constexpr int VPR = D / 16;  // threads to a row
     __shared__ __align__(16) float cs[kMaxTile][D / 2], sn[kMaxTile][D / 2];
     __shared__ int32_t slot_s[kMaxTile];
+    dependent_begin();
     const int t0 = blockIdx.x * a.tile;
     const int live = min(a.tile, a.num_tokens - t0);
 
@@ -209,11 +210,9 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const Args a) {
 }
 
 template <int D, bool FP8>
-static void launch(const Args &a, bool adjacent, dim3 grid, cudaStream_t stream) {
-    if (adjacent)
-        append_kernel<D, FP8, true><<<grid, kThreads, 0, stream>>>(a);
-    else
-        append_kernel<D, FP8, false><<<grid, kThreads, 0, stream>>>(a);
+static cudaError_t launch(const Args &a, bool adjacent, dim3 grid, cudaStream_t stream) {
+    return adjacent ? launch_dependent(append_kernel<D, FP8, true>, grid, kThreads, 0, 0, stream, a)
+                    : launch_dependent(append_kernel<D, FP8, false>, grid, kThreads, 0, 0, stream, a);
 }
 
 static bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
@@ -322,12 +321,10 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
     const int shares = std::max(1, std::min((rows + at_once - 1) / at_once, 4 * 152 / num_tokens));
     a.rows_per_y = (rows + shares - 1) / shares;
     const dim3 grid((num_tokens + a.tile - 1) / a.tile, (rows + a.rows_per_y - 1) / a.rows_per_y);
-    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
-    if (head_dim == 128)
-        fp8 ? rope::launch<128, true>(a, adjacent != 0, grid, stream)
-            : rope::launch<128, false>(a, adjacent != 0, grid, stream);
-    else
-        fp8 ? rope::launch<64, true>(a, adjacent != 0, grid, stream)
-            : rope::launch<64, false>(a, adjacent != 0, grid, stream);
-    return cuda_check(cudaGetLastError(), "rope append launch");
+    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3, adj = adjacent != 0;
+    const cudaError_t e = head_dim == 128 ? (fp8 ? rope::launch<128, true>(a, adj, grid, stream)
+                                                 : rope::launch<128, false>(a, adj, grid, stream))
+                                          : (fp8 ? rope::launch<64, true>(a, adj, grid, stream)
+                                                 : rope::launch<64, false>(a, adj, grid, stream));
+    return cuda_check(e, "rope append launch");
 }

@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kSummaryWarps * 32) summary_kernel(const Summa
     constexpr int PAIRS = EPL / 2;
     auto pair = [](uint32_t w) { return *reinterpret_cast<const T *>(&w); };
     auto bits = [](const T &x) { return *reinterpret_cast<const uint32_t *>(&x); };
+    dependent_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int token = blockIdx.x * kSummarySlots + lane;
     int32_t slot = lane < kSummarySlots && token < a.num_tokens ? a.slots[token] : -1;
@@ -152,6 +153,7 @@ template <int D, int NT, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads, (NT == 2 ? 384 : 512) / kSelThreads) select_kernel(const SelectArgs a) {
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) Choice<D, NT, kSelThreads> sh;
+    dependent_begin();
     choose<D, NT, kSelThreads>(a, dyn, reinterpret_cast<uint32_t *>(dyn + copy_bytes(kSelThreads, D, a.stages)), sh,
                                static_cast<int>(cluster_rank()), static_cast<int>(cluster_size()), blockIdx.y, blockIdx.z);
 }
@@ -167,19 +169,9 @@ static pa_status launch_threads(SelectArgs a, int num_rows, cudaStream_t stream)
     const int copies = copy_bytes(kSelThreads, D, kMaxStages);
     pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), copies + key_bytes(kMaxKeys, 1), raised);
     if (st != PA_OK) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranks, a.num_kv_heads, num_rows);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = copies + key_bytes(a.max_blocks, ranks);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_check(cudaLaunchKernelEx(&cfg, kern, a), "sparse select launch");
+    return cuda_check(launch_dependent(kern, dim3(ranks, a.num_kv_heads, num_rows), kSelThreads,
+                                       copies + key_bytes(a.max_blocks, ranks), ranks, stream, a),
+                      "sparse select launch");
 }
 
 template <int D, int NT>
@@ -254,11 +246,9 @@ pa_status run_select(const SelectArgs &a, int num_rows, int head_dim, cudaStream
 }
 
 template <int D, int BS>
-static void launch_summary(const SummaryArgs &a, bool fp8, unsigned grid, cudaStream_t stream) {
-    if (fp8)
-        summary_kernel<D, BS, true><<<grid, kSummaryWarps * 32, 0, stream>>>(a);
-    else
-        summary_kernel<D, BS, false><<<grid, kSummaryWarps * 32, 0, stream>>>(a);
+static cudaError_t launch_summary(const SummaryArgs &a, bool fp8, unsigned grid, cudaStream_t stream) {
+    return fp8 ? launch_dependent(summary_kernel<D, BS, true>, dim3(grid), kSummaryWarps * 32, 0, 0, stream, a)
+               : launch_dependent(summary_kernel<D, BS, false>, dim3(grid), kSummaryWarps * 32, 0, 0, stream, a);
 }
 
 }  // namespace sparse
@@ -303,13 +293,11 @@ pa_status pa_block_summary(const void *k_cache, const int32_t *slot_mapping, int
     a.err = err;
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
     const unsigned grid = (static_cast<unsigned>(num_tokens) + kSummarySlots - 1) / kSummarySlots;
-    if (head_dim == 128)
-        block_size == 16 ? launch_summary<128, 16>(a, fp8, grid, stream)
-                         : launch_summary<128, 32>(a, fp8, grid, stream);
-    else
-        block_size == 16 ? launch_summary<64, 16>(a, fp8, grid, stream)
-                         : launch_summary<64, 32>(a, fp8, grid, stream);
-    return cuda_check(cudaGetLastError(), "block summary launch");
+    const cudaError_t e = head_dim == 128 ? (block_size == 16 ? launch_summary<128, 16>(a, fp8, grid, stream)
+                                                              : launch_summary<128, 32>(a, fp8, grid, stream))
+                                          : (block_size == 16 ? launch_summary<64, 16>(a, fp8, grid, stream)
+                                                              : launch_summary<64, 32>(a, fp8, grid, stream));
+    return cuda_check(e, "block summary launch");
 }
 
 pa_status pa_sparse_select(const void *q, const int8_t *summary, const int8_t *exponents,

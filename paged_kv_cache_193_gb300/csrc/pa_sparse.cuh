@@ -4,7 +4,7 @@
 
 #include <atomic>
 
-#include "pa_device.cuh"
+#include "pa_launch.cuh"
 
 namespace pa {
 namespace sparse {

@@ -125,12 +125,6 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     const int r = lane >> 2, c = lane & 3;
     const int h = blockIdx.y;
     int s = blockIdx.z;
-    if constexpr (CHOOSE)
-        if (a.longest_first) s = longest_row(a.context_lens, gridDim.z, s, join);
-
-    const float k_scale = FP8 ? (a.k_scales ? __ldg(a.k_scales + h) : a.kv_scale) : 1.f;
-    const float v_scale = FP8 ? (a.v_scales ? __ldg(a.v_scales + h) : a.kv_scale) : 1.f;
-    const float score_scale = a.softmax_log2 * k_scale;
 
     if (tid == 0) {
 #pragma unroll
@@ -140,6 +134,13 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
+    dependent_begin();
+    if constexpr (CHOOSE)
+        if (a.longest_first) s = longest_row(a.context_lens, gridDim.z, s, join);
+
+    const float k_scale = FP8 ? (a.k_scales ? __ldg(a.k_scales + h) : a.kv_scale) : 1.f;
+    const float v_scale = FP8 ? (a.v_scales ? __ldg(a.v_scales + h) : a.kv_scale) : 1.f;
+    const float score_scale = a.softmax_log2 * k_scale;
 
     Chosen chosen{0, nullptr};
     if constexpr (CHOOSE) {
@@ -665,19 +666,8 @@ static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, con
     static std::atomic<uint64_t> raised{0};
     pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), kMostSmem, raised);
     if (st != PA_OK) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(splits, a.num_kv_heads, num_rows);
-    cfg.blockDim = dim3(NW * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_check(cudaLaunchKernelEx(&cfg, kern, tk, tv, a), "sparse decode launch");
+    return cuda_check(launch_dependent(kern, dim3(splits, a.num_kv_heads, num_rows), NW * 32, smem, splits, stream, tk, tv, a),
+                      "sparse decode launch");
 }
 
 // Eight warps to a CTA: only for the kernel that chooses, up to 8 query heads.
