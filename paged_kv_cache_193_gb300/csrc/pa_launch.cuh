@@ -10,12 +10,12 @@ namespace pa {
 
 // First in a kernel launched by launch_dependent, before any global access, in
 // every thread: waits until the kernel before it on the stream is done and its
-// writes are visible (which that kernel's own wait does for the one before
-// it), and then lets the kernel after this one be put on the SMs.
-__device__ __forceinline__ void dependent_begin() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// writes are visible (as that kernel's own wait does for the one before it).
+__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Once every CTA of the grid has come by here, or has ended, the kernel after
+// this one may be put on the SMs.
+__device__ __forceinline__ void dependent_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // `cluster` CTAs along x to a thread-block cluster (0: none).
 template <class... Params, class... Actual>

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
     constexpr int VPR = D / 16;  // threads to a row
     __shared__ __align__(16) float cs[kMaxTile][D / 2], sn[kMaxTile][D / 2];
     __shared__ int32_t slot_s[kMaxTile];
-    dependent_begin();
+    dependent_wait();
     const int t0 = blockIdx.x * a.tile;
     const int live = min(a.tile, a.num_tokens - t0);
     const int j = threadIdx.x % VPR;
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
             *reinterpret_cast<uint4 *>(to + dst + db) = pack8(xb);
         }
     };
+    dependent_release();
     while (i < total) {
         store();
         i += kThreads / VPR;

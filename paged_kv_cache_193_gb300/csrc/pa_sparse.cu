@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kSummaryWarps * 32) summary_kernel(const Summa
     constexpr int PAIRS = EPL / 2;
     auto pair = [](uint32_t w) { return *reinterpret_cast<const T *>(&w); };
     auto bits = [](const T &x) { return *reinterpret_cast<const uint32_t *>(&x); };
-    dependent_begin();
+    dependent_wait();
+    dependent_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int token = blockIdx.x * kSummarySlots + lane;
     int32_t slot = lane < kSummarySlots && token < a.num_tokens ? a.slots[token] : -1;
@@ -153,7 +154,8 @@ template <int D, int NT, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads, (NT == 2 ? 384 : 512) / kSelThreads) select_kernel(const SelectArgs a) {
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) Choice<D, NT, kSelThreads> sh;
-    dependent_begin();
+    dependent_wait();
+    dependent_release();
     choose<D, NT, kSelThreads>(a, dyn, reinterpret_cast<uint32_t *>(dyn + copy_bytes(kSelThreads, D, a.stages)), sh,
                                static_cast<int>(cluster_rank()), static_cast<int>(cluster_size()), blockIdx.y, blockIdx.z);
 }

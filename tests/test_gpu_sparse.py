@@ -592,3 +592,49 @@ def test_decode_loop_captured(api, cuda_device):
         assert graph.launches() == 4
         return graph.replay
     _decode_loop(api, cuda_device, captured, 20)
+
+
+def test_steps_one_after_the_other_equal_steps_that_wait(api, cuda_device):
+    """A chain of the kernels with nothing between them (each is put on the SMs while the one before still runs), the
+    dense decode and the plain append among them: bit for bit what the same calls give when each is waited for."""
+    g = torch.Generator().manual_seed(41)
+    S, Hq, Hkv, D, B, MB, steps = 6, 16, 4, 128, 16, 40, 40
+    q, k, v = (torch.randn(steps, S, h, D, generator=g).to(torch.bfloat16).to(cuda_device) for h in (Hq, Hkv, Hkv))
+    freq = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).to(cuda_device)
+    tables = torch.randperm(S * MB, generator=g).to(torch.int32).view(S, MB).to(cuda_device)
+    first = torch.tensor([0, 15, 100, 333, 500, 599], dtype=torch.int32, device=cuda_device)
+    start = torch.randn(2, S * MB, Hkv, B, D, generator=g).to(torch.bfloat16).to(cuda_device)
+    full = torch.arange(B - 1, S * MB * B, B, dtype=torch.int32, device=cuda_device)
+
+    def chain(after):
+        kc, vc = start[0].clone(), start[1].clone()
+        lens, pos = first.clone(), first - 1
+        step = api.SparseDecodeStep(kc, vc, tables, lens, pos, freq, Hq, 9)
+        api.block_summary(kc, full, step.summary, step.exponents)
+        got = []
+        for i in range(steps):
+            lens += 1
+            pos += 1
+            after()
+            got.append(step(q[i], k[i], v[i]).clone())
+            after()
+            got.append(api.decode(step.q_rotated, kc, vc, tables, lens, partition_size=128))
+            after()
+            api.cache_append(k[i], v[i], step.slots, kc, vc)  # over the rotated row
+            after()
+            sel, cnt = api.sparse_select(q[i], step.summary, step.exponents, tables, lens, B, 7)
+            after()
+            got.append(api.sparse_decode(q[i], kc, vc, tables, lens, sel, cnt))
+            after()
+            api.rope_append(None, k[i], v[i], pos, freq, step.slots, kc, vc)  # and back
+            after()
+            api.block_summary(kc, step.slots, step.summary, step.exponents)
+            after()
+        return got + [kc, vc, step.summary, step.exponents]
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        got = chain(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert api.device_errors() == 0
