@@ -66,7 +66,8 @@ static int splits_of_four_warps(int64_t rows, int pages, int resident) {
 // Measured, 4 against 8 warps, each at its best: 8 rows of 128K tokens 30 and 24
 // us, 64 of 128K 58 and 56, 256 of 1K-8K 33 and 30, 272 at head dim 64 16 and 14.
 // Clusters of three and six of them, and of eight beyond half of the places,
-// measured slower than the next smaller size (32 of 8K: 18 us with 8, 15 with 4).
+// measured slower than the next smaller size (32 of 8K: 18 us with 8, 15 with 4),
+// clusters of sixteen slower than of eight (8 rows of 128K: 30 us, 24 with eight).
 static Launch chosen_launch(const Call &c, int group, int resident) {
     const int64_t rows = static_cast<int64_t>(c.num_rows) * c.num_kv_heads;
     Launch l{4, 1, false};

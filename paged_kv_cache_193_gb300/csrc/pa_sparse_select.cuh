@@ -101,7 +101,9 @@ struct alignas(16) Choice {
 };
 
 // Up to this many candidates, no more than one to a thread, are ranked one
-// against another with no histogram: a cluster's histograms cost five barriers.
+// against another with no histogram, which costs a cluster five barriers (8 rows
+// of 313 pages, 8 CTAs each, choice and attention: 14.3 us with it, 12.4 without;
+// but 17 with half a thousand keys for each thread to look at).
 constexpr int kFew = 500;
 
 // What a row attends to: `count` logical pages, listed, or the first ones when
