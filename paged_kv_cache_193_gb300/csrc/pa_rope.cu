@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
 }
 
 // Grids of several waves want a fifth CTA on each SM (8192 tokens, 32 + 8 heads:
-// 35 against 39 us), others the registers (1000 tokens 5.6 against 6.5 us, 256
-// with an E4M3 cache 4.1 against 4.7).
+// 35 against 39 us), others the registers (1000 tokens 5.6 against 6.4 us, 256
+// with an E4M3 cache 3.9 against 4.7).
 template <int D, bool FP8, bool ADJACENT>
 static cudaError_t launch_ctas(const Args &a, dim3 grid, cudaStream_t stream) {
     const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y;

@@ -164,8 +164,8 @@ template <int D, int NT, int kSelThreads>
 static pa_status launch_threads(SelectArgs a, int num_rows, cudaStream_t stream) {
     a.stages = kMaxStages;
     // A cluster for a row while that leaves half of the SMs to others' and each
-    // CTA some 512 pages: 64 rows of 8192 pages take 45 us with two CTAs of 256
-    // threads, 73 with one, 53 with four.
+    // CTA some 512 pages: 64 rows of 8192 pages take 40 us with two CTAs of 256
+    // threads, 67 with one, 48 with four.
     const int64_t rows = static_cast<int64_t>(num_rows) * a.num_kv_heads;
     int ranks = 1;
     while (ranks < 8 && ((2 * rows * ranks <= kSms && a.max_blocks > 512 * ranks) || a.max_blocks > kMaxKeys * ranks)) ranks *= 2;
@@ -181,8 +181,8 @@ static pa_status launch_threads(SelectArgs a, int num_rows, cudaStream_t stream)
 
 template <int D, int NT>
 static pa_status launch_select(const SelectArgs &a, int num_rows, cudaStream_t stream) {
-    // 272 rows of 560 pages: 8.9 us with 256 threads, 9.3 with 128; 2048 rows of 128
-    // pages: 44 and 27.
+    // 272 rows of up to 560 pages: 10.0 us with 256 threads, 10.5 with 128; 2048 rows
+    // of up to 128 pages: 39 and 27.
     const bool few = static_cast<int64_t>(num_rows) * a.num_kv_heads < 2 * kSms;
     return few ? launch_threads<D, NT, 256>(a, num_rows, stream) : launch_threads<D, NT, 128>(a, num_rows, stream);
 }

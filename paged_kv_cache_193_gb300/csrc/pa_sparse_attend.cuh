@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     }
 
     // Not earlier: the next kernel's CTAs would take the places of this one's
-    // (64 sequences of 4K-32K tokens: 116 us a pass with it at the start, 112 here).
+    // (64 sequences of 4K-32K tokens: 114.7 us a pass with it at the start, 113.4
+    // here; in E4M3 62.1 and 61.0).
     dependent_release();
 
     // ---- join the warps ---------------------------------------------------------
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
 // ---------------------------------------------------------------------------
 
 // Steps of a warp's ring.  Up to 8 query heads at head dim 128 one step, 32 KB
-// to a CTA and four CTAs to an SM, against two steps and three CTAs: 113 and 117
+// to a CTA and four CTAs to an SM, against two steps and three CTAs: 112 and 116
 // us over 64 sequences of 4K-32K tokens, 60 and 63 with E4M3 pages (512 clusters
 // of one CTA: four to an SM have places for all of them).  Groups above 8 need
 // so many registers that fewer CTAs fit, and take the memory: 64 KB for three

@@ -52,7 +52,7 @@ struct Launch {
 // Four warps to a CTA: the most CTAs whose clusters are all resident at once and
 // whose warps have a page each.  An eighth of the CTAs' places is kept back:
 // clusters of three, six or eight leave some of a GPC's places empty (8 rows of
-// 8 heads, 16 queries each, 128K tokens: 62 us with 6, 68 with 4, 87 with 8).
+// 8 heads, 16 queries each, 128K tokens: 62 us with 6, 71 with 4, 85 with 8).
 static int splits_of_four_warps(int64_t rows, int pages, int resident) {
     int splits = 1;
     for (int s : {2, 3, 4, 6, 8})
@@ -63,8 +63,8 @@ static int splits_of_four_warps(int64_t rows, int pages, int resident) {
 // The kernel that chooses takes CTAs of eight warps while a CTA for every row
 // and KV head is resident (up to 8 query heads): half the cluster for the same
 // warps, and most of a choice's steps are waits for the whole cluster.
-// Measured, 4 against 8 warps, each at its best: 8 rows of 128K tokens 30 and 24
-// us, 64 of 128K 58 and 56, 256 of 1K-8K 33 and 30, 272 at head dim 64 16 and 14.
+// Measured, 4 against 8 warps, each at its best: 8 rows of 128K tokens 30 and 23
+// us, 64 of 128K 57 and 55, 256 of 1K-8K 33 and 30, 272 at head dim 64 16 and 14.
 // Clusters of three and six of them, and of eight beyond half of the places,
 // measured slower than the next smaller size (32 of 8K: 18 us with 8, 15 with 4),
 // clusters of sixteen slower than of eight (8 rows of 128K: 30 us, 24 with eight).
@@ -82,9 +82,13 @@ static Launch chosen_launch(const Call &c, int group, int resident) {
         l.splits = splits_of_four_warps(rows, c.top_k, resident);
     }
     while (c.max_blocks > kMaxKeys * l.splits) ++l.splits;  // at most 8, by the limit on the table
-    // With more CTAs than places, and rows that few threads can sort, the longest
-    // go first (64 rows of 8 heads, 4K-32K tokens: 118 us, 130 in their order).
-    l.longest_first = c.num_rows > 1 && c.num_rows <= kMaxSorted && rows * l.splits > places * kSms;
+    // With a few more CTAs than places, and rows that few threads can sort, the
+    // longest go first, so that the last to start are the shortest (80 rows of 8
+    // heads, 2K-32K tokens, 640 CTAs on 608 places: 144 us, 159 in their order; 512
+    // of 16 query heads on 456: 72 and 76).  With more, rows in any order spread
+    // the choices over the time better (800 on 608, E4M3: 87 us, 92 longest first).
+    const int64_t ctas = rows * l.splits, room = static_cast<int64_t>(places) * kSms;
+    l.longest_first = c.num_rows > 1 && c.num_rows <= kMaxSorted && ctas > room && ctas <= room + room / 4;
     return l;
 }
 

@@ -410,11 +410,11 @@ def test_every_number_of_ctas_to_a_row(api, cuda_device, G, S):
     assert api.device_errors() == 0
 
 
-@pytest.mark.parametrize("Hkv", [5, 9])
-def test_rows_taken_by_length(api, cuda_device, Hkv):
-    """More clusters than places with 128 rows or fewer: the rows are taken longest first, equal ones in their order."""
-    lens = ([700, 16, 700, 0, 33] * 26)[:128]
-    case = Case(cuda_device, lens, Hkv, Hkv, D=64)
+@pytest.mark.parametrize("S,Hkv", [(125, 5), (70, 9), (128, 5), (128, 9)])
+def test_rows_taken_by_length(api, cuda_device, S, Hkv):
+    """A few more clusters than places with 128 rows or fewer: the rows are taken longest first, equal ones in their
+    order; with many more, in the order given."""
+    case = Case(cuda_device, ([700, 16, 700, 0, 33] * 26)[:S], Hkv, Hkv, D=64)
     s, e = case.summaries(api)
     sel, cnt, out = case.attend(api, s, e, 8)
     want_sel, want_cnt = R.select(f64(case.q), s.cpu().numpy(), e.cpu().numpy(), case.tables, case.lens, 16, 8, 1, 2)
