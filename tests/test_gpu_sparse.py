@@ -638,3 +638,41 @@ def test_steps_one_after_the_other_equal_steps_that_wait(api, cuda_device):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert api.device_errors() == 0
+
+
+def test_captured_behind_copies_joins_and_other_kernels(api, cuda_device):
+    """In one graph: behind a memory copy, behind a memset, behind two streams that join, and with a branch after."""
+    case = Case(cuda_device, [900, 41, 300], 8, 2)
+    s, e = case.summaries(api)
+    want = api.sparse_attend(case.q, case.kc, case.vc, s, e, case.bt, case.cl, 9)
+    other = api.decode(case.q, case.kc, case.vc, case.bt, case.cl, case.scale)
+    full = [case.tables[i, j] * 16 + 15 for i, n in enumerate(case.lens) for j in range(n // 16)]
+    full = torch.tensor(full, dtype=torch.int32, device=cuda_device)
+    q, s2, e2 = torch.zeros_like(case.q), torch.zeros_like(s), torch.zeros_like(e)
+    sel, cnt = torch.zeros(3, 2, 9, dtype=torch.int32, device=cuda_device), torch.zeros(3, 2, dtype=torch.int32, device=cuda_device)
+    outs = [torch.zeros_like(case.q) for _ in range(3)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        q.zero_()
+        q.copy_(case.q)                                    # a copy, then a kernel of ours
+        api.sparse_attend(q, case.kc, case.vc, s, e, case.bt, case.cl, 9, selected=sel, counts=cnt, out=outs[0])
+        side.wait_stream(main)
+        s2.zero_()
+        with torch.cuda.stream(side):
+            api.block_summary(case.kc, full, s2, e2)       # on its own branch, after the attention
+            api.decode(q, case.kc, case.vc, case.bt, case.cl, case.scale, out=outs[2])
+        main.wait_stream(side)                             # the join, then a kernel of ours
+        api.block_summary(case.kc, full, s2, e2)
+        api.sparse_attend(q, case.kc, case.vc, s2, e2, case.bt, case.cl, 9, selected=sel, counts=cnt, out=outs[1])
+    for _ in range(5):
+        for t in (q, s2, e2, *outs):
+            t.fill_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and torch.equal(outs[2], other)
+        done = full.long() // 16  # the others' exponents are left as they were: filled above
+        assert torch.equal(s2, s) and torch.equal(e2[done], e[done])
+    assert api.device_errors() == 0
