@@ -11,6 +11,12 @@
 // softmax, O^T += V^T P^T.  The CTA's warps, then the cluster's CTAs over
 // distributed shared memory, join their (max, sum, accumulator) triples, so
 // there is no workspace and no second kernel however few rows there are.
+//
+// Bound by memory: a page is read once and used for all queries of its KV head.
+// 64 sequences of 4K-32K tokens, 64 / 8 heads, top 128: 689 MB in 112 us with the
+// choice, 6.1 TB/s (0.90 of a copy's rate); 256 sequences of 512-2,048 tokens, top
+// 32: 575 MB in 99.6 us, 5.8 TB/s.  With few rows by latency: one sequence of
+// 5,003 tokens, top 64, 10.2 us.
 #pragma once
 
 #include <cudaTypedefs.h>

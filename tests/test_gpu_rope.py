@@ -215,3 +215,29 @@ def test_rotated_attention_depends_on_differences_of_positions(api, cuda_device)
         outs.append(api.decode(rq[-1:].contiguous(), kc, vc, tables, torch.tensor([T], dtype=torch.int32, device=cuda_device)).float())
     # scores move by the bf16 roundings of q and k: 2 * 2^-8 |q||k| / sqrt(D) in the worst direction, |q||k| about D
     assert (outs[0] - outs[1]).abs().max() <= 2 * 2 * 2.0 ** -8 * D ** 0.5 * v.float().abs().max()
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.03, 1 / 448, 0.6250001, 1.9999999, 3.0, 1e-3, 7e-18, 9e17, 1e-20, 1e25, 1e-40, 3e38])
+def test_every_value_into_an_e4m3_cache(api, oracle, cuda_device, scale):
+    """All 65,536 bf16 values as V and as unrotated K (position 0 turns nothing): the codes of the plain append, which
+    divides.  NaN only has to stay NaN."""
+    D, Hkv = 128, 2
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(-1, Hkv, D)
+    T = bits.shape[0]
+    x = bits.to(cuda_device)
+    kc, vc = (torch.zeros(T // 16, Hkv, 16, D, dtype=torch.uint8, device=cuda_device) for _ in range(2))
+    k2, v2 = torch.zeros_like(kc), torch.zeros_like(vc)
+    slots = torch.arange(T, dtype=torch.int32, device=cuda_device)
+    zero = torch.zeros(T, dtype=torch.int32, device=cuda_device)
+    freq = torch.ones(16, dtype=torch.float64, device=cuda_device)
+    # elements from 32 on are not rotated at all
+    api.rope_append(None, x, x, zero, freq, slots, kc, vc, kv_scale=scale)
+    api.cache_append(x, x, slots, k2, v2, scale)
+    nan = lambda c: (c & 0x7F) == 0x7F  # noqa: E731
+    assert torch.equal(nan(vc), nan(v2)) and torch.equal(vc[~nan(v2)], v2[~nan(v2)])
+    kr, kw = kc[..., 32:], k2[..., 32:]
+    assert torch.equal(nan(kr), nan(kw)) and torch.equal(kr[~nan(kw)], kw[~nan(kw)])
+    per_head = torch.full((Hkv,), scale, device=cuda_device)
+    v3 = torch.zeros_like(vc)
+    api.rope_append(None, x, x, zero, freq, slots, torch.zeros_like(kc), v3, k_scales=per_head, v_scales=per_head)
+    assert torch.equal(v3, vc)
