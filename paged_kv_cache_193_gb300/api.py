@@ -488,6 +488,18 @@ class DecodeStep:
 # rotate-and-append, page bounds, block-sparse decode
 # ---------------------------------------------------------------------------
 
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor for a kernel on ``stream``: of that stream's
+    own memory, which work pending on the current stream cannot still be
+    using, nor work launched there later reuse before the kernel has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
                 inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
                 v_cache: torch.Tensor, pair_axis: torch.Tensor | None = None, adjacent: bool = False,
@@ -505,7 +517,7 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positi
     A negative slot writes nothing for its token.  Returns the rotated q,
     bf16 [T, Hq, D] (``out``; may be a dense ``q`` itself)."""
     if out is None and isinstance(q, torch.Tensor):
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     status = _lib.binding().rope_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, pair_axis,
                                         adjacent, magnitude, kv_scale, k_scales, v_scales, out, stream)
     if status is not None:
@@ -530,11 +542,11 @@ def block_summary(k_cache: torch.Tensor, slot_mapping: torch.Tensor, summary: to
         _check(status)
 
 
-def _choice(q, Hkv, top_k, selected, counts):
+def _choice(q, Hkv, top_k, selected, counts, stream):
     if selected is None:
-        selected = torch.empty(q.shape[0], Hkv, top_k, dtype=torch.int32, device=q.device)
+        selected = _empty((q.shape[0], Hkv, top_k), torch.int32, q.device, stream)
     if counts is None:
-        counts = torch.empty(q.shape[0], Hkv, dtype=torch.int32, device=q.device)
+        counts = _empty((q.shape[0], Hkv), torch.int32, q.device, stream)
     return selected, counts
 
 
@@ -547,7 +559,7 @@ def sparse_select(q: torch.Tensor, summary: torch.Tensor, exponents: torch.Tenso
     largest bound of q . k (pa_sparse_select).  Returns (selected int32
     [S, Hkv, top_k] ascending then -1, counts int32 [S, Hkv])."""
     if selected is None or counts is None:
-        selected, counts = _choice(q, summary.shape[1], top_k, selected, counts)
+        selected, counts = _choice(q, summary.shape[1], top_k, selected, counts, stream)
     status = _lib.binding().sparse_select(q, summary, exponents, block_tables, context_lens, block_size, top_k,
                                           sink_blocks, recent_blocks, selected, counts, stream)
     if status is not None:
@@ -565,7 +577,7 @@ def sparse_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     status = _lib.binding().sparse_decode(q, k_cache, v_cache, block_tables, context_lens, selected, counts,
                                           softmax_scale, kv_scale, k_scales, v_scales, splits, out, stream)
     if status is not None:
@@ -584,11 +596,11 @@ def sparse_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     returns bf16 [S, Hq, D] and leaves the choice in ``selected`` and
     ``counts`` when they are given."""
     if selected is None or counts is None:
-        selected, counts = _choice(q, k_cache.shape[1], top_k, selected, counts)
+        selected, counts = _choice(q, k_cache.shape[1], top_k, selected, counts, stream)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(q.shape[-1])
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     status = _lib.binding().sparse_attend(q, k_cache, v_cache, summary, exponents, block_tables, context_lens, top_k,
                                           sink_blocks, recent_blocks, softmax_scale, kv_scale, k_scales, v_scales,
                                           selected, counts, out, stream)

@@ -676,3 +676,31 @@ def test_captured_behind_copies_joins_and_other_kernels(api, cuda_device):
         done = full.long() // 16  # the others' exponents are left as they were: filled above
         assert torch.equal(s2, s) and torch.equal(e2[done], e[done])
     assert api.device_errors() == 0
+
+
+def test_tensors_made_for_another_stream_belong_to_it(api, cuda_device):
+    """What a call on a busy stream allocates is not memory that the current stream hands out, or has in use."""
+    case = Case(cuda_device, [900, 41, 300], 8, 2)
+    s, e = case.summaries(api)
+    T, Hq, D = case.q.shape
+    want_sel, want_cnt = api.sparse_select(case.q, s, e, case.bt, case.cl, 16, 9)
+    want = api.sparse_attend(case.q, case.kc, case.vc, s, e, case.bt, case.cl, 9)
+    none = torch.full((T,), -1, dtype=torch.int32, device=cuda_device)
+    zero = none + 1  # the inputs outlive the calls: they are the caller's
+    kv = case.q[:, :2].contiguous()
+    freq = torch.ones(D // 2, dtype=torch.float64, device=cuda_device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = api.sparse_attend(case.q, case.kc, case.vc, s, e, case.bt, case.cl, 9, stream=side)
+    sel, cnt = api.sparse_select(case.q, s, e, case.bt, case.cl, 16, 9, stream=side)
+    out = api.sparse_decode(case.q, case.kc, case.vc, case.bt, case.cl, sel, cnt, stream=side)
+    rot = api.rope_append(case.q, kv, kv, zero, freq, none, case.kc, case.vc, stream=side)
+    # the sizes of what those calls made, now on the current stream
+    mine = [torch.full(t.shape, 5, dtype=t.dtype, device=cuda_device) for _ in range(4) for t in (sel, cnt, got)]
+    torch.cuda.synchronize()
+    assert all((t == 5).all() for t in mine)
+    assert torch.equal(got, want) and torch.equal(sel, want_sel) and torch.equal(cnt, want_cnt)
+    case.check(out, want_sel.cpu().numpy(), want_cnt.cpu().numpy())
+    assert torch.equal(rot, case.q)  # position 0 turns nothing
