@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(kSummaryWarps * 32) summary_kernel(const Summa
     dependent_wait();
     dependent_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int token = blockIdx.x * kSummarySlots + lane;
-    int32_t slot = lane < kSummarySlots && token < a.num_tokens ? a.slots[token] : -1;
+    const int token0 = blockIdx.x * kSummarySlots;
+    int32_t slot = lane < min(kSummarySlots, a.num_tokens - token0) ? a.slots[token0 + lane] : -1;
     if (slot >= a.num_slots) {
         if (warp == 0) set_device_error(a.err, PA_DEVERR_BAD_SLOT);
         slot = -1;

@@ -80,6 +80,16 @@ def test_summary_slot_outside_the_pool_is_flagged(api, cuda_device):
     api.block_summary(kc, torch.empty(0, dtype=torch.int32, device=cuda_device), s, e)
 
 
+def test_summary_of_as_many_slots_as_an_int_counts(api, cuda_device):
+    kc = torch.ones(2, 1, 16, 64, dtype=torch.bfloat16, device=cuda_device)
+    s, e = api.alloc_block_summary(kc)
+    slots = torch.full((2 ** 31 - 1,), -1, dtype=torch.int32, device=cuda_device)
+    slots[-1] = 31
+    api.block_summary(kc, slots, s, e)
+    assert api.device_errors() == 0
+    assert (s[0] == 0).all() and (s[1] == 64).all()
+
+
 # ---- a paged case ---------------------------------------------------------------
 
 class Case:
