@@ -430,7 +430,8 @@ pa_status pa_prefill_mma(const void *q, const void *k_cache, const void *v_cache
  *                 so the three may be slices of one projection's output.
  *   positions     int32 [num_axes][num_tokens], any value (negative too)
  *   inv_freq      fp64 [rotary_dim / 2] (device): pair i of token t turns by
- *                 theta = positions[pair_axis[i]][t] * inv_freq[i] radians
+ *                 theta = positions[pair_axis[i]][t] * inv_freq[i] radians;
+ *                 below 2^65 in magnitude (others, infinity and NaN count as 0)
  *   pair_axis     int32 [rotary_dim / 2] (device); NULL: axis 0 for every pair
  *                 (needed when num_axes > 1).  Several axes (time, height,
  *                 width, ...) give each pair the position along its own axis.
@@ -442,7 +443,8 @@ pa_status pa_prefill_mma(const void *q, const void *k_cache, const void *v_cache
  *   (x_a, x_b) of a pair becomes magnitude * (x_a cos theta - x_b sin theta,
  *   x_a sin theta + x_b cos theta), in fp32, rounded once:
  *   q_out         bf16 [num_tokens][num_q_heads][head_dim], dense; may be q
- *                 itself when q is dense, and may not overlap it otherwise.
+ *                 itself when q is dense, and may not overlap it otherwise,
+ *                 nor k or v.
  *                 num_q_heads 0: no q (q and q_out may be NULL).
  *   k_cache, v_cache  row slot_mapping[t] gets the rotated k and v as they
  *                 are (PA_KV_BF16), or e4m3_rn_satfinite(x / scale) of the

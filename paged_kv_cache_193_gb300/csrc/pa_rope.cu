@@ -20,6 +20,7 @@
 // chain position, sine and cosine, row, so a thread's first row is on its way
 // while the angles are made.
 #include <algorithm>
+#include <utility>
 
 #include "pa_launch.cuh"
 
@@ -313,6 +314,11 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
         if (rope::overlaps(q, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
             return fail(PA_ERR_INVALID_ARG, "q_out overlaps q but is not q itself");
     }
+    for (const auto &[rows, stride] : {std::pair(k, k_stride), std::pair(v, v_stride)}) {
+        const size_t span = (static_cast<size_t>(num_tokens - 1) * stride + krow) * 2;
+        if (num_q_heads > 0 && rope::overlaps(rows, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
+            return fail(PA_ERR_INVALID_ARG, "q_out overlaps k or v");
+    }
     unsigned int *err = device_error_word();
     if (!err) return fail(PA_ERR_CUDA, "cannot resolve the device error word");
 
@@ -351,7 +357,7 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
     // With few tokens a token's rows are shared out too, up to four CTAs to an SM.
     const int shares = std::max(1, std::min((rows + at_once - 1) / at_once, 4 * 152 / num_tokens));
     a.rows_per_y = (rows + shares - 1) / shares;
-    const dim3 grid((num_tokens + a.tile - 1) / a.tile, (rows + a.rows_per_y - 1) / a.rows_per_y);
+    const dim3 grid((static_cast<unsigned>(num_tokens) + a.tile - 1) / a.tile, (rows + a.rows_per_y - 1) / a.rows_per_y);
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3, adj = adjacent != 0;
     const cudaError_t e = head_dim == 128 ? (fp8 ? rope::launch<128, true>(a, adj, grid, stream)
                                                  : rope::launch<128, false>(a, adj, grid, stream))

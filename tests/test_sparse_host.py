@@ -42,6 +42,7 @@ def _rope(lib, **kw):
     (dict(qs=1020), 1), (dict(ks=260), 1), (dict(vs=248), 1), (dict(qs=1016), 1),
     (dict(qo=FAKE, qs=1536), 1),                                    # strided q cannot be its own output
     (dict(qo=ctypes.c_void_p((1 << 20) + 4096)), 1),                # q_out inside q
+    (dict(k=FAR), 1), (dict(v=FAR, vs=512), 1),                     # q_out on k or v
     (dict(NB=1 << 28), 2),
 ])
 def test_rope_append_rejects_on_host(lib, kw, status):
