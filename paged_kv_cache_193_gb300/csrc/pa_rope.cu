@@ -20,12 +20,36 @@
 // chain position, sine and cosine, row, so a thread's first row is on its way
 // while the angles are made.
 #include <algorithm>
+#include <cstring>
 #include <utility>
 
 #include "pa_launch.cuh"
 
 namespace pa {
 namespace rope {
+
+// How x / scale is found where only its E4M3 code matters: x times RN(1 /
+// scale) is within two units in the last place of RN(x / scale), so both have
+// the same code unless a border between two codes is that near, and then the
+// division decides (Ziv's rounding test, "Fast evaluation of elementary
+// mathematical functions with correctly rounded last bit", 1991).  The borders,
+// and the codes, have at most five significant bits, so near them the lower 19
+// of a float's are almost all 0 or almost all 1.  Below 2^-126 and above 448 the
+// code is 0 or the largest, whatever the last place.  (8192 tokens, 32 + 8 heads:
+// 36.5 us with it, 39.5 with a division for every element; 256 tokens of 64 + 8
+// heads 3.7 and 4.0.)
+struct Divisor {
+    float scale, inverse;
+    // Of the 2^19 endings of a product, how many are in doubt, times 2^13: none when
+    // the product is exact, all when 1 / scale may be out of range.
+    uint32_t near;
+    __host__ __device__ __forceinline__ static Divisor of(float x) {
+        const bool all = !(x >= 7.888609052210118e-31f && x <= 1.2676506002282294e30f);  // 2^-100, 2^100
+        uint32_t bits;
+        memcpy(&bits, &x, 4);
+        return {x, 1.f / x, all ? 0xffffffffu : bits & 0x7fffff ? 9u << 13 : 0u};
+    }
+};
 
 struct Args {
     const __nv_bfloat16 *q, *k, *v;
@@ -41,7 +65,8 @@ struct Args {
     int pairs;       // rotary_dim / 2
     int tile;        // tokens per CTA
     int rows_per_y;  // rows (of one token's q, k and v heads) per CTA
-    float magnitude, kv_scale;
+    float magnitude;
+    Divisor kv_scale;
     const float *k_scales, *v_scales;
     unsigned int *err;
 };
@@ -82,19 +107,22 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
 
 // Eight fp32 values as E4M3 codes of x / scale: one rounding from fp32 (the
 // rotated row is not rounded to bf16 on the way).
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-    uint32_t w[2];
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divisor &by) {
+    uint32_t w[2] = {0, 0};
+    uint32_t least = 0xffffffffu;  // of the endings, plus 4, in the upper 19 bits
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t packed = 0;
+    for (int i = 0; i < 8; i += 2) {
+        const float2 y = make_float2(__fmul_rn(x[i], by.inverse), __fmul_rn(x[i + 1], by.inverse));
+        least = min(least, min(__float_as_uint(y.x) * 8192u + 32768u, __float_as_uint(y.y) * 8192u + 32768u));
+        w[i / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << 8 * (i % 4);
+    }
+    if (least < by.near) {
+        w[0] = w[1] = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 f = make_float2(__fdiv_rn(x[4 * i + 2 * j], scale),
-                                         __fdiv_rn(x[4 * i + 2 * j + 1], scale));
-            packed |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3))
-                      << (16 * j);
+        for (int i = 0; i < 8; i += 2) {
+            const float2 y = make_float2(__fdiv_rn(x[i], by.scale), __fdiv_rn(x[i + 1], by.scale));
+            w[i / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << 8 * (i % 4);
         }
-        w[i] = packed;
     }
     return make_uint2(w[0], w[1]);
 }
@@ -108,7 +136,7 @@ template <int D, bool FP8, bool ADJACENT, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
     constexpr int VPR = D / 16;  // threads to a row
     __shared__ __align__(16) float cs[kMaxTile][D / 2], sn[kMaxTile][D / 2];
-    __shared__ int32_t slot_s[kMaxTile];
+    __shared__ int64_t row_s[kMaxTile];  // the slot's row of head 0, or -1
     dependent_wait();
     const int t0 = blockIdx.x * a.tile;
     const int live = min(a.tile, a.num_tokens - t0);
@@ -116,18 +144,18 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
     const int rows = a.num_q_heads + 2 * a.num_kv_heads;
     const int row0 = blockIdx.y * a.rows_per_y;
     const int nrows = min(a.rows_per_y, rows - row0);
-    const int total = live * nrows;
     const bool turn = 8 * j < a.pairs;
     // first elements of the thread's two vectors
     const int rest = 2 * a.pairs + 16 * (j - a.pairs / 8);
     const int ea = !turn ? rest : ADJACENT ? 16 * j : 8 * j;
     const int eb = !turn || ADJACENT ? ea + 8 : a.pairs + 8 * j;
     uint4 wa, wb;  // the thread's present piece
-    int tt, h;
+    const int first = threadIdx.x / VPR;
+    int tt = first / nrows, at = first - tt * nrows;  // token and row of the piece
+    int h;
     bool is_q, is_v;
-    auto load = [&](int i) {
-        tt = i / nrows;
-        const int row = row0 + i - tt * nrows;
+    auto load = [&]() {
+        const int row = row0 + at;
         const int64_t t = t0 + tt;
         is_q = row < a.num_q_heads;
         is_v = row >= a.num_q_heads + a.num_kv_heads;
@@ -137,8 +165,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         wa = *reinterpret_cast<const uint4 *>(src + (is_v ? 16 * j : ea));
         wb = *reinterpret_cast<const uint4 *>(src + (is_v ? 16 * j + 8 : eb));
     };
-    int i = threadIdx.x / VPR;
-    if (i < total) load(i);  // on its way while the angles are made
+    if (tt < live) load();  // on its way while the angles are made
 
     for (int x = threadIdx.x; x < live * a.pairs; x += kThreads) {
         const int tok = x / a.pairs, p = x - tok * a.pairs;
@@ -163,19 +190,16 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
             if (blockIdx.y == 0) set_device_error(a.err, PA_DEVERR_BAD_SLOT);
             slot = -1;
         }
-        slot_s[threadIdx.x] = slot;
+        row_s[threadIdx.x] = slot < 0 ? -1 : static_cast<int64_t>(slot / a.block_size) * a.num_kv_heads * a.block_size + slot % a.block_size;
     }
     __syncthreads();
 
     auto store = [&]() {
         const int64_t t = t0 + tt;
-        const int32_t slot = slot_s[tt];
-        if (!is_q && slot < 0) return;
+        const int64_t row = row_s[tt];
+        if (!is_q && row < 0) return;
         const int da = is_v ? 16 * j : ea, db = is_v ? da + 8 : eb;
-        const int64_t dst =
-            is_q ? (t * a.num_q_heads + h) * D
-                 : ((static_cast<int64_t>(slot / a.block_size) * a.num_kv_heads + h) * a.block_size +
-                    slot % a.block_size) * D;
+        const int64_t dst = (is_q ? t * a.num_q_heads + h : row + h * a.block_size) * D;
         const bool rotate = turn && !is_v;
         if (!rotate && (!FP8 || is_q)) {  // bits as they are
             __nv_bfloat16 *to = is_q ? a.q_out : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache);
@@ -214,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
             *reinterpret_cast<uint4 *>(a.q_out + dst + db) = pack8(xb);
         } else if constexpr (FP8) {
             const float *scales = is_v ? a.v_scales : a.k_scales;
-            const float scale = scales ? scales[h] : a.kv_scale;
+            const Divisor by = scales ? Divisor::of(scales[h]) : a.kv_scale;
             uint8_t *to = is_v ? a.v_cache : a.k_cache;
-            *reinterpret_cast<uint2 *>(to + dst + da) = codes8(xa, scale);
-            *reinterpret_cast<uint2 *>(to + dst + db) = codes8(xb, scale);
+            *reinterpret_cast<uint2 *>(to + dst + da) = codes8(xa, by);
+            *reinterpret_cast<uint2 *>(to + dst + db) = codes8(xb, by);
         } else {
             __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.k_cache);
             *reinterpret_cast<uint4 *>(to + dst + da) = pack8(xa);
@@ -225,21 +249,23 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         }
     };
     dependent_release();
-    while (i < total) {
+    while (tt < live) {
         store();
-        i += kThreads / VPR;
-        if (i < total) load(i);
+        for (at += kThreads / VPR; at >= nrows; at -= nrows) ++tt;
+        if (tt < live) load();
     }
 }
 
-// Grids of several waves want a fifth CTA on each SM (8192 tokens, 32 + 8 heads:
-// 35 against 39 us), others the registers (1000 tokens 5.6 against 6.4 us, 256
-// with an E4M3 cache 3.9 against 4.7).
+// Grids of several waves want a fifth CTA on each SM at head dim 128 (8192
+// tokens, 32 + 8 heads: 34.8 against 38.9 us, E4M3 36.5 against 38.8), others the
+// registers (1000 tokens 5.6 against 6.4 us; 8192 of head dim 64, E4M3 cache, 21.1
+// against 22.6).
 template <int D, bool FP8, bool ADJACENT>
 static cudaError_t launch_ctas(const Args &a, dim3 grid, cudaStream_t stream) {
-    const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y;
-    return ctas > 4 * 152 ? launch_dependent(append_kernel<D, FP8, ADJACENT, 5>, grid, kThreads, 0, 0, stream, a)
-                          : launch_dependent(append_kernel<D, FP8, ADJACENT, 4>, grid, kThreads, 0, 0, stream, a);
+    if constexpr (D == 128)
+        if (static_cast<int64_t>(grid.x) * grid.y > 4 * 152)
+            return launch_dependent(append_kernel<D, FP8, ADJACENT, 5>, grid, kThreads, 0, 0, stream, a);
+    return launch_dependent(append_kernel<D, FP8, ADJACENT, 4>, grid, kThreads, 0, 0, stream, a);
 }
 
 template <int D, bool FP8>
@@ -344,7 +370,7 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
     a.block_size = block_size;
     a.pairs = rotary_dim / 2;
     a.magnitude = magnitude;
-    a.kv_scale = kv_scale;
+    a.kv_scale = rope::Divisor::of(kv_scale);
     a.k_scales = k_scales;
     a.v_scales = v_scales;
     a.err = err;
