@@ -260,10 +260,35 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
 // tokens, 32 + 8 heads: 34.8 against 38.9 us, E4M3 36.5 against 38.8), others the
 // registers (1000 tokens 5.6 against 6.4 us; 8192 of head dim 64, E4M3 cache, 21.1
 // against 22.6).
+static constexpr bool five_to_an_sm(int head_dim, int64_t ctas) { return head_dim == 128 && ctas > 4 * 152; }
+
+// Tokens to a CTA: the least of tokens on the fullest SM plus, for each wave of
+// CTAs, its start (the angles) and its last CTA's own time, in units of 6144
+// elements.  Weights fitted to tiles of 1 to 8 over 400 to 7000 tokens of 24 to
+// 80 rows at both head dims: within 2% of the best tile.  (32 + 8 heads, 700
+// tokens: 4.3 us with 1 to a CTA, 5.3 with 2; 1500: 6.4 with 2, 8.5 with 4; 3500:
+// 16.8 with 5, 19.4 with 4; 8192: 34.7 with 6, 39.6 with 8.)
+static int tokens_per_cta(int num_tokens, int rows, int head_dim) {
+    const double work = static_cast<double>(rows) * head_dim / 6144;
+    int best = 1;
+    double least = INFINITY;
+    for (int tile = 1; tile <= kMaxTile; ++tile) {
+        const int64_t ctas = (static_cast<int64_t>(num_tokens) + tile - 1) / tile;
+        const int64_t places = static_cast<int64_t>(five_to_an_sm(head_dim, ctas) ? 5 : 4) * 152;
+        const int64_t waves = (ctas + places - 1) / places, fullest = (ctas + 151) / 152 * tile;
+        const double cost = work * fullest + waves * (3.5 + 1.5 * work * tile);
+        if (cost < least) {
+            least = cost;
+            best = tile;
+        }
+    }
+    return best;
+}
+
 template <int D, bool FP8, bool ADJACENT>
 static cudaError_t launch_ctas(const Args &a, dim3 grid, cudaStream_t stream) {
     if constexpr (D == 128)
-        if (static_cast<int64_t>(grid.x) * grid.y > 4 * 152)
+        if (five_to_an_sm(D, static_cast<int64_t>(grid.x) * grid.y))
             return launch_dependent(append_kernel<D, FP8, ADJACENT, 5>, grid, kThreads, 0, 0, stream, a);
     return launch_dependent(append_kernel<D, FP8, ADJACENT, 4>, grid, kThreads, 0, 0, stream, a);
 }
@@ -375,10 +400,7 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
     a.v_scales = v_scales;
     a.err = err;
     const int rows = num_q_heads + 2 * num_kv_heads;
-    // Tokens to a CTA: up to some 24,000 elements, so that the angles of its
-    // tokens are a small part of its work, but two CTAs to an SM.
-    a.tile = 1;
-    while (a.tile < rope::kMaxTile && 2 * a.tile * rows * head_dim <= 24576 && num_tokens >= 2 * a.tile * 2 * 152) a.tile *= 2;
+    a.tile = rope::tokens_per_cta(num_tokens, rows, head_dim);
     const int at_once = rope::kThreads / (head_dim / 16);  // rows of one pass of the CTA's threads
     // With few tokens a token's rows are shared out too, up to four CTAs to an SM.
     const int shares = std::max(1, std::min((rows + at_once - 1) / at_once, 4 * 152 / num_tokens));
