@@ -68,6 +68,18 @@ static int splits_of_four_warps(int64_t rows, int pages, int resident) {
 // Clusters of three and six of them, and of eight beyond half of the places,
 // measured slower than the next smaller size (32 of 8K: 18 us with 8, 15 with 4),
 // clusters of sixteen slower than of eight (8 rows of 128K: 30 us, 24 with eight).
+// In clusters of two all places can be taken, in clusters of four not quite (76
+// rows of 375 pages, top 128, 304 CTAs on 304 places: 32.8 us, 27.7 in clusters of
+// two; 72 rows 23.3 and 26.8).
+// Rows of few pages take one CTA, which needs no cluster's barriers (48 rows of 125
+// pages, top 24: 8.1 us, 10.0 with two; 96 of 157: 11.7 and 14.5).  Clusters of two
+// pay from some 800 pages on (96 rows of 625, top 64: 21.2 us with one CTA, 26.5
+// with two; 136 of 1000, top 128: 38.6 and 37.2, of 2500, top 192: 62.5 and 56.1).
+// Where four do not fit, six of four warps fill the SMs better for long rows, or
+// for lists that are long beside them (96 rows of 2500 pages, top 192: 43.8 us, 47.6
+// with two of eight warps; of 375, top 128: 28.0, 30.3 with one; of 94, top 24, one:
+// 10.8 and 12.8), but not where only three CTAs of four warps fit an SM (72 rows of
+// 1000 pages of 32 bf16 tokens, top 128: 37.3, 35.4 with two of eight warps).
 static Launch chosen_launch(const Call &c, int group, int resident) {
     const int64_t rows = static_cast<int64_t>(c.num_rows) * c.num_kv_heads;
     Launch l{4, 1, false};
@@ -76,8 +88,15 @@ static Launch chosen_launch(const Call &c, int group, int resident) {
         l.warps = 8;
         places = resident / 2;
         const int pages = std::max(c.top_k, c.max_blocks / 4);
-        for (int s : {2, 4, 8})
-            if (rows * s <= (s == 8 ? places * kSms / 2 : places * kSms * 7 / 8) && pages >= 8 * s) l.splits = s;
+        const int64_t room = static_cast<int64_t>(places) * kSms;
+        if (rows * 2 <= room && c.max_blocks >= 800) l.splits = 2;
+        if (rows * 4 <= room * 19 / 20 && pages >= 32) l.splits = 4;
+        if (rows * 8 <= room / 2 && pages >= 64) l.splits = 8;
+        const bool long_list = c.top_k >= 48 && c.top_k >= c.max_blocks / 8;
+        if (l.splits <= 2 && resident >= 4 && rows * 6 <= resident * kSms * 19 / 20 && (c.max_blocks >= 800 || long_list)) {
+            l = {4, 6, false};
+            places = resident;
+        }
     } else {
         l.splits = splits_of_four_warps(rows, c.top_k, resident);
     }

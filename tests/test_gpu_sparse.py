@@ -408,13 +408,33 @@ def test_choice_flags_bad_table_entries_and_contexts(api, cuda_device):
 @pytest.mark.parametrize("G,S", [(2, 10), (2, 40), (2, 110), (2, 240), (2, 310), (2, 700), (9, 40), (9, 60), (9, 90), (9, 130),
                                  (9, 190), (9, 300)])
 def test_every_number_of_ctas_to_a_row(api, cuda_device, G, S):
-    """Row counts for which a row gets 8, 4, 2 and 1 CTAs of eight warps, and 8, 6, 4, 3, 2 and 1 of four."""
+    """Row counts for which a row gets 8, 4 and 1 CTAs of eight warps, and 8, 6, 4, 3, 2 and 1 of four."""
     rng = np.random.default_rng(S)
     case = Case(cuda_device, [int(n) for n in rng.integers(0, 330, S)], G, 1, D=64, seed=S, width=260)
     s, e = case.summaries(api)
     top_k = 34 if S < 100 else 16
     sel, cnt, out = case.attend(api, s, e, top_k)
     want_sel, want_cnt = R.select(f64(case.q), s.cpu().numpy(), e.cpu().numpy(), case.tables, case.lens, 16, top_k, 1, 2)
+    assert np.array_equal(sel, want_sel) and np.array_equal(cnt, want_cnt)
+    case.check(out, sel, cnt)
+    assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("G,S,width,top_k,B,fp8", [
+    (2, 85, 900, 20, 16, False), (2, 85, 900, 50, 16, True), (2, 96, 200, 60, 16, False), (3, 90, 390, 49, 32, True),   # six of four warps
+    (2, 140, 900, 20, 16, False), (2, 152, 800, 33, 16, True), (1, 70, 900, 20, 32, False),                             # two of eight
+    (2, 72, 900, 40, 16, False), (2, 36, 900, 40, 32, False), (2, 85, 900, 10, 16, False), (2, 100, 799, 40, 16, False),
+])
+def test_clusters_by_length_of_the_tables(api, cuda_device, G, S, width, top_k, B, fp8):
+    """Row counts at which the tables' width and the lists' length say how many CTAs a row gets; some rows with as many
+    pages as fit, some with few, some with none."""
+    rng = np.random.default_rng(S + width)
+    lens = [int(n) for n in rng.integers(0, 25 * B, S)]
+    lens[1], lens[S // 2], lens[-1], lens[3] = width * B, (width // 2 + 3) * B - 1, width * B - B // 2, 300
+    case = Case(cuda_device, lens, G, 1, D=64, B=B, fp8=fp8, seed=S, width=width)
+    s, e = case.summaries(api)
+    sel, cnt, out = case.attend(api, s, e, top_k)
+    want_sel, want_cnt = R.select(f64(case.q), s.cpu().numpy(), e.cpu().numpy(), case.tables, case.lens, B, top_k, 1, 2)
     assert np.array_equal(sel, want_sel) and np.array_equal(cnt, want_cnt)
     case.check(out, sel, cnt)
     assert api.device_errors() == 0
