@@ -161,14 +161,9 @@ __global__ void __launch_bounds__(kSelThreads, (NT == 2 ? 384 : 512) / kSelThrea
 }
 
 template <int D, int NT, int kSelThreads>
-static pa_status launch_threads(SelectArgs a, int num_rows, cudaStream_t stream) {
+static pa_status launch_threads(SelectArgs a, int num_rows, int ranks, cudaStream_t stream) {
     a.stages = kMaxStages;
-    // A cluster for a row while that leaves half of the SMs to others' and each
-    // CTA some 512 pages: 64 rows of 8192 pages take 40 us with two CTAs of 256
-    // threads, 67 with one, 48 with four.
-    const int64_t rows = static_cast<int64_t>(num_rows) * a.num_kv_heads;
-    int ranks = 1;
-    while (ranks < 8 && ((2 * rows * ranks <= kSms && a.max_blocks > 512 * ranks) || a.max_blocks > kMaxKeys * ranks)) ranks *= 2;
+    while (a.max_blocks > kMaxKeys * ranks) ranks *= 2;  // at most 8, by the limit on the table
     auto kern = select_kernel<D, NT, kSelThreads>;
     static std::atomic<uint64_t> raised{0};
     const int copies = copy_bytes(kSelThreads, D, kMaxStages);
@@ -179,12 +174,39 @@ static pa_status launch_threads(SelectArgs a, int num_rows, cudaStream_t stream)
                       "sparse select launch");
 }
 
+// Up to a row to an SM: CTAs of 256 threads, several to a row while each has an SM
+// to itself and enough pages to pay for the cluster's barriers (8 rows of 625 pages: 6.7
+// us with eight, 8.0 with four; 16 of 2500: 11.4 with four, 12.4 with eight; of 313: 6.0
+// with four, 8.0 with one; 72 of 625: 11.6 with two, 9.2 with one; of 2500: 19.3 and
+// 25.1), or, of very many pages, of 128 threads, three to an SM (48 of 8192 pages: 27.8
+// us with eight, 37.5 with two of 256; 96 of 2500: 19.8 with four, 24.8 with one of 256).
+// Beyond, the fullest SM counts: 192 rows of 157 pages take 7.8 us with 128 threads and
+// 8.8 with 256, of 625 15.5 and 13.5 (16.6 and 19.4 with 16 query heads, where one CTA of
+// 256 fits an SM), of 2500 31.0 with two of 128 and 43.5 with one of 256; 1024 rows of
+// 157 18.3 and 25.2.
 template <int D, int NT>
 static pa_status launch_select(const SelectArgs &a, int num_rows, cudaStream_t stream) {
-    // 272 rows of up to 560 pages: 10.0 us with 256 threads, 10.5 with 128; 2048 rows
-    // of up to 128 pages: 39 and 27.
-    const bool few = static_cast<int64_t>(num_rows) * a.num_kv_heads < 2 * kSms;
-    return few ? launch_threads<D, NT, 256>(a, num_rows, stream) : launch_threads<D, NT, 128>(a, num_rows, stream);
+    const int64_t rows = static_cast<int64_t>(num_rows) * a.num_kv_heads;
+    const int pages = a.max_blocks;
+    int threads = 256, ranks = 1;
+    if (rows <= kSms) {
+        if (rows * 16 <= kSms && pages > 256)
+            ranks = 8;
+        else if (rows * 4 <= kSms && pages > 128)
+            ranks = 4;
+        else if (rows * 8 <= 3 * kSms && pages >= 2000)
+            threads = 128, ranks = 8;
+        else if (rows * 2 <= kSms && pages >= 1000)
+            ranks = 2;
+        else if (rows * 2 > kSms && rows * 4 <= 3 * kSms && pages >= 2000)
+            threads = 128, ranks = 4;
+    } else {
+        const bool two = rows * 2 <= 3 * kSms && pages >= 1000;  // the fullest SM has three
+        if (rows > 2 * kSms || pages < 400 || NT == 2) threads = 128;
+        if (two || pages >= 5000) threads = 128, ranks = 2;
+    }
+    return threads == 256 ? launch_threads<D, NT, 256>(a, num_rows, ranks, stream)
+                          : launch_threads<D, NT, 128>(a, num_rows, ranks, stream);
 }
 
 pa_status check_select(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,

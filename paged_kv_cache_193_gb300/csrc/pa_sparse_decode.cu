@@ -99,6 +99,9 @@ static Launch chosen_launch(const Call &c, int group, int resident) {
         }
     } else {
         l.splits = splits_of_four_warps(rows, c.top_k, resident);
+        // as above (16 query heads: 192 rows of 250 pages, top 32: 20.4 us with one, 23.1
+        // with two; 72 of 94, top 24: 13.1, 14.3 with six)
+        if ((l.splits == 2 && c.max_blocks < 800) || (rows >= 48 && std::max(c.top_k, c.max_blocks / 4) < 32)) l.splits = 1;
     }
     while (c.max_blocks > kMaxKeys * l.splits) ++l.splits;  // at most 8, by the limit on the table
     // With a few more CTAs than places, and rows that few threads can sort, the

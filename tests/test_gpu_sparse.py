@@ -423,6 +423,7 @@ def test_every_number_of_ctas_to_a_row(api, cuda_device, G, S):
 @pytest.mark.parametrize("G,S,width,top_k,B,fp8", [
     (2, 85, 900, 20, 16, False), (2, 85, 900, 50, 16, True), (2, 96, 200, 60, 16, False), (3, 90, 390, 49, 32, True),   # six of four warps
     (2, 140, 900, 20, 16, False), (2, 152, 800, 33, 16, True), (1, 70, 900, 20, 32, False),                             # two of eight
+    (9, 190, 1000, 40, 16, False), (9, 190, 200, 40, 16, True), (16, 60, 100, 20, 16, False),                           # groups above 8
     (2, 72, 900, 40, 16, False), (2, 36, 900, 40, 32, False), (2, 85, 900, 10, 16, False), (2, 100, 799, 40, 16, False),
 ])
 def test_clusters_by_length_of_the_tables(api, cuda_device, G, S, width, top_k, B, fp8):
@@ -437,6 +438,25 @@ def test_clusters_by_length_of_the_tables(api, cuda_device, G, S, width, top_k, 
     want_sel, want_cnt = R.select(f64(case.q), s.cpu().numpy(), e.cpu().numpy(), case.tables, case.lens, B, top_k, 1, 2)
     assert np.array_equal(sel, want_sel) and np.array_equal(cnt, want_cnt)
     case.check(out, sel, cnt)
+    assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("G,S,width", [(2, 9, 257), (2, 9, 128), (9, 30, 400), (2, 30, 2100), (2, 50, 2000), (2, 70, 1000), (2, 70, 400),
+                                       (9, 100, 2000), (2, 140, 2000), (2, 160, 300), (9, 160, 500), (2, 200, 1000), (2, 310, 999),
+                                       (9, 310, 5000), (2, 240, 5000)])
+def test_choice_alone_by_rows_and_tables(api, cuda_device, G, S, width):
+    """Every number of threads and CTAs that the choice alone gives a row, bit for bit."""
+    D, NB = 64, 700
+    g = torch.Generator().manual_seed(S + width)
+    q = torch.randn(S, G, D, generator=g).to(torch.bfloat16)
+    s = torch.randint(-127, 128, (NB, 1, 2, D), generator=g).to(torch.int8).sort(dim=2, descending=True).values
+    e = torch.randint(-9, -6, (NB, 1), generator=g).to(torch.int8)
+    tables = torch.randint(0, NB, (S, width), generator=g).to(torch.int32)
+    lens = torch.randint(0, 60 * 16, (S,), generator=g).to(torch.int32)
+    lens[::S // 4] = width * 16 - torch.randint(0, 16 * 16, lens[::S // 4].shape, generator=g).to(torch.int32)
+    sel, cnt = api.sparse_select(*(t.to(cuda_device) for t in (q, s, e, tables, lens)), 16, 37)
+    want_sel, want_cnt = R.select(f64(q), s.numpy(), e.numpy(), tables.numpy(), lens.numpy(), 16, 37, 1, 2)
+    assert np.array_equal(sel.cpu().numpy(), want_sel) and np.array_equal(cnt.cpu().numpy(), want_cnt)
     assert api.device_errors() == 0
 
 
