@@ -53,10 +53,13 @@ struct Launch {
 // whose warps have a page each.  An eighth of the CTAs' places is kept back:
 // clusters of three, six or eight leave some of a GPC's places empty (8 rows of
 // 8 heads, 16 queries each, 128K tokens: 62 us with 6, 71 with 4, 85 with 8).
+// Short lists are not shared out, or little (152 rows of 8 pages 4.8 us, 5.3 with two
+// CTAs, of 16 query heads 5.4 and 7.8; 72 rows of 24 pages 6.1 with two, 6.7 with six).
 static int splits_of_four_warps(int64_t rows, int pages, int resident) {
+    const int most = pages < 16 ? 1 : pages < 32 && rows >= 48 ? 2 : 8;
     int splits = 1;
     for (int s : {2, 3, 4, 6, 8})
-        if (rows * s <= resident * kSms * 7 / 8 && pages >= 4 * s) splits = s;
+        if (s <= most && rows * s <= resident * kSms * 7 / 8 && pages >= 4 * s) splits = s;
     return splits;
 }
 

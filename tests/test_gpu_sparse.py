@@ -32,7 +32,7 @@ def pool(shape, fp8, g, device, gain=1.0):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D,B,Hkv,T", [(128, 16, 8, 1), (128, 16, 3, 33), (128, 32, 8, 257), (64, 16, 1, 100), (64, 32, 2, 64),
-                                       (64, 32, 5, 2000)])
+                                       (64, 32, 5, 2000), (64, 16, 9, 600), (128, 32, 20, 300), (64, 16, 2, 5000)])
 def test_summary_bit_exact(api, cuda_device, D, B, Hkv, T, fp8):
     g = torch.Generator().manual_seed(D + B + Hkv + T)
     NB = max(4, T // 4)
