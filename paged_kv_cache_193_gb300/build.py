@@ -5,7 +5,8 @@ shared library with the CUDA runtime linked statically, so the library only
 needs the driver at run time.  Output: ``paged_kv_cache_193_gb300/_build/libpa.so``.
 Beside it ``csrc/binding.cpp`` becomes ``_pa_binding.so``, the CPython binding
 of the calls whose kernels are shorter than a check of their arguments in
-Python.
+Python.  The library needs no torch; without one that has CUDA the binding
+alone is left out.
 """
 from __future__ import annotations
 
@@ -59,16 +60,19 @@ def compile_flags(verbose_ptxas: bool = False) -> list[str]:
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile the CPython binding if its source is newer; return its path."""
+    """Compile the CPython binding if its source is newer; return its path.
+    Raises ImportError without a torch that has CUDA."""
     newest = max(os.path.getmtime(f) for f in [BINDING_SRC, *_headers(), __file__])
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
         return BINDING
     import torch
     root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    if not os.path.exists(os.path.join(lib, "libc10_cuda.so")):
+        raise ImportError(f"the torch in {root} has no CUDA")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     os.makedirs(OUT_DIR, exist_ok=True)
     tmp = BINDING + f".tmp{os.getpid()}"
-    lib = os.path.join(root, "lib")
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib,
@@ -80,6 +84,16 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
+def _finish(binding) -> None:
+    """The result of ``build_binding``: what it needs of torch may be missing,
+    anything else that fails is raised."""
+    try:
+        binding()
+    except ImportError as e:
+        sys.stderr.write(f"{BINDING} not built ({e}): the calls of the library itself are all there, "
+                         "the Python calls that go through the binding are not\n")
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = None,
           defines: tuple[str, ...] = ()) -> str:
     """Compile and link if any source is newer than the library; return its
@@ -87,7 +101,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = No
     variant of the library elsewhere, for launch-shape tuning."""
     lib = out or LIB
     if not force and not defines and out is None and not _stale():
-        build_binding()
+        _finish(build_binding)
         return LIB
     obj_dir = os.path.join(os.path.dirname(lib), os.path.basename(lib) + ".objs") if out else OUT_DIR
     os.makedirs(obj_dir, exist_ok=True)
@@ -106,8 +120,6 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = No
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(build_binding, force) if out is None else None
         results = list(ex.map(one, srcs))
-        if binding is not None:
-            binding.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)
@@ -117,6 +129,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = No
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if binding is not None:
+        _finish(binding.result)
     return lib
 
 
