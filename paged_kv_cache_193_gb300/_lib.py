@@ -86,14 +86,22 @@ _binding = None
 
 def binding():
     """The CPython binding, calling into the library that load() gives.  Like
-    load(), raises ImportError when it has not been built."""
+    load(), raises ImportError when it has not been built, or was built for
+    another torch or Python than this one's."""
     global _binding
     if _binding is None:
         if not os.path.exists(BINDING_PATH):
             raise ImportError(
                 f"{BINDING_PATH} not found: build the CUDA library first "
                 "(python -c 'import __graft_entry__ as g; g.build()')")
-        import torch  # noqa: F401  (the module links against its libraries)
+        import torch  # the module links against its libraries
+
+        from .build import binding_for, built_for
+        has, needs = built_for(BINDING_PATH), binding_for(torch)
+        if has != needs:
+            raise ImportError(
+                f"{BINDING_PATH} was built for {has}, this is {needs}: build it again "
+                "(python -c 'import __graft_entry__ as g; g.build()')")
         loader = importlib.machinery.ExtensionFileLoader("_pa_binding", BINDING_PATH)
         spec = importlib.util.spec_from_file_location("_pa_binding", BINDING_PATH, loader=loader)
         module = importlib.util.module_from_spec(spec)
@@ -102,7 +110,6 @@ def binding():
         module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in BINDING_CALLS))
         _binding = module
     return _binding
-
 
 
 def load(path: str | None = None) -> ctypes.CDLL:

@@ -59,13 +59,29 @@ def compile_flags(verbose_ptxas: bool = False) -> list[str]:
     return flags
 
 
+def binding_for(torch) -> str:
+    """What a binding built now fits: it uses C++ interfaces of torch, which
+    change between versions, and Python's.  Kept beside it in a ``.for`` file."""
+    return f"torch {torch.__version__}, Python {sysconfig.get_config_var('SOABI')}"
+
+
+def built_for(binding: str) -> str:
+    try:
+        with open(binding + ".for") as f:
+            return f.read()
+    except FileNotFoundError:
+        return "unknown"
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile the CPython binding if its source is newer; return its path.
-    Raises ImportError without a torch that has CUDA."""
-    newest = max(os.path.getmtime(f) for f in [BINDING_SRC, *_headers(), __file__])
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+    """Compile the CPython binding if its source is newer, or it was built for
+    another torch; return its path.  Raises ImportError without a torch that
+    has CUDA."""
     import torch
+    newest = max(os.path.getmtime(f) for f in [BINDING_SRC, *_headers(), __file__])
+    if (not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest
+            and built_for(BINDING) == binding_for(torch)):
+        return BINDING
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
     if not os.path.exists(os.path.join(lib, "libc10_cuda.so")):
@@ -80,7 +96,12 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(BINDING + ".for"):
+        os.remove(BINDING + ".for")  # says nothing while the two do not belong together
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(binding_for(torch))
+    os.replace(tmp, BINDING + ".for")
     return BINDING
 
 

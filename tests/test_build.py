@@ -57,3 +57,42 @@ def test_a_binding_that_does_not_compile_is_raised_after_the_link(tree, monkeypa
     with pytest.raises(RuntimeError, match="binding"):
         build.build()
     assert linked(tree / "libpa.so")
+
+
+def test_a_binding_of_another_torch_is_built_again(tree, monkeypatch):
+    """Its C++ interface is that of the torch, and the Python, that it was built with, whatever the files' times."""
+    built = []
+
+    def compiled(cmd, **kw):
+        if build.BINDING_SRC in cmd:
+            built.append(cmd)
+            open(cmd[cmd.index("-o") + 1], "wb").close()
+            return build.subprocess.CompletedProcess(cmd, 0, "", "")
+        return run(cmd, **kw)
+
+    run = build.subprocess.run
+    monkeypatch.setattr(build.subprocess, "run", compiled)
+    import torch
+    build.build_binding()
+    build.build_binding()
+    assert len(built) == 1
+    monkeypatch.setattr(torch, "__version__", "9.9.9+cu999")
+    build.build_binding()
+    build.build_binding()
+    assert len(built) == 2
+    os.remove(build.BINDING + ".for")  # one that does not say
+    build.build_binding()
+    assert len(built) == 3
+
+
+def test_a_binding_of_another_torch_is_not_loaded(monkeypatch, tmp_path):
+    import torch
+
+    from paged_kv_cache_193_gb300 import _lib
+    path = tmp_path / "_pa_binding.so"
+    path.write_bytes(b"not a module: reading it would fail differently")
+    (tmp_path / "_pa_binding.so.for").write_text(build.binding_for(torch).replace(torch.__version__, "1.0"))
+    monkeypatch.setattr(_lib, "_binding", None)
+    monkeypatch.setattr(_lib, "BINDING_PATH", str(path))
+    with pytest.raises(ImportError, match="torch 1.0.*build"):
+        _lib.binding()
