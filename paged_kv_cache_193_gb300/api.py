@@ -623,6 +623,8 @@ class SparseDecodeStep:
                  top_k, sink_blocks=1, recent_blocks=2, softmax_scale=None, kv_scale=1.0, k_scales=None,
                  v_scales=None, pair_axis=None, adjacent=False, magnitude=1.0, summary=None,
                  exponents=None):
+        if (summary is None) != (exponents is None):
+            raise ValueError("summary and exponents must both be given or both be None")
         self.k_cache, self.v_cache = k_cache, v_cache
         self.block_tables, self.context_lens, self.positions = block_tables, context_lens, positions
         self.inv_freq, self.pair_axis = inv_freq, pair_axis

@@ -234,3 +234,16 @@ def test_binding_fails_loudly_when_it_is_not_built(monkeypatch, tmp_path):
     monkeypatch.setattr(_lib, "BINDING_PATH", str(tmp_path / "missing.so"))
     with pytest.raises(ImportError, match="build"):
         _lib.binding()
+
+
+@pytest.mark.parametrize("given", ["summary", "exponents"])
+def test_a_step_wants_summary_and_exponents_together(given):
+    """One without the other: neither may be made up beside it."""
+    kc = z(4, 2, 16, 64, dtype=bf)
+    both = dict(zip(("summary", "exponents"), api.alloc_block_summary(kc)))
+    args = (kc, kc, z(3, 8), z(3), z(3), z(32, dtype=torch.float64), 4, 4)
+    with pytest.raises(ValueError, match="summary and exponents"):
+        api.SparseDecodeStep(*args, **{given: both[given]})
+    step = api.SparseDecodeStep(*args, **both)
+    assert step.summary is both["summary"] and step.exponents is both["exponents"]
+    assert api.SparseDecodeStep(*args).summary.shape == (4, 2, 2, 64)
