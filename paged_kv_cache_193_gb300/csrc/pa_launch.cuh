@@ -11,6 +11,9 @@ namespace pa {
 // First in a kernel launched by launch_dependent, before any global access, in
 // every thread: waits until the kernel before it on the stream is done and its
 // writes are visible (as that kernel's own wait does for the one before it).
+// Plain loads are ordered behind it.  Read-only ones (__ldg, ld.global.nc) are
+// not for memory that a kernel before may write: they hold for memory that nobody
+// writes while this kernel is there, and it is there early.
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Once every CTA of the grid has come by here, or has ended, the kernel after

@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     if constexpr (CHOOSE)
         if (a.longest_first) s = longest_row(a.context_lens, gridDim.z, s, join);
 
-    const float k_scale = FP8 ? (a.k_scales ? __ldg(a.k_scales + h) : a.kv_scale) : 1.f;
-    const float v_scale = FP8 ? (a.v_scales ? __ldg(a.v_scales + h) : a.kv_scale) : 1.f;
+    const float k_scale = FP8 ? (a.k_scales ? a.k_scales[h] : a.kv_scale) : 1.f;
+    const float v_scale = FP8 ? (a.v_scales ? a.v_scales[h] : a.kv_scale) : 1.f;
     const float score_scale = a.softmax_log2 * k_scale;
 
     Chosen chosen{0, nullptr};
@@ -169,12 +169,12 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
 #pragma unroll
             for (int kk = 0; kk < C::KSTEPS; ++kk) {
                 if constexpr (!FP8) {
-                    qf[kk][nt][0] = live ? __ldg(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 2 * c)) : 0u;
-                    qf[kk][nt][1] = live ? __ldg(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 8 + 2 * c)) : 0u;
+                    qf[kk][nt][0] = live ? *reinterpret_cast<const uint32_t *>(qg + kk * 16 + 2 * c) : 0u;
+                    qf[kk][nt][1] = live ? *reinterpret_cast<const uint32_t *>(qg + kk * 16 + 8 + 2 * c) : 0u;
                 } else {
                     // permuted order, as the K bytes below: this thread's dims
                     // are c*16*CPT + 4*kk + {0,1,2,3}
-                    const uint2 w = live ? __ldg(reinterpret_cast<const uint2 *>(qg + c * 16 * C::CPT + 4 * kk))
+                    const uint2 w = live ? *reinterpret_cast<const uint2 *>(qg + c * 16 * C::CPT + 4 * kk)
                                          : make_uint2(0u, 0u);
                     const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.x));
                     const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.y));
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
             return rows_total;
         }
-        const int b = __ldg(table + j);
+        const int b = table[j];
         if (b < 0 || b >= a.num_blocks) {
             set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
             return rows_total;

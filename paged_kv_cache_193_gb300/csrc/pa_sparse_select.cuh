@@ -170,14 +170,14 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
 #pragma unroll
     for (int i = 0; i < QV; ++i) {
         const int g = min((i * kSelThreads + tid) / TPH, a.group - 1);
-        qraw[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (out_row * a.group + g) * D) + tid % TPH);
+        qraw[i] = *(reinterpret_cast<const uint4 *>(a.q + (out_row * a.group + g) * D) + tid % TPH);
     }
     // with one CTA to the row its first pages are known before the length is
     const int32_t *table = a.block_tables + static_cast<int64_t>(t) * a.max_blocks + a.sink;
     int32_t next_blk = -1;
     {
         const int at = warp * kStepPages + lane % kStepPages;
-        if (ranks == 1 && a.sink + at < a.max_blocks) next_blk = __ldg(table + at);
+        if (ranks == 1 && a.sink + at < a.max_blocks) next_blk = table[at];
     }
     int n = a.context_lens[t];
     if (n > a.max_blocks * a.block_size) {
@@ -217,7 +217,7 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
     constexpr int PPC = 32 / LPP;      // pages per copy instruction
     const int own = lane % STEP;       // the step's page that the lane looks up
     const int steps = have > warp * STEP ? (have - warp * STEP + STEP * kSelWarps - 1) / (STEP * kSelWarps) : 0;
-    if (ranks > 1 && warp * STEP + own < have) next_blk = __ldg(table + c0 + warp * STEP + own);
+    if (ranks > 1 && warp * STEP + own < have) next_blk = table[c0 + warp * STEP + own];
     const uint8_t *ring = copies + warp * a.stages * STEP * PAGE;
     const uint32_t ring_at = smem_addr(ring);
     int put = 0;
@@ -228,7 +228,7 @@ __device__ __forceinline__ Chosen choose(const SelectArgs &a, uint8_t *copies, u
         if (i < steps) {
             const int at = (i * kSelWarps + warp) * STEP + own;
             int32_t blk = next_blk;
-            next_blk = at + STEP * kSelWarps < have ? __ldg(table + c0 + at + STEP * kSelWarps) : -1;
+            next_blk = at + STEP * kSelWarps < have ? table[c0 + at + STEP * kSelWarps] : -1;
             const bool bad = blk < 0 || blk >= a.num_blocks;
             if (bad) {
                 if (at < have) set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
