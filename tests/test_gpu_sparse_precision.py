@@ -1,0 +1,73 @@
+"""What the block-sparse attention rounds: its output once, and on the way no
+more than the plain form in 32 bits does."""
+import numpy as np
+import pytest
+import torch
+
+import ops_reference as R
+from paged_kv_cache_193_gb300 import _lib  # noqa: F401
+from test_gpu_sparse import Case, api, f64  # noqa: F401  (api: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+# A probability p goes into P V as two bf16 numbers, hi = p (1 - 2^-9) cut off to bf16 and the rest: below
+# (2^-9 + 2^-7) p, rounded by at most 2^-8 of itself.  (2^-9 + 2^-7) 2^-8 < 2^-14.
+TWO_BF16 = 2.0 ** -14
+
+CASES = [
+    dict(lens=[700, 64, 333], Hq=16, Hkv=1, top_k=9),
+    dict(lens=[500, 501, 512, 3], Hq=5, Hkv=5, D=64, top_k=8),
+    dict(lens=[900, 31, 32, 33], Hq=6, Hkv=2, B=32, top_k=7),
+    dict(lens=[900, 31, 32, 33], Hq=24, Hkv=2, D=64, B=32, top_k=5),
+    dict(lens=[5000], Hq=8, Hkv=2, top_k=40),
+    dict(lens=[2000] * 90, Hq=16, Hkv=8, D=64, top_k=64),
+]
+
+
+@pytest.mark.parametrize("kw", CASES, ids=[str(i) for i in range(len(CASES))])
+def test_probabilities_keep_their_bits(api, cuda_device, kw, monkeypatch):  # noqa: F811
+    kw = dict(kw)
+    top_k = kw.pop("top_k")
+    case = Case(cuda_device, **kw)
+    s, e = case.summaries(api)
+    sel, cnt, out = case.attend(api, s, e, top_k)
+    monkeypatch.setitem(R.HALF, "bf16x2", TWO_BF16)
+    ref, bound = R.attend(f64(case.q), R.values(case.kc), R.values(case.vc), case.tables, case.lens, sel, cnt, case.scale,
+                          *case.ref_scales, probability="bf16x2")
+    off = np.abs(f64(out) - ref) - bound
+    assert off.max() <= 0, f"{off.max()}: {(off > 0).mean():.3f} of the outputs are further off"
+
+
+@pytest.mark.parametrize("D,B,Hq", [(128, 16, 4), (64, 32, 9)])
+def test_one_token_gives_its_value(api, cuda_device, D, B, Hq):  # noqa: F811
+    """Its probability is 1: the output is v, bit for bit, infinities and the largest numbers too."""
+    case = Case(cuda_device, [1, 1, 1], Hq, 1, D, B)
+    row = torch.randn(D, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    row[:4] = torch.tensor([float("inf"), float("-inf"), 3.38e38, -3.38e38]).to(torch.bfloat16)
+    for i in range(3):
+        case.vc[case.tables[i, 0], 0, 0] = (row * (1 + i)).to(cuda_device)
+    s, e = case.summaries(api)
+    _, _, out = case.attend(api, s, e, 4)
+    for i in range(3):
+        want = (row * (1 + i)).to(cuda_device)
+        assert torch.equal(out[i], want[None].expand(Hq, D))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_infinite_and_nan_values_reach_the_outputs_that_hold_them(api, cuda_device, fp8):  # noqa: F811
+    case = Case(cuda_device, [777, 60], 8, 2, fp8=fp8)
+    s, e = case.summaries(api)
+    _, _, base = case.attend(api, s, e, 12)
+    page = int(case.tables[0, 0])  # the first page is always read
+    v = case.vc.view(torch.float8_e4m3fn) if fp8 else case.vc
+    wrong = {3: float("nan")} if fp8 else {3: float("inf"), 70: float("-inf"), 99: float("nan")}
+    for d, x in wrong.items():
+        v[page, 1, 5, d] = torch.tensor(x).to(v.dtype)
+    _, _, out = case.attend(api, s, e, 12)
+    for d, x in wrong.items():
+        got = out[0, 4:, d].float()
+        assert got.isnan().all() if x != x else (got == x).all()
+    rest = torch.ones_like(out, dtype=torch.bool)
+    for d in wrong:
+        rest[0, 4:, d] = False
+    assert torch.equal(out[rest], base[rest]) and api.device_errors() == 0
