@@ -285,6 +285,11 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     // maximum exceeds it by more than kLazy (base-2 units): they stay below
     // 2^kLazy and the accumulator is rescaled rarely
     constexpr float kLazy = 8.f;
+    // With an E4M3 cache they go into P V in fp16, which holds V's codes: eleven bits
+    // down to 2^-14 and ever fewer below.  Taken times 2^7 they stay in its range,
+    // below 2^15, and keep their bits down to 2^-21 (a long list's small ones add up:
+    // outputs of 6000 tokens, most at 2^-23, were up to 14% off without).
+    constexpr float kRaise = FP8 ? 7.f : 0.f;
     float m_ref[NT][2], l_run[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -438,7 +443,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     // no finite score so far: any reference will do for the zeros
-                    const float ref = m_ref[nt][j] == -INFINITY ? 0.f : m_ref[nt][j];
+                    const float ref = m_ref[nt][j] == -INFINITY ? 0.f : m_ref[nt][j] - kRaise;
                     float sum = 0.f;
 #pragma unroll
                     for (int mi = 0; mi < MI; ++mi)

@@ -71,3 +71,34 @@ def test_infinite_and_nan_values_reach_the_outputs_that_hold_them(api, cuda_devi
     for d in wrong:
         rest[0, 4:, d] = False
     assert torch.equal(out[rest], base[rest]) and api.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,B,Hq", [(128, 16, 4), (64, 32, 9), (128, 32, 16), (64, 16, 1)])
+def test_many_small_probabilities_count_in_full(api, cuda_device, D, B, Hq):  # noqa: F811
+    """A token in each of the first 32 pages takes nearly all of the softmax and has value 0, thousands have some 2^-23 of
+    it each and the same value.  The probabilities are fp16 times 2^7: each is off by at most 2^-25 2^-7 of the largest,
+    and by 2^-16 of itself through its fp32 score."""
+    n, few, value = 6000, 32, 384.0
+    case = Case(cuda_device, [n], Hq, 1, D, B, fp8=True)
+    case.kc.zero_()
+    case.vc.zero_()
+    k, v = case.kc.view(torch.float8_e4m3fn), case.vc.view(torch.float8_e4m3fn)
+    live = torch.from_numpy(case.tables[0].astype(np.int64)).to(cuda_device)
+    v[live] = torch.tensor(value).to(v.dtype)
+    for page in live[:few].tolist():
+        v[page, 0, 2] = torch.tensor(0.0).to(v.dtype)
+        k[page, 0, 2, 0] = torch.tensor(16.0).to(k.dtype)
+    case.q.zero_()
+    # score of those: scale kv_scale 16 q0 = ln(2^23 / 1.5) and a little less from head to head
+    q0 = torch.linspace(1.0, 0.98, Hq) * float(np.log(2.0 ** 23 / 1.5)) / (case.scale * case.kv_scale * 16)
+    case.q[0, :, 0] = q0.to(torch.bfloat16).to(cuda_device)
+    top_k = -(-n // B)
+    sel = torch.arange(top_k, dtype=torch.int32, device=cuda_device)[None, None].contiguous()
+    cnt = torch.full((1, 1), top_k, dtype=torch.int32, device=cuda_device)
+    p = (n - few) * np.exp(-f64(case.q)[0, :, 0] * case.scale * case.kv_scale * 16)
+    want = p / (few + p) * value * case.kv_scale
+    bound = (2.0 ** -8 + 2.0 ** -16) * want + n * 2.0 ** -32 / few * value * case.kv_scale
+    for splits in (1, 4):
+        out = api.sparse_decode(case.q, case.kc, case.vc, case.bt, case.cl, sel, cnt, case.scale, case.kv_scale, splits=splits)
+        off = np.abs(f64(out)[0] - want[:, None])
+        assert (off <= bound[:, None]).all(), (off / want[:, None]).max()
