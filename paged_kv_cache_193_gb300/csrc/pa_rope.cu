@@ -8,11 +8,12 @@
 // theta = position * inv_freq[i]:
 //   x'_a = m (x_a cos theta - x_b sin theta)
 //   x'_b = m (x_a sin theta + x_b cos theta)
-// The angle is reduced exactly: inv_freq / 2 pi, taken modulo one turn, is
-// held as a 64-bit fraction F of a turn, and position * F modulo 2^64 is the
-// angle as a fraction of a turn with no rounding in the product, however far
-// the position.  One rounding of F (2^-53 relative) times the position is
-// all that is lost before sine and cosine are taken in fp32.
+// The angle is reduced in whole numbers: inv_freq / 2 pi, taken modulo one
+// turn, is held as a 64-bit fraction F of a turn, and position * F modulo 2^64
+// is the angle as a fraction of a turn with no rounding in the product.  F is off
+// by at most 2^-64 turns plus 2^-61 inv_freq, so the angle by |position| times
+// that: below 2^-29 turns at any position for frequencies up to 1.  Its upper 32
+// bits go to sine and cosine as an fp32 number of half turns, within 2^-24.
 //
 // Bound: memory.  Every q, k, v element is read once and written once: 8192
 // tokens of 32 query and 8 KV heads, 201 MB, take 35 us, where a library copy of
