@@ -79,3 +79,81 @@ def test_small_frequencies_at_far_positions(cuda_device, adjacent):
         slack = angle_slack(x, pos.numpy(), freq.numpy(), adjacent)
         off = np.abs(got.double().cpu().numpy() - want) - (R.HALF["bf16"] * (np.abs(want) + slack) + slack)
         assert off.max() <= 0, np.unravel_index(off.argmax(), off.shape)
+
+
+def by_differences(q, k, v, freq, apart, scale):
+    """(out [H, D], bound [H, D]): attention of one query to T tokens ``apart`` positions away, in 64 bits, each score
+    from the difference of positions alone, and how far a decode over rows rotated by the positions themselves may be.
+
+    An element of a rotated row is off by 2^-21 of its pair in fp32 and by at most 2^-8 of itself in bf16, so score t by
+    e_t = scale sum_d ((2^-8 + 2^-20) (|q'_d| |k'_d|) 2 + 2^-16 |q'_d| |k'_d|), with |x'_d| at most its pair's length, and by
+    2^-17 (128 fp32 products of at most that, 2^-24 each).  The probabilities p then become p_t exp(d_t) / sum, |d_t| <= e_t, and
+    are off by at most p_t (exp(e_t + e) - 1) with exp(e) = sum_t p_t exp(e_t); one more 2^-8 for their rounding to bf16
+    and one for the output's."""
+    H, D = q.shape
+    half = D // 2
+    group = H // k.shape[1]
+    out, bound = np.zeros((H, D)), np.zeros((H, D))
+    turn = np.exp(1j * np.outer(apart, freq))
+    for h in range(H):
+        qc = q[h, :half] + 1j * q[h, half:]
+        kc = k[:, h // group, :half] + 1j * k[:, h // group, half:]
+        z = scale * ((qc * kc.conj()) * turn).real.sum(1)
+        p = np.exp(z - z.max())
+        p /= p.sum()
+        out[h] = p @ v[:, h // group]
+        # |q_a k_a| + |q_b k_b| of two rotated pairs is at most the product of their lengths
+        size = scale * (np.abs(qc) * np.abs(kc)).sum(1)
+        e = (2 * (2.0 ** -8 + 2.0 ** -20) + 2.0 ** -16) * size + 2.0 ** -17 * size
+        moved = p * (np.exp(e + np.log(p @ np.exp(e))) - 1)
+        bound[h] = moved @ np.abs(v[:, h // group] - out[h])
+        bound[h] += 2.0 ** -8 * (p + moved) @ np.abs(v[:, h // group]) + 2.0 ** -8 * (np.abs(out[h]) + bound[h])
+    return out, bound
+
+
+def _sequence():
+    T, Hq, Hkv, D = 48, 4, 2, 128
+    g = torch.Generator().manual_seed(4)
+    # every key is much like every query, so a score is a sum of cosines that falls off with the distance
+    alike = torch.randn(D, generator=g)
+    q, k = (1.5 * alike + 0.2 * torch.randn(T, h, D, generator=g) for h in (Hq, Hkv))
+    v = torch.randn(T, Hkv, D, generator=g)
+    q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+    freq = 30.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))
+    apart = (T // 2 - np.arange(T)).astype(np.float64)  # the query stands in the middle
+    return q, k, v, freq, apart
+
+
+def _exact(moved=0):
+    q, k, v, freq, apart = _sequence()
+    return by_differences(q[-1].double().numpy(), k.double().numpy(), v.double().numpy(), freq.numpy(), apart + moved, 128 ** -0.5)
+
+
+def test_a_shift_of_one_position_is_past_the_bound():
+    """The test below can fail: with the query one position off, three quarters of the outputs are past its bound, half
+    past twice the bound."""
+    (want, bound), (a, _), (b, _) = _exact(), _exact(1), _exact(-1)
+    for wrong in (a, b):
+        assert (np.abs(wrong - want) > bound).mean() > 0.7 and (np.abs(wrong - want) > 2 * bound).mean() > 0.5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [0, 4096, -70000, 2 ** 31 - 48])
+def test_rotated_attention_is_that_of_the_differences(cuda_device, first):
+    """Through the cache, at near and far positions: the attention that the differences of positions alone define."""
+    from paged_kv_cache_193_gb300 import api
+    q, k, v, freq, apart = _sequence()
+    (T, Hkv, D), B = k.shape, 16
+    kc = torch.zeros(T // B, Hkv, B, D, dtype=torch.bfloat16, device=cuda_device)
+    vc = torch.zeros_like(kc)
+    pos = torch.arange(first, first + T, dtype=torch.int64).to(torch.int32).to(cuda_device)
+    slots = torch.arange(T, dtype=torch.int32, device=cuda_device)
+    f = freq.to(cuda_device)
+    api.rope_append(None, k.to(cuda_device), v.to(cuda_device), pos, f, slots, kc, vc)
+    one = k[:1].to(cuda_device)
+    rq = api.rope_append(q[-1:].to(cuda_device), one, one, pos[T // 2:T // 2 + 1].contiguous(), f, slots[:1] - 1, kc, vc)
+    out = api.decode(rq, kc, vc, torch.arange(T // B, dtype=torch.int32, device=cuda_device)[None],
+                     torch.tensor([T], dtype=torch.int32, device=cuda_device))
+    want, bound = _exact()
+    off = np.abs(out[0].double().cpu().numpy() - want) - bound
+    assert off.max() <= 0, off.max()
