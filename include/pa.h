@@ -467,7 +467,7 @@ pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t
  * decode attention over a chosen part of a long context.  The pages motivate
  * contexts of 128K tokens ("vLLM PagedAttention Optimization: Complete
  * Step-by-Step Tuning Guide", Step 1) and attend to all of them; reading only
- * the pages with the largest bound on q . k is this library's own.
+ * the pages with the largest estimate of a bound of q . k is this library's own.
  *
  * pa_block_summary: for every slot of slot_mapping that is the LAST row of its
  *   block (slot % block_size == block_size - 1; others, and negative ones, do
@@ -492,6 +492,10 @@ pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t
  *   holding an infinity or NaN counts as zero), ties to the lower block; a
  *   block with e = 127 scores +infinity, one outside the pool -infinity (and
  *   PA_DEVERR_BAD_BLOCK).  The scores are exact, so the choice is unique.
+ *   score(j) estimates the largest q . k that the block's bounds allow: both
+ *   sides are rounded to the nearest, half a unit (2^e) per element at most, so it
+ *   may lie below a q . k of the block.  Elements far below the largest of their
+ *   block or query keep few levels.
  *   The other blocks' bounds must have been made by pa_block_summary.
  *   selected int32 [num_rows][num_kv_heads][top_k]: ascending logical blocks,
  *   then -1; counts int32 [num_rows][num_kv_heads].  recent_blocks >= 1,

@@ -556,7 +556,7 @@ def sparse_select(q: torch.Tensor, summary: torch.Tensor, exponents: torch.Tenso
                   counts: torch.Tensor | None = None, stream=None):
     """The ``top_k`` logical blocks each (row, KV head) should attend to: the
     first ``sink_blocks``, the last ``recent_blocks`` and those with the
-    largest bound of q . k (pa_sparse_select).  Returns (selected int32
+    largest estimate of a bound of q . k (pa_sparse_select).  Returns (selected int32
     [S, Hkv, top_k] ascending then -1, counts int32 [S, Hkv])."""
     if selected is None or counts is None:
         selected, counts = _choice(q, summary.shape[1], top_k, selected, counts, stream)

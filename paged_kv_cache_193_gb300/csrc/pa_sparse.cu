@@ -1,6 +1,6 @@
 // Which pages a decode step attends to: int8 bounds of every full page's keys
-// (block summary), and the choice of the pages whose bound of q . k is
-// largest (sparse select).  The pages motivate contexts of 128K tokens ("vLLM
+// (block summary), and the choice of the pages with the largest estimate of a
+// bound of q . k (sparse select).  The pages motivate contexts of 128K tokens ("vLLM
 // PagedAttention Optimization: Complete Step-by-Step Tuning Guide", Step 1)
 // and attend to all of them; attending to a chosen part is this library's own.
 //
@@ -8,10 +8,17 @@
 // k_t,d and lo_d = min_t k_t,d.  Then for any query q,
 //   q . k_t <= sum_d max(q_d hi_d, q_d lo_d).
 // hi, lo and q are held as whole numbers of at most 127 times a power of two
-// shared by the page and head (by the query head), so the bound is a whole
+// shared by the page and head (by the query head), so the score is a whole
 // number, the sum has no rounding and no order, and two pages compare the
 // same way on any machine.  Eight bits with a shared power of two are coarse
-// (steps of 1/64 to 1/127 of the largest value) but only rank pages.
+// (steps of 1/64 to 1/127 of the largest value) and rounded to the nearest, not
+// outward: with u_k and u_q the two units, the score is within
+//   sum_d (u_k |q_d| + u_q max(|hi_d|, |lo_d|) + u_k u_q / 2) / 2
+// of the bound (of values in the exponents' range), and below it about as often
+// as above.  It ranks pages and bounds nothing.  Of 128 of 2,048 pages that the bound itself would choose it finds 97%
+// on normal keys, 90% where four dims are 15 times the others (69% for the worst
+// of 1,280 queries), 84% where two are 50 times them (36%): the largest dim sets
+// the unit of all.
 #include "pa_sparse_select.cuh"
 
 namespace pa {
