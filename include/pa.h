@@ -508,8 +508,9 @@ pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t
  *   sequence's blocks contributes nothing and sets PA_DEVERR_BAD_BLOCK.
  *   Cache types and scales as pa_rope_append; softmax_scale > 0.  splits: CTAs
  *   that share a (row, KV head)'s list, 1, 2, 4 or 8; 0 lets the library
- *   choose.  One kernel, no workspace.  With an E4M3 cache the query is
- *   rounded to fp16 as in pa_decode_partitions.
+ *   choose.  One kernel, no workspace.  out may be q itself and may not overlap
+ *   it otherwise.  With an E4M3 cache the query is rounded to fp16 as in
+ *   pa_decode_partitions.
  * pa_sparse_attend: pa_sparse_select followed by pa_sparse_decode; selected and
  *   counts are outputs.  One kernel, in which each (row, KV head)'s CTAs choose
  *   and attend, so that one row's attention hides another's choice.

@@ -20,6 +20,12 @@ __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.
 // this one may be put on the SMs.
 __device__ __forceinline__ void dependent_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// whether np bytes from p on and nq bytes from q on have any in common
+inline bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + nq && b < a + np;
+}
+
 // `cluster` CTAs along x to a thread-block cluster (0: none).
 template <class... Params, class... Actual>
 inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,

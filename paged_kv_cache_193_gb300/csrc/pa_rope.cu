@@ -299,11 +299,6 @@ static cudaError_t launch(const Args &a, bool adjacent, dim3 grid, cudaStream_t 
     return adjacent ? launch_ctas<D, FP8, true>(a, grid, stream) : launch_ctas<D, FP8, false>(a, grid, stream);
 }
 
-static bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + nq && b < a + np;
-}
-
 }  // namespace rope
 }  // namespace pa
 
@@ -363,12 +358,12 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
         return fail(PA_ERR_INVALID_ARG, "a token stride is smaller than one token's rows");
     if (num_q_heads > 0 && !(q == q_out && (num_tokens == 1 || q_stride == qrow))) {
         const size_t span = (static_cast<size_t>(num_tokens - 1) * q_stride + qrow) * 2;
-        if (rope::overlaps(q, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
+        if (overlaps(q, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
             return fail(PA_ERR_INVALID_ARG, "q_out overlaps q but is not q itself");
     }
     for (const auto &[rows, stride] : {std::pair(k, k_stride), std::pair(v, v_stride)}) {
         const size_t span = (static_cast<size_t>(num_tokens - 1) * stride + krow) * 2;
-        if (num_q_heads > 0 && rope::overlaps(rows, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
+        if (num_q_heads > 0 && overlaps(rows, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
             return fail(PA_ERR_INVALID_ARG, "q_out overlaps k or v");
     }
     unsigned int *err = device_error_word();

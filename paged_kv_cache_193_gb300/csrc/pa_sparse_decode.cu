@@ -39,6 +39,9 @@ static pa_status check_pointers(const Call &c) {
         return fail(PA_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(c.q) || !aligned16(c.k_cache) || !aligned16(c.v_cache) || !aligned16(c.out))
         return fail(PA_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
+    const size_t bytes = static_cast<size_t>(c.num_rows) * c.num_q_heads * c.head_dim * 2;
+    if (c.out != c.q && overlaps(c.q, bytes, c.out, bytes))
+        return fail(PA_ERR_INVALID_ARG, "out overlaps q but is not q itself");
     return PA_OK;
 }
 

@@ -247,3 +247,12 @@ def test_a_step_wants_summary_and_exponents_together(given):
     step = api.SparseDecodeStep(*args, **both)
     assert step.summary is both["summary"] and step.exponents is both["exponents"]
     assert api.SparseDecodeStep(*args).summary.shape == (4, 2, 2, 64)
+
+
+@pytest.mark.parametrize("fn", ["decode", "attend"])
+def test_an_output_that_overlaps_the_query_is_refused(lib, fn):
+    """In place is fine, a shifted overlap is not: outputs would be written over queries still to be read."""
+    rows = 4 * 8 * 128 * 2  # bytes of the query of _select's call
+    for off in (16, rows - 16, -16, 16 - rows):
+        assert _select(lib, fn, out=ctypes.c_void_p((1 << 20) + off)) == 1
+        assert b"overlap" in lib.pa_last_error()
