@@ -13,10 +13,11 @@
 // there is no workspace and no second kernel however few rows there are.
 //
 // Bound by memory: a page is read once and used for all queries of its KV head.
-// 64 sequences of 4K-32K tokens, 64 / 8 heads, top 128: 689 MB in 112 us with the
+// 64 sequences of 4K-32K tokens, 64 / 8 heads, top 128: 689 MB in 113 us with the
 // choice, 6.1 TB/s (0.90 of a copy's rate); 256 sequences of 512-2,048 tokens, top
-// 32: 575 MB in 99.6 us, 5.8 TB/s.  With few rows by latency: one sequence of
-// 5,003 tokens, top 64, 10.2 us.
+// 32: 575 MB in 100.6 us, 5.7 TB/s.  Over a list that is there the pages alone take
+// 80 us in both, 6.7 TB/s.  With few rows by latency: one sequence of 5,003 tokens,
+// top 64, 10.4 us.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     // maximum exceeds it by more than kLazy (base-2 units): they stay below
     // 2^kLazy and the accumulator is rescaled rarely
     constexpr float kLazy = 8.f;
-    // With an E4M3 cache they go into P V in fp16, which holds V's codes: eleven bits
-    // down to 2^-14 and ever fewer below.  Taken times 2^7 they stay in its range,
+    // With an E4M3 cache they go into P V in fp16, which holds V's codes: rounded by
+    // 2^-11, an eighth of the output's own rounding, down to 2^-14 and ever more below.  Taken times 2^7 they stay in its range,
     // below 2^15, and keep their bits down to 2^-21 (a long list's small ones add up:
     // outputs of 6000 tokens, most at 2^-23, were up to 14% off without).
     constexpr float kRaise = FP8 ? 7.f : 0.f;
