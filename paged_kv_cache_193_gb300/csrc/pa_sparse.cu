@@ -15,10 +15,10 @@
 // outward: with u_k and u_q the two units, the score is within
 //   sum_d (u_k |q_d| + u_q max(|hi_d|, |lo_d|) + u_k u_q / 2) / 2
 // of the bound (of values in the exponents' range), and below it about as often
-// as above.  It ranks pages and bounds nothing.  Of 128 of 2,048 pages that the bound itself would choose it finds 97%
-// on normal keys, 90% where four dims are 15 times the others (69% for the worst
-// of 1,280 queries), 84% where two are 50 times them (36%): the largest dim sets
-// the unit of all.
+// as above.  It ranks pages and bounds nothing.  Of 128 of 2,048 pages that the
+// bound itself would choose it finds 97% on normal keys, 90% where four dims are
+// 15 times the others (69% for the worst of 1,280 queries), 84% where two are 50
+// times them (36%): the largest dim sets the unit of all.
 #include "pa_sparse_select.cuh"
 
 namespace pa {

@@ -287,10 +287,11 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     // 2^kLazy and the accumulator is rescaled rarely
     constexpr float kLazy = 8.f;
     // With an E4M3 cache they go into P V in fp16, which holds V's codes: rounded by
-    // 2^-11, an eighth of the output's own rounding, down to 2^-14 and ever more below.  Taken times 2^7 they stay in its range,
-    // below 2^15, and keep their bits down to 2^-21 (a long list's small ones add up:
-    // outputs of 6000 tokens, most at 2^-23, were up to 14% off without).
-    constexpr float kRaise = FP8 ? 7.f : 0.f;
+    // 2^-11, an eighth of the output's own rounding, down to 2^-14 and ever more
+    // below.  Taken times 2^7 they stay in its range, up to 2^15, and keep their bits
+    // down to 2^-21 (a long list's small ones add up: outputs of 6000 tokens, most at
+    // 2^-23, were up to 14% off without).
+    constexpr float kRaise = 7.f;
     float m_ref[NT][2], l_run[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -444,13 +445,15 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     // no finite score so far: any reference will do for the zeros
-                    const float ref = m_ref[nt][j] == -INFINITY ? 0.f : m_ref[nt][j] - kRaise;
+                    const float ref = m_ref[nt][j] == -INFINITY ? 0.f : m_ref[nt][j];
                     float sum = 0.f;
 #pragma unroll
                     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
                         for (int hi = 0; hi < 2; ++hi) {
-                            const float pr = fast_exp2(sc[mi][nt][hi * 2 + j] - ref);
+                            float y = sc[mi][nt][hi * 2 + j] - ref;
+                            if constexpr (FP8) y += kRaise;  // not to the reference, which may be large
+                            const float pr = fast_exp2(y);
                             sc[mi][nt][hi * 2 + j] = pr;
                             sum += pr;
                         }

@@ -102,3 +102,35 @@ def test_many_small_probabilities_count_in_full(api, cuda_device, D, B, Hq):  # 
         out = api.sparse_decode(case.q, case.kc, case.vc, case.bt, case.cl, sel, cnt, case.scale, case.kv_scale, splits=splits)
         off = np.abs(f64(out)[0] - want[:, None])
         assert (off <= bound[:, None]).all(), (off / want[:, None]).max()
+
+
+@pytest.mark.parametrize("step", [8])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scores_past_the_whole_numbers_of_fp32(api, cuda_device, fp8, step):  # noqa: F811
+    """A score of 3 * 2^23 and one 8 above, or of 2^27 + 16 and one 16 above, in powers of two: fp32 steps by 2 and by 16
+    there.  The second token, in a later page of the same warp, weighs 2^step against the first, all others nothing."""
+    D, n = 128, 400
+    case = Case(cuda_device, [n], 4, 1, D, 16, fp8=fp8)
+    case.kc.zero_()
+    case.vc.zero_()
+    scale = float(np.float32(2) / np.float32(1.4426950408889634))
+    assert np.float32(scale) * np.float32(1.4426950408889634) == 2  # a product q . k counts twice
+    k, v = (c.view(torch.float8_e4m3fn) if fp8 else c for c in (case.kc, case.vc))
+    put = lambda t, at, x: t.__setitem__(at, torch.tensor(x).to(t.dtype))  # noqa: E731
+    dims, size, unit, extras = (1, 49152.0, 4.0, (0.0, 1.0)) if step == 8 else (8, 32768.0, 8.0, (1.0, 2.0))
+    case.q.zero_()
+    case.q[0, :, :dims], case.q[0, :, 64] = size, unit
+    for page, extra, value in ((int(case.tables[0, 0]), extras[0], 3.0), (int(case.tables[0, 16]), extras[1], 5.0)):
+        for d in range(dims):
+            put(k, (page, 0, 2, d), 256.0)
+        put(k, (page, 0, 2, 64), extra)
+        put(v, (page, 0, 2), value)
+    x = [2 * (dims * size * 256 + unit * e) for e in extras]
+    assert x[1] - x[0] == step and all(np.float32(y) == y for y in x)
+    sel = torch.arange(25, dtype=torch.int32, device=cuda_device)[None, None].contiguous()
+    cnt = torch.full((1, 1), 25, dtype=torch.int32, device=cuda_device)
+    want = (3 + 2 ** step * 5) / (1 + 2 ** step)
+    for splits in (1, 2, 4, 8):
+        out = api.sparse_decode(case.q, case.kc, case.vc, case.bt, case.cl, sel, cnt, scale, 1.0, splits=splits)
+        off = (out.float() - want).abs().max().item()
+        assert off <= 2.0 ** -8 * want, off
