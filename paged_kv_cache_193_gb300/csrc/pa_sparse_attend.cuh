@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                     mx[nt][j] = m;
-                    grow |= m > m_ref[nt][j] + kLazy;
+                    grow |= m - m_ref[nt][j] > kLazy;  // the difference: a large score's sum would round
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll

@@ -104,7 +104,7 @@ def test_many_small_probabilities_count_in_full(api, cuda_device, D, B, Hq):  # 
         assert (off <= bound[:, None]).all(), (off / want[:, None]).max()
 
 
-@pytest.mark.parametrize("step", [8])
+@pytest.mark.parametrize("step", [8, 16])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_scores_past_the_whole_numbers_of_fp32(api, cuda_device, fp8, step):  # noqa: F811
     """A score of 3 * 2^23 and one 8 above, or of 2^27 + 16 and one 16 above, in powers of two: fp32 steps by 2 and by 16
