@@ -544,6 +544,120 @@ pa_status pa_sparse_attend(const void *q, const void *k_cache, const void *v_cac
                            cudaStream_t stream);
 
 /*
+ * pa_norm_rope_append -- pa_rope_append for models that normalise every head's
+ * query and key row first (root-mean-square norm), in the same kernel.
+ * Source: as pa_rope_append; the pages leave the norm, like the rotation, to
+ * the model.
+ *   Each row x of q and k (one token, one head, head_dim elements) becomes
+ *     x_d * 1 / sqrt(mean_d x_d^2 + eps) * (weight_offset + weight_d)
+ *   in fp32 before it is rotated, with no rounding between; v is not
+ *   normalised.  Everything else is as in pa_rope_append.
+ *   q_weight, k_weight  bf16 (device, 16-byte aligned): head h's weights are the
+ *                 head_dim elements from h * q_weight_stride (k_weight_stride)
+ *                 on; stride 0: all heads have the same.  A stride is a multiple
+ *                 of 8.  NULL: no weights (1, whatever the offset).  q_out may
+ *                 not overlap them.
+ *   weight_offset finite; 0, or 1 for weights that are stored around 0
+ *   eps           finite, at least 1e-12
+ *   Elements are below 2^59 in magnitude: the sum of squares is taken in fp32.
+ */
+pa_status pa_norm_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, const void *q_weight,
+                              int64_t q_weight_stride, const void *k_weight, int64_t k_weight_stride,
+                              float weight_offset, float eps, const int32_t *positions, int num_axes,
+                              const double *inv_freq, const int32_t *pair_axis, int rotary_dim,
+                              int adjacent, float magnitude, const int32_t *slot_mapping,
+                              int num_tokens, int num_q_heads, void *q_out, void *k_cache,
+                              void *v_cache, int num_blocks, int num_kv_heads, int head_dim,
+                              int block_size, pa_kv_dtype kv_dtype, float kv_scale,
+                              const float *k_scales, const float *v_scales, cudaStream_t stream);
+
+/*
+ * pa_shared_prefix_decode -- decode attention of a batch whose sequences share,
+ * in groups, the first pages of their contexts; each group's prefix is read and
+ * multiplied once for all of its sequences.
+ * Source: "Optimizing Llama 3.1 405B Inference with vLLM PagedAttention",
+ * section "PagedAttention Mechanics", and "vLLM PagedAttention: Memory
+ * Optimization & High-Throughput LLM Inference Tuning", section 2: sequences may
+ * point at the same physical pages.  The pages say nothing of the attention
+ * over them; taking a prefix once for its group is this library's own.
+ *   The result is pa_decode's: for every sequence s and query head hq the
+ *   softmax over all of its context_lens[s] tokens; zeros for none.
+ *   group_start   int32 [num_groups + 1] (device), ascending: group g is the
+ *                 sequences group_start[g] .. group_start[g + 1] - 1 (none, if the
+ *                 two are equal); those in no group share nothing.
+ *   prefix_blocks int32 [num_groups] (device): the first prefix_blocks[g] entries
+ *                 of the group's table rows are the same physical blocks.  A
+ *                 sequence that has fewer tokens than those hold (a padded row of
+ *                 none, for instance) is attended to by itself, through its own
+ *                 table row.
+ *   max_prefix_blocks  a bound for the launch: of longer prefixes so many blocks
+ *                 are taken together, the others for each sequence.  At most
+ *                 max_blocks_per_seq.
+ *   num_groups <= num_seqs; 0 groups, or max_prefix_blocks 0: nothing is shared,
+ *                 and group_start, prefix_blocks and workspace may be NULL.
+ *   workspace     pa_shared_prefix_workspace_size bytes, 16-byte aligned, which
+ *                 may overlap neither q nor out; nothing in it has to start at
+ *                 zero.  Calls that may run at the same time need one each.
+ *   Cache types and scales as pa_rope_append; softmax_scale > 0; group 1..16.
+ *   out may be q itself and may not overlap it otherwise.  With an E4M3 cache
+ *   the query is rounded to fp16 as in pa_decode_partitions.  Two kernels (one
+ *   when nothing is shared).
+ */
+size_t pa_shared_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads,
+                                       int num_kv_heads, int head_dim, int block_size,
+                                       int max_prefix_blocks);
+pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *context_lens, int num_seqs,
+                                  const int32_t *group_start, const int32_t *prefix_blocks,
+                                  int num_groups, int max_prefix_blocks, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                  pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
+                                  const float *v_scales, float softmax_scale, void *workspace,
+                                  size_t workspace_bytes, void *out, cudaStream_t stream);
+
+/*
+ * pa_cross_attention -- attention of a sequence's rows to all of an encoder's
+ * states, whose keys and values are in the paged cache (written there once, by
+ * pa_cache_append).
+ * Source: "vLLM PagedAttention: Memory Optimization & High-Throughput LLM
+ * Inference Tuning", section 2, for the walk through the block table; the pages
+ * speak of decoders alone, and rows that are not part of the context they
+ * attend to are this library's own.
+ *   q, out        bf16 [num_tokens][num_q_heads][head_dim]
+ *   query_start   int32 [num_seqs + 1] (device), ascending within 0 .. num_tokens:
+ *                 sequence s has the rows query_start[s] .. query_start[s + 1] - 1
+ *                 (none, one decoded token, several beams, a chunk); rows of no
+ *                 sequence are left as they were.
+ *   state_lens    int32 [num_seqs] (device): the states of each sequence
+ *   max_query_len the most rows of a sequence (a bound for the launch).  A
+ *                 sequence with more, or whose rows are no range of the tokens,
+ *                 is left out and sets PA_DEVERR_BAD_CONTEXT.
+ *   out[i][hq] = bf16_rn( softmax_{t < state_lens[s]}(softmax_scale * kscale *
+ *   q[i][hq] . K[t]) . vscale * V ), not causal; zeros with no states.
+ *   workspace     pa_cross_workspace_size bytes for these sizes (0: NULL will do),
+ *                 16-byte aligned, which may overlap neither q nor out; nothing in
+ *                 it has to start at zero.  Calls that may run at the same time need
+ *                 one each.
+ *   Cache types and scales as pa_rope_append; softmax_scale > 0; group 1..16.
+ *   out may be q itself and may not overlap it otherwise.  With an E4M3 cache
+ *   the query is rounded to fp16 as in pa_decode_partitions.  One kernel, two
+ *   with a workspace.
+ */
+size_t pa_cross_workspace_size(int num_tokens, int num_seqs, int max_query_len, int num_q_heads,
+                               int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                               int block_size);
+pa_status pa_cross_attention(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, int max_blocks_per_seq,
+                             const int32_t *state_lens, const int32_t *query_start, int num_seqs,
+                             int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
+                             int head_dim, int num_blocks, int block_size, pa_kv_dtype kv_dtype,
+                             float kv_scale, const float *k_scales, const float *v_scales,
+                             float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
+                             cudaStream_t stream);
+
+/*
  * pa_decode_static_workspace -- pa_decode with partition_size > 0, without
  * the caller's workspace.
  * The source pages have no counterpart to this entry point.  It exists for

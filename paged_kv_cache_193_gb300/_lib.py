@@ -68,6 +68,14 @@ SIGNATURES = {
                               _I, _I, _P, _P]),
     "pa_sparse_attend": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _F,
                               _I, _I, _I, _P, _P, _P, _P]),
+    "pa_norm_rope_append": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _F, _F, _P, _I, _P, _P, _I, _I, _F, _P, _I,
+                                 _I, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "pa_shared_prefix_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_shared_prefix_decode": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
+                                     _P, _F, _P, _SZ, _P, _P]),
+    "pa_cross_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_cross_attention": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _F,
+                                _P, _SZ, _P, _P]),
     "pa_decode_static_workspace": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                         _F, _I, _P, _P]),
     "pa_test_set_wait": (_I, [ctypes.c_uint64, _I]),
@@ -78,7 +86,8 @@ SIGNATURES = {
 
 BINDING_PATH = os.path.join(HERE, "_build", "_pa_binding.so")
 # the calls of the CPython binding, in the order its bind() takes their addresses
-BINDING_CALLS = ("pa_rope_append", "pa_block_summary", "pa_sparse_select", "pa_sparse_decode", "pa_sparse_attend")
+BINDING_CALLS = ("pa_rope_append", "pa_block_summary", "pa_sparse_select", "pa_sparse_decode", "pa_sparse_attend",
+                 "pa_norm_rope_append", "pa_shared_prefix_decode", "pa_cross_attention")
 
 _lib = None
 _binding = None

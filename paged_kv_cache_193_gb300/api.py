@@ -525,6 +525,30 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positi
     return None if q is None else out
 
 
+def norm_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                     inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                     pair_axis: torch.Tensor | None = None, adjacent: bool = False, magnitude: float = 1.0,
+                     kv_scale: float = 1.0, k_scales: torch.Tensor | None = None,
+                     v_scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor | None:
+    """rope_append of q and k rows that are normalised first, each head's by
+    itself, in the same kernel (pa_norm_rope_append): a row becomes
+    x * rsqrt(mean(x^2) + eps) * (weight_offset + weight).
+
+    ``q_weight`` bf16 [D] or [Hq, D], ``k_weight`` [D] or [Hkv, D]; None: no
+    weights.  The other arguments are rope_append's."""
+    if out is None and isinstance(q, torch.Tensor):
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+    status = _lib.binding().norm_rope_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, pair_axis,
+                                             adjacent, magnitude, kv_scale, k_scales, v_scales, out, stream, q_weight,
+                                             k_weight, weight_offset, eps)
+    if status is not None:
+        _check(status)
+    return None if q is None else out
+
+
 def alloc_block_summary(k_cache: torch.Tensor):
     """(summary int8 [NB, Hkv, 2, D], exponents int8 [NB, Hkv]) for a cache,
     zeroed; block_summary fills in a block when its last token arrives."""
@@ -607,6 +631,143 @@ def sparse_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if status is not None:
         _check(status)
     return out
+
+
+def shared_prefix_workspace_size(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
+                                 head_dim: int, block_size: int, max_prefix_blocks: int) -> int:
+    return int(_lib_handle().pa_shared_prefix_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads,
+                                                             head_dim, block_size, max_prefix_blocks))
+
+
+def alloc_shared_prefix_workspace(q: torch.Tensor, k_cache: torch.Tensor, group_start: torch.Tensor,
+                                  max_prefix_blocks: int, stream=None) -> torch.Tensor | None:
+    """Workspace of shared_prefix_decode for these sizes (None: none needed)."""
+    S, Hq, D = q.shape
+    n = shared_prefix_workspace_size(S, group_start.shape[0] - 1, Hq, k_cache.shape[1], D, k_cache.shape[2],
+                                     max_prefix_blocks)
+    return _empty((n,), torch.uint8, q.device, stream) if n else None
+
+
+def shared_prefix_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor, group_start: torch.Tensor,
+                         prefix_blocks: torch.Tensor, max_prefix_blocks: int | None = None,
+                         softmax_scale: float | None = None, kv_scale: float = 1.0,
+                         k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Decode attention of a batch whose sequences share the first pages of
+    their contexts, each group's taken once (pa_shared_prefix_decode); returns
+    bf16 [S, Hq, D], what ``decode`` would.
+
+    ``group_start`` int32 [G + 1]: group g is sequences group_start[g] ..
+    group_start[g + 1] - 1; ``prefix_blocks`` int32 [G]: how many of the first
+    entries of their table rows are the same blocks.  ``max_prefix_blocks``: no
+    entry of prefix_blocks counts for more (None: the tables' width; a closer
+    bound launches a better shape)."""
+    if max_prefix_blocks is None:
+        max_prefix_blocks = block_tables.shape[1]
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
+    if workspace is None:
+        workspace = alloc_shared_prefix_workspace(q, k_cache, group_start, max_prefix_blocks, stream)
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    status = _lib.binding().shared_prefix_decode(q, k_cache, v_cache, block_tables, context_lens, group_start,
+                                                 prefix_blocks, max_prefix_blocks, softmax_scale, kv_scale, k_scales,
+                                                 v_scales, workspace, out, stream)
+    if status is not None:
+        _check(status)
+    return out
+
+
+def cross_workspace_size(num_tokens: int, num_seqs: int, max_query_len: int, num_q_heads: int,
+                         num_kv_heads: int, head_dim: int, max_blocks_per_seq: int, block_size: int) -> int:
+    return int(_lib_handle().pa_cross_workspace_size(num_tokens, num_seqs, max_query_len, num_q_heads, num_kv_heads,
+                                                     head_dim, max_blocks_per_seq, block_size))
+
+
+def alloc_cross_workspace(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                          max_query_len: int, stream=None) -> torch.Tensor | None:
+    """Workspace of cross_attention for these sizes (None: none needed)."""
+    T, Hq, D = q.shape
+    n = cross_workspace_size(T, block_tables.shape[0], min(max_query_len, T), Hq, k_cache.shape[1], D,
+                             block_tables.shape[1], k_cache.shape[2])
+    return _empty((n,), torch.uint8, q.device, stream) if n else None
+
+
+def cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, state_lens: torch.Tensor, query_start: torch.Tensor,
+                    max_query_len: int, softmax_scale: float | None = None, kv_scale: float = 1.0,
+                    k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Attention of each sequence's rows to all of an encoder's states in the
+    paged cache (pa_cross_attention); returns bf16 [T, Hq, D].
+
+    Sequence s has the rows query_start[s] .. query_start[s + 1] - 1 of ``q``
+    (``query_start`` int32 [S + 1]; at most ``max_query_len`` each) and the
+    first ``state_lens[s]`` tokens of its table row.  Rows of no sequence come
+    back as ``out`` had them."""
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
+    if workspace is None:
+        workspace = alloc_cross_workspace(q, k_cache, block_tables, max_query_len, stream)
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    status = _lib.binding().cross_attention(q, k_cache, v_cache, block_tables, state_lens, query_start, max_query_len,
+                                            softmax_scale, kv_scale, k_scales, v_scales, workspace, out, stream)
+    if status is not None:
+        _check(status)
+    return out
+
+
+class SharedPrefixDecodeStep:
+    """One decode step of one attention layer for a batch that shares prefixes:
+    slot mapping, rotate-and-append (with ``q_weight`` or ``k_weight`` given, or
+    ``norm`` true, of normalised q and k), attention with each group's prefix
+    taken once.  Every buffer is allocated here; calling it allocates nothing.
+    ``positions``, ``context_lens``, ``block_tables``, ``group_start`` and
+    ``prefix_blocks`` are the caller's and read at every call.  Works as a step
+    of ``StepGraph``."""
+
+    def __init__(self, k_cache, v_cache, block_tables, context_lens, positions, inv_freq, num_q_heads,
+                 group_start, prefix_blocks, max_prefix_blocks=None, softmax_scale=None, kv_scale=1.0,
+                 k_scales=None, v_scales=None, pair_axis=None, adjacent=False, magnitude=1.0, norm=False,
+                 q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0):
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.block_tables, self.context_lens, self.positions = block_tables, context_lens, positions
+        self.inv_freq, self.pair_axis = inv_freq, pair_axis
+        self.adjacent, self.magnitude = adjacent, magnitude
+        self.norm = norm or q_weight is not None or k_weight is not None
+        self.q_weight, self.k_weight, self.eps, self.weight_offset = q_weight, k_weight, eps, weight_offset
+        self.group_start, self.prefix_blocks = group_start, prefix_blocks
+        self.max_prefix_blocks = block_tables.shape[1] if max_prefix_blocks is None else max_prefix_blocks
+        self.softmax_scale = softmax_scale
+        self.kv_scale, self.k_scales, self.v_scales = kv_scale, k_scales, v_scales
+        _, _, self.B, D = k_cache.shape
+        S, dev = block_tables.shape[0], k_cache.device
+        self.slots = torch.empty(S, dtype=torch.int32, device=dev)
+        self.q_rotated = torch.empty(S, num_q_heads, D, dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty(S, num_q_heads, D, dtype=torch.bfloat16, device=dev)
+        self.workspace = alloc_shared_prefix_workspace(self.q_rotated, k_cache, group_start, self.max_prefix_blocks)
+
+    def launches(self) -> int:
+        """Kernels one call launches."""
+        return 3 if self.workspace is None else 4
+
+    def __call__(self, q, k_new, v_new, stream=None):
+        slot_mapping(self.block_tables, self.context_lens, self.B, out=self.slots, stream=stream)
+        if self.norm:
+            norm_rope_append(q, k_new, v_new, self.positions, self.inv_freq, self.slots, self.k_cache, self.v_cache,
+                             self.q_weight, self.k_weight, self.eps, self.weight_offset, self.pair_axis, self.adjacent,
+                             self.magnitude, self.kv_scale, self.k_scales, self.v_scales, self.q_rotated, stream)
+        else:
+            rope_append(q, k_new, v_new, self.positions, self.inv_freq, self.slots, self.k_cache, self.v_cache,
+                        self.pair_axis, self.adjacent, self.magnitude, self.kv_scale, self.k_scales, self.v_scales,
+                        self.q_rotated, stream)
+        return shared_prefix_decode(self.q_rotated, self.k_cache, self.v_cache, self.block_tables, self.context_lens,
+                                    self.group_start, self.prefix_blocks, self.max_prefix_blocks, self.softmax_scale,
+                                    self.kv_scale, self.k_scales, self.v_scales, self.workspace, self.out, stream)
 
 
 class SparseDecodeStep:

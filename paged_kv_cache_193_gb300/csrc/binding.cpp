@@ -1,4 +1,5 @@
-// CPython binding of the rotate-and-append and block-sparse entry points.
+// CPython binding of the rotate-and-append, block-sparse, shared-prefix and
+// cross-attention entry points.
 //
 // A decode step calls these once per layer, and on a small batch the kernels
 // take a few microseconds: checking a dozen tensors and marshalling some
@@ -29,6 +30,9 @@ decltype(&pa_block_summary) f_block_summary;
 decltype(&pa_sparse_select) f_sparse_select;
 decltype(&pa_sparse_decode) f_sparse_decode;
 decltype(&pa_sparse_attend) f_sparse_attend;
+decltype(&pa_norm_rope_append) f_norm_rope_append;
+decltype(&pa_shared_prefix_decode) f_shared_prefix_decode;
+decltype(&pa_cross_attention) f_cross_attention;
 
 // Thrown after a Python exception has been set.
 struct Raised {};
@@ -127,7 +131,7 @@ private:
         if (ndim >= 0 && t.dim() != ndim)
             raise(PyExc_ValueError, "%s must have %d dimensions (got shape %s)", name, ndim, shape_of(t).c_str());
     }
-    static constexpr int kMost = 16;
+    static constexpr int kMost = 20;
     const at::Tensor *seen_[kMost];
     const char *names_[kMost];
     int count_ = 0;
@@ -212,38 +216,120 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F &&body) {
     }
 }
 
+// A head's weights: [head_dim] for all of them, or [heads, head_dim].
+const at::Tensor *weights(Call &c, PyObject *o, const char *name, int64_t heads, int64_t dim, int64_t *stride) {
+    const at::Tensor *w = c.dense(o, name, at::kBFloat16, -1, true);
+    *stride = 0;
+    if (!w) return nullptr;
+    const bool one = w->dim() == 1 && w->size(0) == dim;
+    if (!one && !(w->dim() == 2 && w->size(0) == heads && w->size(1) == dim))
+        raise(PyExc_ValueError, "%s must be [head_dim] or [heads, head_dim] (got %s)", name, shape_of(*w).c_str());
+    if (!one) *stride = dim;
+    return w;
+}
+
+// Both appends: the first 16 arguments are theirs alike; a norm has four more.
+pa_status append(PyObject *const *a, bool norm) {
+    Call c;
+    int64_t qs = 0, ks = 0, vs = 0, qws = 0, kws = 0;
+    const at::Tensor *k = c.rows(a[1], "k", &ks), *v = c.rows(a[2], "v", &vs);
+    const Caches cc(c, a[6], a[7], a[12], a[13]);
+    const int T = size(k, 0);
+    if (v->sizes() != k->sizes() || k->size(1) != cc.heads || k->size(2) != cc.dim)
+        raise(PyExc_ValueError, "inconsistent K/V and cache shapes");
+    const at::Tensor *pos = c.dense(a[3], "positions", at::kInt);
+    if ((pos->dim() != 1 && pos->dim() != 2) || pos->size(-1) != T)
+        raise(PyExc_ValueError, "positions must be [tokens] or [axes, tokens] (got %s)", shape_of(*pos).c_str());
+    const at::Tensor *freq = c.dense(a[4], "inv_freq", at::kDouble, 1);
+    if (freq->size(0) > 65536) raise(PyExc_ValueError, "inv_freq is longer than half a head");
+    const at::Tensor *axis = c.shaped(a[8], "pair_axis", at::kInt, {freq->size(0)}, true);
+    const at::Tensor *slots = c.shaped(a[5], "slot_mapping", at::kInt, {T});
+    const at::Tensor *q = c.rows(a[0], "q", &qs, true), *out = nullptr;
+    if (q) {
+        if (q->size(0) != T || q->size(2) != cc.dim) raise(PyExc_ValueError, "inconsistent q and k shapes");
+        out = c.shaped(a[14], "out", at::kBFloat16, {T, q->size(1), cc.dim});
+    }
+    const at::Tensor *qw = nullptr, *kw = nullptr;
+    float offset = 0.f, eps = 0.f;
+    if (norm) {
+        qw = weights(c, a[16], "q_weight", q ? q->size(1) : 0, cc.dim, &qws);
+        kw = weights(c, a[17], "k_weight", cc.heads, cc.dim, &kws);
+        offset = to_float(a[18]);
+        eps = to_float(a[19]);
+    }
+    const int adjacent = PyObject_IsTrue(a[9]);
+    if (adjacent < 0) throw Raised{};
+    const float magnitude = to_float(a[10]), kv_scale = to_float(a[11]);
+    const int axes = pos->dim() == 2 ? size(pos, 0) : 1, rotary = 2 * size(freq, 0), heads = q ? size(q, 1) : 0;
+    const cudaStream_t s = c.stream(a[15]);
+    const Unlocked unlocked;
+    if (norm)
+        return f_norm_rope_append(ptr<void>(q), qs, k->data_ptr(), ks, v->data_ptr(), vs, ptr<void>(qw), qws, ptr<void>(kw), kws,
+                                  offset, eps, ptr<int32_t>(pos), axes, ptr<double>(freq), ptr<int32_t>(axis), rotary, adjacent,
+                                  magnitude, ptr<int32_t>(slots), T, heads, ptr<void>(out), cc.k->data_ptr(), cc.v->data_ptr(),
+                                  cc.blocks, cc.heads, cc.dim, cc.block, cc.type, kv_scale, ptr<float>(cc.k_scales),
+                                  ptr<float>(cc.v_scales), s);
+    return f_rope_append(ptr<void>(q), qs, k->data_ptr(), ks, v->data_ptr(), vs, ptr<int32_t>(pos), axes,
+                         ptr<double>(freq), ptr<int32_t>(axis), rotary, adjacent, magnitude, ptr<int32_t>(slots), T, heads,
+                         ptr<void>(out), cc.k->data_ptr(),
+                         cc.v->data_ptr(), cc.blocks, cc.heads, cc.dim, cc.block, cc.type, kv_scale, ptr<float>(cc.k_scales),
+                         ptr<float>(cc.v_scales), s);
+}
+
 PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 16, [&] {
+    return guarded(n, 16, [&] { return append(a, false); });
+}
+
+PyObject *norm_rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 20, [&] { return append(a, true); });
+}
+
+// A workspace of bytes, or none.
+const at::Tensor *workspace(Call &c, PyObject *o) { return c.dense(o, "workspace", at::kByte, 1, true); }
+size_t bytes(const at::Tensor *t) { return t ? static_cast<size_t>(t->numel()) : 0; }
+
+PyObject *shared_prefix_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 15, [&] {
         Call c;
-        int64_t qs = 0, ks = 0, vs = 0;
-        const at::Tensor *k = c.rows(a[1], "k", &ks), *v = c.rows(a[2], "v", &vs);
-        const Caches cc(c, a[6], a[7], a[12], a[13]);
-        const int T = size(k, 0);
-        if (v->sizes() != k->sizes() || k->size(1) != cc.heads || k->size(2) != cc.dim)
-            raise(PyExc_ValueError, "inconsistent K/V and cache shapes");
-        const at::Tensor *pos = c.dense(a[3], "positions", at::kInt);
-        if ((pos->dim() != 1 && pos->dim() != 2) || pos->size(-1) != T)
-            raise(PyExc_ValueError, "positions must be [tokens] or [axes, tokens] (got %s)", shape_of(*pos).c_str());
-        const at::Tensor *freq = c.dense(a[4], "inv_freq", at::kDouble, 1);
-        if (freq->size(0) > 65536) raise(PyExc_ValueError, "inv_freq is longer than half a head");
-        const at::Tensor *axis = c.shaped(a[8], "pair_axis", at::kInt, {freq->size(0)}, true);
-        const at::Tensor *slots = c.shaped(a[5], "slot_mapping", at::kInt, {T});
-        const at::Tensor *q = c.rows(a[0], "q", &qs, true), *out = nullptr;
-        if (q) {
-            if (q->size(0) != T || q->size(2) != cc.dim) raise(PyExc_ValueError, "inconsistent q and k shapes");
-            out = c.shaped(a[14], "out", at::kBFloat16, {T, q->size(1), cc.dim});
-        }
-        const int adjacent = PyObject_IsTrue(a[9]);
-        if (adjacent < 0) throw Raised{};
-        const float magnitude = to_float(a[10]), kv_scale = to_float(a[11]);
-        const int axes = pos->dim() == 2 ? size(pos, 0) : 1, rotary = 2 * size(freq, 0), heads = q ? size(q, 1) : 0;
-        const cudaStream_t s = c.stream(a[15]);
+        const Rows r(c, a[0], a[3], a[4]);
+        const Caches cc(c, a[1], a[2], a[10], a[11]);
+        if (cc.dim != r.dim) raise(PyExc_ValueError, "inconsistent q / cache shapes");
+        const at::Tensor *start = c.dense(a[5], "group_start", at::kInt, 1), *blocks = c.dense(a[6], "prefix_blocks", at::kInt, 1);
+        if (start->size(0) != blocks->size(0) + 1)
+            raise(PyExc_ValueError, "group_start needs one entry more than prefix_blocks (got %lld and %lld)",
+                  static_cast<long long>(start->size(0)), static_cast<long long>(blocks->size(0)));
+        const int groups = size(blocks, 0), most = to_int(a[7], "max_prefix_blocks");
+        const float softmax_scale = to_float(a[8]), kv_scale = to_float(a[9]);
+        const at::Tensor *ws = workspace(c, a[12]);
+        const at::Tensor *out = c.shaped(a[13], "out", at::kBFloat16, {r.rows, r.heads, r.dim});
+        const cudaStream_t s = c.stream(a[14]);
         const Unlocked unlocked;
-        return f_rope_append(ptr<void>(q), qs, k->data_ptr(), ks, v->data_ptr(), vs, ptr<int32_t>(pos), axes,
-                             ptr<double>(freq), ptr<int32_t>(axis), rotary, adjacent, magnitude, ptr<int32_t>(slots), T, heads,
-                             ptr<void>(out), cc.k->data_ptr(),
-                             cc.v->data_ptr(), cc.blocks, cc.heads, cc.dim, cc.block, cc.type, kv_scale, ptr<float>(cc.k_scales),
-                             ptr<float>(cc.v_scales), s);
+        return f_shared_prefix_decode(r.q->data_ptr(), cc.k->data_ptr(), cc.v->data_ptr(), ptr<int32_t>(r.tables), r.width,
+                                      ptr<int32_t>(r.lens), r.rows, ptr<int32_t>(start), ptr<int32_t>(blocks), groups, most, r.heads,
+                                      cc.heads, r.dim, cc.blocks, cc.block, cc.type, kv_scale, ptr<float>(cc.k_scales),
+                                      ptr<float>(cc.v_scales), softmax_scale, ptr<void>(ws), bytes(ws), out->data_ptr(), s);
+    });
+}
+
+PyObject *cross_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        Call c;
+        const at::Tensor *q = c.dense(a[0], "q", at::kBFloat16, 3), *tables = c.dense(a[3], "block_tables", at::kInt, 2);
+        const int seqs = size(tables, 0), width = size(tables, 1), tokens = size(q, 0), heads = size(q, 1), dim = size(q, 2);
+        const at::Tensor *lens = c.shaped(a[4], "state_lens", at::kInt, {seqs});
+        const at::Tensor *start = c.shaped(a[5], "query_start", at::kInt, {static_cast<int64_t>(seqs) + 1});
+        const Caches cc(c, a[1], a[2], a[9], a[10]);
+        if (cc.dim != dim) raise(PyExc_ValueError, "inconsistent q / cache shapes");
+        const int most = to_int(a[6], "max_query_len");
+        const float softmax_scale = to_float(a[7]), kv_scale = to_float(a[8]);
+        const at::Tensor *ws = workspace(c, a[11]);
+        const at::Tensor *out = c.shaped(a[12], "out", at::kBFloat16, {tokens, heads, dim});
+        const cudaStream_t s = c.stream(a[13]);
+        const Unlocked unlocked;
+        return f_cross_attention(q->data_ptr(), cc.k->data_ptr(), cc.v->data_ptr(), ptr<int32_t>(tables), width, ptr<int32_t>(lens),
+                                 ptr<int32_t>(start), seqs, tokens, most, heads, cc.heads, dim, cc.blocks, cc.block, cc.type, kv_scale,
+                                 ptr<float>(cc.k_scales), ptr<float>(cc.v_scales), softmax_scale, ptr<void>(ws), bytes(ws),
+                                 out->data_ptr(), s);
     });
 }
 
@@ -327,11 +413,11 @@ PyObject *sparse_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bind(rope_append, block_summary, sparse_select, sparse_decode, sparse_attend): addresses in the loaded library
+// The addresses in the loaded library, in the order of _lib.BINDING_CALLS.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 5, [&] {
-        void *p[5];
-        for (int i = 0; i < 5; ++i) {
+    return guarded(n, 8, [&] {
+        void *p[8];
+        for (int i = 0; i < 8; ++i) {
             p[i] = PyLong_AsVoidPtr(a[i]);
             if (!p[i]) {
                 if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -343,6 +429,9 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
         f_sparse_select = reinterpret_cast<decltype(f_sparse_select)>(p[2]);
         f_sparse_decode = reinterpret_cast<decltype(f_sparse_decode)>(p[3]);
         f_sparse_attend = reinterpret_cast<decltype(f_sparse_attend)>(p[4]);
+        f_norm_rope_append = reinterpret_cast<decltype(f_norm_rope_append)>(p[5]);
+        f_shared_prefix_decode = reinterpret_cast<decltype(f_shared_prefix_decode)>(p[6]);
+        f_cross_attention = reinterpret_cast<decltype(f_cross_attention)>(p[7]);
         return PA_OK;
     });
 }
@@ -355,6 +444,9 @@ PyMethodDef methods[] = {
     {"sparse_select", FAST(sparse_select), nullptr},
     {"sparse_decode", FAST(sparse_decode), nullptr},
     {"sparse_attend", FAST(sparse_attend), nullptr},
+    {"norm_rope_append", FAST(norm_rope_append), nullptr},
+    {"shared_prefix_decode", FAST(shared_prefix_decode), nullptr},
+    {"cross_attention", FAST(cross_attention), nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,150 @@
+// Cross attention: every row of a sequence attends to all of an encoder's
+// states, whose keys and values lie in the paged cache ("vLLM PagedAttention:
+// Memory Optimization & High-Throughput LLM Inference Tuning", section 2: the
+// cache is read through the sequence's block table).
+//
+// The rows' products are pa_rows.cu's.  With few rows to a batch a run of states
+// is cut into parts, so that all SMs read it, and the kernel here joins them:
+// a warp to a row, whose parts' weights are made once, a lane to a part.
+#include <math.h>
+
+#include "pa_rows.cuh"
+#include "pa_sparse.cuh"
+
+namespace pa {
+namespace rows {
+
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, const float v_scale, __nv_bfloat16 *out) {
+    constexpr int E = D / 32;  // head dims of a lane
+    dependent_wait();
+    const int lane = threadIdx.x & 31, s = blockIdx.y;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const int t = static_cast<int>(row / a.num_q_heads), hq = static_cast<int>(row - static_cast<int64_t>(t) * a.num_q_heads);
+    int first, count;
+    if (!query_range(a, s, first, count) || t >= count) return;
+    const int keys = min(max(a.lens[s], 0), a.max_blocks * a.block_size);
+    const int parts = live_parts((keys + kKeys - 1) / kKeys, a.parts);
+    const int64_t at = (static_cast<int64_t>(first) + t) * a.num_q_heads + hq, stride = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+    const float2 ml = lane < parts ? a.part_ml[lane * stride + at] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    // a part that saw no finite score is left out, one with a NaN in its sum keeps it
+    float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : fast_exp2(ml.x - top);
+    float sum = f != 0.f ? f * ml.y : 0.f;
+#pragma unroll
+    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float scale = a.v_scales ? a.v_scales[hq / a.group] : v_scale;
+    f *= sum != 0.f ? scale / sum : 0.f;
+    dependent_release();
+    float acc[E] = {};
+    const float *o = a.part_o + at * D + lane * E;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        float x[E];
+        if constexpr (E == 4)
+            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(o + p * stride * D);
+        else
+            *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(o + p * stride * D);
+        const float w = __shfl_sync(0xffffffffu, f, p);
+        if (w != 0.f)
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] += w * x[i];
+    }
+    __nv_bfloat16 *to = out + at * D + lane * E;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<false>(acc[0], acc[1]), pack2<false>(acc[2], acc[3]));
+    else
+        *reinterpret_cast<uint32_t *>(to) = pack2<false>(acc[0], acc[1]);
+}
+
+static int cross_parts(int64_t num_seqs, int max_query_len, int num_q_heads, int num_kv_heads, int max_blocks, int block_size) {
+    const int64_t ctas = tile_pairs(max_query_len, num_q_heads / num_kv_heads) * num_kv_heads * num_seqs;
+    return choose_parts(ctas, static_cast<int>((static_cast<int64_t>(max_blocks) * block_size + kKeys - 1) / kKeys));
+}
+
+}  // namespace rows
+}  // namespace pa
+
+using namespace pa;
+using namespace pa::rows;
+
+extern "C" {
+
+size_t pa_cross_workspace_size(int num_tokens, int num_seqs, int max_query_len, int num_q_heads, int num_kv_heads,
+                               int head_dim, int max_blocks_per_seq, int block_size) {
+    if (num_tokens <= 0 || num_seqs <= 0 || max_query_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16 || head_dim <= 0 || max_blocks_per_seq <= 0 || block_size <= 0 ||
+        static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
+        return 0;
+    const int parts = cross_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads, max_blocks_per_seq, block_size);
+    return parts == 1 ? 0 : workspace_bytes(parts, static_cast<int64_t>(num_tokens) * num_q_heads, head_dim);
+}
+
+pa_status pa_cross_attention(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *state_lens, const int32_t *query_start, int num_seqs,
+                             int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                             int num_blocks, int block_size, pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
+                             const float *v_scales, float softmax_scale, void *workspace, size_t workspace_bytes,
+                             void *out, cudaStream_t stream) {
+    clear_error();
+    Args a = {};
+    pa_status st = check_rows(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size,
+                              max_blocks_per_seq, kv_dtype, kv_scale, k_scales, v_scales, softmax_scale);
+    if (st != PA_OK) return st;
+    if (max_query_len < 0) return fail(PA_ERR_INVALID_ARG, "max_query_len %d is negative", max_query_len);
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (max_query_len == 0) return fail(PA_ERR_INVALID_ARG, "max_query_len 0 with %d rows", num_tokens);
+    if (max_query_len > num_tokens) max_query_len = num_tokens;
+    if (!query_start) return fail(PA_ERR_INVALID_ARG, "null pointer");
+    st = check_row_pointers(q, k_cache, v_cache, block_tables, state_lens, out, num_tokens, num_q_heads, head_dim);
+    if (st != PA_OK) return st;
+    const int parts = cross_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads, max_blocks_per_seq, block_size);
+    const int64_t num_rows = static_cast<int64_t>(num_tokens) * num_q_heads;
+    if (parts > 1) {
+        st = check_workspace(workspace, workspace_bytes, rows::workspace_bytes(parts, num_rows, head_dim), q, out,
+                             static_cast<size_t>(num_rows) * head_dim * 2);
+        if (st != PA_OK) return st;
+    }
+    unsigned int *err = device_error_word();
+    if (!err) return fail(PA_ERR_CUDA, "cannot resolve the device error word");
+    a.block_tables = block_tables;
+    a.lens = state_lens;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = num_q_heads / num_kv_heads;
+    a.num_tokens = num_tokens;
+    a.num_seqs = num_seqs;
+    a.max_query_len = max_query_len;
+    a.softmax_log2 = softmax_scale * 1.4426950408889634f;
+    a.kv_scale = kv_scale;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.parts = parts;
+    a.query_start = query_start;
+    a.err = err;
+    if (parts == 1) {
+        a.out = static_cast<__nv_bfloat16 *>(out);
+    } else {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float2 *>(a.part_o + parts * num_rows * head_dim);
+    }
+    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
+    st = launch_rows(q, k_cache, v_cache, head_dim, fp8, a, tile_pairs(max_query_len, a.group), num_seqs, stream);
+    if (st != PA_OK || parts == 1) return st;
+    const int64_t join = (static_cast<int64_t>(max_query_len) * num_q_heads + kJoinWarps - 1) / kJoinWarps;
+    const dim3 grid(static_cast<unsigned>(join), num_seqs);
+    const float v_scale = fp8 ? kv_scale : 1.f;
+    auto *to = static_cast<__nv_bfloat16 *>(out);
+    return cuda_check(head_dim == 128 ? launch_dependent(join_kernel<128>, grid, kJoinWarps * 32, 0, 0, stream, a, v_scale, to)
+                                      : launch_dependent(join_kernel<64>, grid, kJoinWarps * 32, 0, 0, stream, a, v_scale, to),
+                      "cross attention join launch");
+}
+
+}  // extern "C"

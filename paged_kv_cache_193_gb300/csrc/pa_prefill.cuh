@@ -7,6 +7,11 @@
 
 namespace pa {
 
+// Tensor map over queries [total_tokens][num_q_heads][head_dim]; one box is 64
+// dims of `group` heads of `tile_tokens` tokens (pa_prefill_tc.cu).
+pa_status make_q_map(CUtensorMap *map, const void *q, int total_tokens, int num_q_heads, int head_dim,
+                     int group, int tile_tokens);
+
 // try_wait that lets the hardware suspend the thread until the phase
 // completes (or `hint_ns` passes), instead of returning at once: a waiting
 // warp then takes no issue slots from the warps of its SM sub-partition.

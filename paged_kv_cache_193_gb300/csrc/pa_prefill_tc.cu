@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // Queries [Tq][Hq][D] as a 3-D tensor (D, Hq, Tq); one box is 64 dims x
 // `group` heads x `tile_tokens` tokens with the 128-byte swizzle.
-static pa_status make_q_map(CUtensorMap *map, const void *q, int total_tokens, int num_q_heads,
-                            int head_dim, int group, int tile_tokens) {
+pa_status make_q_map(CUtensorMap *map, const void *q, int total_tokens, int num_q_heads, int head_dim,
+                     int group, int tile_tokens) {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult qr;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) !=

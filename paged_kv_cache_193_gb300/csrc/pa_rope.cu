@@ -2,7 +2,8 @@
 // rows, and the write of their k and v rows into the paged cache, in one
 // kernel ("Optimizing Llama 3.1 405B Inference with vLLM PagedAttention",
 // section "PagedAttention Mechanics": a token's K and V are appended on
-// arrival; the pages leave the rotation to the model).
+// arrival; the pages leave the rotation to the model).  For models that
+// normalise every head's q and k first, that is done on the way (NORM).
 //
 // Mathematics: pair i of a row (x_a, x_b) is turned by the angle
 // theta = position * inv_freq[i]:
@@ -15,6 +16,11 @@
 // that: below 2^-29 turns at any position for frequencies up to 1.  Its upper 32
 // bits go to sine and cosine as an fp32 number of half turns, within 2^-24.
 //
+// NORM: a row of q or k becomes x * rsqrt(mean x^2 + eps) * (offset + w) before it
+// is turned, all in fp32 and rounded once with the rotation.  A row is in the
+// registers of head_dim / 16 neighbouring lanes, so its sum of squares takes two or
+// three shuffles and no pass of its own over memory.
+//
 // Bound: memory.  Every q, k, v element is read once and written once: 8192
 // tokens of 32 query and 8 KV heads, 201 MB, take 35 us, where a library copy of
 // as much takes 32.5; few tokens are bound by the launch (one: 2.0 us) and by the
@@ -22,6 +28,7 @@
 // while the angles are made.
 #include <algorithm>
 #include <cstring>
+#include <tuple>
 #include <utility>
 
 #include "pa_launch.cuh"
@@ -70,6 +77,10 @@ struct Args {
     Divisor kv_scale;
     const float *k_scales, *v_scales;
     unsigned int *err;
+    // NORM: bf16 weights of head 0, or null (1), elements between heads' weights
+    const __nv_bfloat16 *q_weight, *k_weight;
+    int64_t q_weight_stride, k_weight_stride;
+    float weight_offset, eps;
 };
 
 constexpr int kThreads = 256;
@@ -133,7 +144,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divisor &by) 
 // elements 16j .. 16j+15; either way pairs 8j .. 8j+7, and two 16-byte loads.
 // Its j is the same for every row it takes.
 // CTAS: of the kernel to an SM, which caps its registers.
-template <int D, bool FP8, bool ADJACENT, int CTAS>
+template <int D, bool FP8, bool ADJACENT, bool NORM, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
     constexpr int VPR = D / 16;  // threads to a row
     __shared__ __align__(16) float cs[kMaxTile][D / 2], sn[kMaxTile][D / 2];
@@ -202,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         const int da = is_v ? 16 * j : ea, db = is_v ? da + 8 : eb;
         const int64_t dst = (is_q ? t * a.num_q_heads + h : row + h * a.block_size) * D;
         const bool rotate = turn && !is_v;
-        if (!rotate && (!FP8 || is_q)) {  // bits as they are
+        if (!rotate && (!FP8 || is_q) && (!NORM || is_v)) {  // bits as they are
             __nv_bfloat16 *to = is_q ? a.q_out : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache);
             *reinterpret_cast<uint4 *>(to + dst + da) = wa;
             *reinterpret_cast<uint4 *>(to + dst + db) = wb;
@@ -211,6 +222,42 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         float xa[8], xb[8];
         unpack8(wa, xa);
         unpack8(wb, xb);
+        if constexpr (NORM) {
+            if (!is_v) {
+                const __nv_bfloat16 *weight = is_q ? a.q_weight : a.k_weight;
+                uint4 ga, gb;
+                if (weight) {
+                    weight += h * (is_q ? a.q_weight_stride : a.k_weight_stride);
+                    ga = *reinterpret_cast<const uint4 *>(weight + ea);
+                    gb = *reinterpret_cast<const uint4 *>(weight + eb);
+                }
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    sum[0] = fmaf(xa[u], xa[u], sum[0]);
+                    sum[1] = fmaf(xb[u], xb[u], sum[1]);
+                }
+                sum[0] += sum[1];
+                const unsigned lanes = ((1u << VPR) - 1u) << (threadIdx.x & 31 & ~(VPR - 1));  // the row's
+#pragma unroll
+                for (int d = 1; d < VPR; d *= 2) sum[0] += __shfl_xor_sync(lanes, sum[0], d);
+                const float r = rsqrtf(sum[0] * (1.f / D) + a.eps);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    xa[u] *= r;
+                    xb[u] *= r;
+                }
+                if (weight) {
+                    float g[8];
+                    unpack8(ga, g);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) xa[u] *= g[u] + a.weight_offset;
+                    unpack8(gb, g);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) xb[u] *= g[u] + a.weight_offset;
+                }
+            }
+        }
         if (rotate) {
             float c[8], s[8];
 #pragma unroll
@@ -286,33 +333,42 @@ static int tokens_per_cta(int num_tokens, int rows, int head_dim) {
     return best;
 }
 
-template <int D, bool FP8, bool ADJACENT>
+template <int D, bool FP8, bool ADJACENT, bool NORM>
 static cudaError_t launch_ctas(const Args &a, dim3 grid, cudaStream_t stream) {
     if constexpr (D == 128)
         if (five_to_an_sm(D, static_cast<int64_t>(grid.x) * grid.y))
-            return launch_dependent(append_kernel<D, FP8, ADJACENT, 5>, grid, kThreads, 0, 0, stream, a);
-    return launch_dependent(append_kernel<D, FP8, ADJACENT, 4>, grid, kThreads, 0, 0, stream, a);
+            return launch_dependent(append_kernel<D, FP8, ADJACENT, NORM, 5>, grid, kThreads, 0, 0, stream, a);
+    return launch_dependent(append_kernel<D, FP8, ADJACENT, NORM, 4>, grid, kThreads, 0, 0, stream, a);
+}
+
+template <int D, bool FP8, bool NORM>
+static cudaError_t launch_adjacent(const Args &a, bool adjacent, dim3 grid, cudaStream_t stream) {
+    return adjacent ? launch_ctas<D, FP8, true, NORM>(a, grid, stream) : launch_ctas<D, FP8, false, NORM>(a, grid, stream);
 }
 
 template <int D, bool FP8>
-static cudaError_t launch(const Args &a, bool adjacent, dim3 grid, cudaStream_t stream) {
-    return adjacent ? launch_ctas<D, FP8, true>(a, grid, stream) : launch_ctas<D, FP8, false>(a, grid, stream);
+static cudaError_t launch(const Args &a, bool adjacent, bool norm, dim3 grid, cudaStream_t stream) {
+    return norm ? launch_adjacent<D, FP8, true>(a, adjacent, grid, stream)
+                : launch_adjacent<D, FP8, false>(a, adjacent, grid, stream);
 }
 
-}  // namespace rope
-}  // namespace pa
+// What the norm adds to a call.
+struct Norm {
+    const void *q_weight;
+    int64_t q_weight_stride;
+    const void *k_weight;
+    int64_t k_weight_stride;
+    float weight_offset, eps;
+};
 
-using namespace pa;
-
-extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
-                                    const void *v, int64_t v_stride, const int32_t *positions,
-                                    int num_axes, const double *inv_freq, const int32_t *pair_axis,
-                                    int rotary_dim, int adjacent, float magnitude,
-                                    const int32_t *slot_mapping, int num_tokens, int num_q_heads,
-                                    void *q_out, void *k_cache, void *v_cache, int num_blocks,
-                                    int num_kv_heads, int head_dim, int block_size,
-                                    pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
-                                    const float *v_scales, cudaStream_t stream) {
+// `norm`: null without one.
+static pa_status append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                        const Norm *norm, const int32_t *positions, int num_axes, const double *inv_freq,
+                        const int32_t *pair_axis, int rotary_dim, int adjacent, float magnitude,
+                        const int32_t *slot_mapping, int num_tokens, int num_q_heads, void *q_out, void *k_cache,
+                        void *v_cache, int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                        pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales, const float *v_scales,
+                        cudaStream_t stream) {
     clear_error();
     if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_blocks <= 0)
         return fail(PA_ERR_INVALID_ARG, "bad size (num_tokens=%d, num_q_heads=%d, num_kv_heads=%d, num_blocks=%d)",
@@ -343,6 +399,19 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
         return fail(PA_ERR_INVALID_ARG, "fp8 kv_scale must be positive and finite");
     if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffffLL)
         return fail(PA_ERR_UNSUPPORTED, "pool of %d blocks exceeds 2^31 slots", num_blocks);
+    if (norm) {
+        if (!(norm->eps >= 1e-12f && norm->eps <= 3.4e38f))
+            return fail(PA_ERR_INVALID_ARG, "eps must be finite and at least 1e-12");
+        if (!(norm->weight_offset >= -3.4e38f && norm->weight_offset <= 3.4e38f))
+            return fail(PA_ERR_INVALID_ARG, "weight_offset must be finite");
+        for (const auto &[weight, stride, heads] : {std::tuple(norm->q_weight, norm->q_weight_stride, num_q_heads),
+                                                    std::tuple(norm->k_weight, norm->k_weight_stride, num_kv_heads)}) {
+            if (!weight) continue;
+            if (!aligned16(weight)) return fail(PA_ERR_INVALID_ARG, "weights must be 16-byte aligned");
+            if (stride % 8 || stride < 0 || (stride && heads > 1 && stride < head_dim))
+                return fail(PA_ERR_INVALID_ARG, "a weight stride is 0, or a multiple of 8 elements and at least head_dim");
+        }
+    }
     if (num_tokens == 0) return PA_OK;
     if (!k || !v || !positions || !inv_freq || !slot_mapping || !k_cache || !v_cache ||
         (num_q_heads > 0 && (!q || !q_out)))
@@ -366,10 +435,17 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
         if (num_q_heads > 0 && overlaps(rows, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
             return fail(PA_ERR_INVALID_ARG, "q_out overlaps k or v");
     }
+    if (norm && num_q_heads > 0)
+        for (const auto &[weight, stride, heads] : {std::tuple(norm->q_weight, norm->q_weight_stride, num_q_heads),
+                                                    std::tuple(norm->k_weight, norm->k_weight_stride, num_kv_heads)}) {
+            const size_t span = (static_cast<size_t>(heads - 1) * stride + head_dim) * 2;
+            if (weight && overlaps(weight, span, q_out, static_cast<size_t>(num_tokens) * qrow * 2))
+                return fail(PA_ERR_INVALID_ARG, "q_out overlaps the weights");
+        }
     unsigned int *err = device_error_word();
     if (!err) return fail(PA_ERR_CUDA, "cannot resolve the device error word");
 
-    rope::Args a;
+    Args a;
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.k = static_cast<const __nv_bfloat16 *>(k);
     a.v = static_cast<const __nv_bfloat16 *>(v);
@@ -391,21 +467,62 @@ extern "C" pa_status pa_rope_append(const void *q, int64_t q_stride, const void 
     a.block_size = block_size;
     a.pairs = rotary_dim / 2;
     a.magnitude = magnitude;
-    a.kv_scale = rope::Divisor::of(kv_scale);
+    a.kv_scale = Divisor::of(kv_scale);
     a.k_scales = k_scales;
     a.v_scales = v_scales;
     a.err = err;
+    a.q_weight = norm ? static_cast<const __nv_bfloat16 *>(norm->q_weight) : nullptr;
+    a.k_weight = norm ? static_cast<const __nv_bfloat16 *>(norm->k_weight) : nullptr;
+    a.q_weight_stride = norm ? norm->q_weight_stride : 0;
+    a.k_weight_stride = norm ? norm->k_weight_stride : 0;
+    a.weight_offset = norm ? norm->weight_offset : 0.f;
+    a.eps = norm ? norm->eps : 0.f;
     const int rows = num_q_heads + 2 * num_kv_heads;
-    a.tile = rope::tokens_per_cta(num_tokens, rows, head_dim);
-    const int at_once = rope::kThreads / (head_dim / 16);  // rows of one pass of the CTA's threads
+    a.tile = tokens_per_cta(num_tokens, rows, head_dim);
+    const int at_once = kThreads / (head_dim / 16);  // rows of one pass of the CTA's threads
     // With few tokens a token's rows are shared out too, up to four CTAs to an SM.
     const int shares = std::max(1, std::min((rows + at_once - 1) / at_once, 4 * 152 / num_tokens));
     a.rows_per_y = (rows + shares - 1) / shares;
     const dim3 grid((static_cast<unsigned>(num_tokens) + a.tile - 1) / a.tile, (rows + a.rows_per_y - 1) / a.rows_per_y);
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3, adj = adjacent != 0;
-    const cudaError_t e = head_dim == 128 ? (fp8 ? rope::launch<128, true>(a, adj, grid, stream)
-                                                 : rope::launch<128, false>(a, adj, grid, stream))
-                                          : (fp8 ? rope::launch<64, true>(a, adj, grid, stream)
-                                                 : rope::launch<64, false>(a, adj, grid, stream));
+    const cudaError_t e = head_dim == 128 ? (fp8 ? launch<128, true>(a, adj, norm, grid, stream)
+                                                 : launch<128, false>(a, adj, norm, grid, stream))
+                                          : (fp8 ? launch<64, true>(a, adj, norm, grid, stream)
+                                                 : launch<64, false>(a, adj, norm, grid, stream));
     return cuda_check(e, "rope append launch");
 }
+
+}  // namespace rope
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+pa_status pa_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, const int32_t *positions, int num_axes, const double *inv_freq,
+                         const int32_t *pair_axis, int rotary_dim, int adjacent, float magnitude,
+                         const int32_t *slot_mapping, int num_tokens, int num_q_heads, void *q_out, void *k_cache,
+                         void *v_cache, int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                         pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales, const float *v_scales,
+                         cudaStream_t stream) {
+    return rope::append(q, q_stride, k, k_stride, v, v_stride, nullptr, positions, num_axes, inv_freq, pair_axis,
+                        rotary_dim, adjacent, magnitude, slot_mapping, num_tokens, num_q_heads, q_out, k_cache, v_cache,
+                        num_blocks, num_kv_heads, head_dim, block_size, kv_dtype, kv_scale, k_scales, v_scales, stream);
+}
+
+pa_status pa_norm_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, const void *q_weight, int64_t q_weight_stride, const void *k_weight,
+                              int64_t k_weight_stride, float weight_offset, float eps, const int32_t *positions,
+                              int num_axes, const double *inv_freq, const int32_t *pair_axis, int rotary_dim,
+                              int adjacent, float magnitude, const int32_t *slot_mapping, int num_tokens,
+                              int num_q_heads, void *q_out, void *k_cache, void *v_cache, int num_blocks,
+                              int num_kv_heads, int head_dim, int block_size, pa_kv_dtype kv_dtype, float kv_scale,
+                              const float *k_scales, const float *v_scales, cudaStream_t stream) {
+    const rope::Norm norm{q_weight, q_weight_stride, k_weight, k_weight_stride, weight_offset, eps};
+    return rope::append(q, q_stride, k, k_stride, v, v_stride, &norm, positions, num_axes, inv_freq, pair_axis,
+                        rotary_dim, adjacent, magnitude, slot_mapping, num_tokens, num_q_heads, q_out, k_cache, v_cache,
+                        num_blocks, num_kv_heads, head_dim, block_size, kv_dtype, kv_scale, k_scales, v_scales, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,103 @@
+// Attention of many query rows to one run of cached pages on the tcgen05
+// tensor cores: what cross attention and the shared part of a prefix-sharing
+// batch's decode have in common.  Here the parts that both sides of a launch
+// agree on; the kernel is in pa_rows.cu.
+//
+// Rows are (token, query head of one KV head) pairs, 128 to a tile; a run of
+// keys may be cut into parts, each with its own
+//   m = max_t s_t (or what the kernel takes for it), l = sum_t 2^(s_t - m),
+//   o = sum_t 2^(s_t - m) V[t],   s_t = softmax_scale * log2(e) * q . K[t],
+// which join as M = max m, sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+#pragma once
+
+#include <algorithm>
+
+#include "pa_launch.cuh"
+
+namespace pa {
+namespace rows {
+
+constexpr int kSms = 152;
+constexpr int kRows = 128;     // query rows of a tile (lanes of tensor memory)
+constexpr int kTiles = 2;      // tiles of a CTA: both read every stage of keys
+constexpr int kKeys = 64;      // keys of a block
+constexpr int kMaxParts = 32;  // of a run of keys
+// A part has at least so many blocks: its start and end cost about as much.
+constexpr int kLeastBlocks = 4;
+
+// Blocks of each part of a run of `blocks`; parts from ceil(blocks / that) on
+// have none, and nothing is written for them.
+__host__ __device__ __forceinline__ int blocks_per_part(int blocks, int parts) {
+    const int even = (blocks + parts - 1) / parts;
+    return even > kLeastBlocks ? even : kLeastBlocks;
+}
+__host__ __device__ __forceinline__ int live_parts(int blocks, int parts) {
+    const int each = blocks_per_part(blocks, parts);
+    return (blocks + each - 1) / each;
+}
+
+// Floats of the parts: [parts][num_tokens * num_q_heads] of (head_dim, and m, l).
+inline size_t workspace_bytes(int parts, int64_t num_rows, int head_dim) {
+    return static_cast<size_t>(parts) * num_rows * (head_dim + 2) * sizeof(float);
+}
+
+struct Args {
+    const int32_t *block_tables;
+    const int32_t *lens;  // tokens of each sequence
+    int max_blocks, num_blocks, block_size;
+    int num_q_heads, num_kv_heads, group;
+    int num_tokens, num_seqs;
+    int max_query_len;   // cross attention: rows of a sequence, at most
+    int tile_tokens;     // 128 / group
+    float softmax_log2;  // softmax_scale * log2(e)
+    float kv_scale;      // E4M3: one scale, or one of K and V for each head
+    const float *k_scales, *v_scales;
+    uint64_t wait_limit_ns;
+    int stall_first_wait;
+    int parts;
+    __nv_bfloat16 *out;  // one part: the result goes here
+    float *part_o;       // several, or a prefix: [parts][rows][head_dim]
+    float2 *part_ml;     // [parts][rows]
+    // cross attention: sequence s's rows are tokens query_start[s] .. query_start[s + 1] - 1
+    const int32_t *query_start;
+    // shared prefix: group g's sequences are group_start[g] .. group_start[g + 1] - 1
+    const int32_t *group_start;
+    const int32_t *prefix_blocks;
+    int num_groups, max_prefix_blocks;
+    unsigned int *err;
+};
+
+// Tile pairs of `tokens` tokens of a KV head's group.
+inline int64_t tile_pairs(int64_t tokens, int group) {
+    const int each = kTiles * (kRows / group);
+    return (tokens + each - 1) / each;
+}
+
+// Into how many parts to cut runs of up to `blocks` blocks for `ctas` CTAs to a part.
+int choose_parts(int64_t ctas, int blocks);
+
+// Rows of sequence s: false for what is no range of the tokens, or longer than it may be.
+__device__ __forceinline__ bool query_range(const Args &a, int s, int &first, int &count) {
+    first = a.query_start[s];
+    const int end = a.query_start[s + 1];
+    if (first < 0 || end < first || end > a.num_tokens || end - first > a.max_query_len) return false;
+    count = end - first;
+    return true;
+}
+
+// Checks of arguments, for both (pa_shared.cu).
+pa_status check_rows(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+                     int block_size, int max_blocks, pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
+                     const float *v_scales, float softmax_scale);
+pa_status check_row_pointers(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                             const int32_t *lens, const void *out, int64_t num_tokens, int num_q_heads, int head_dim);
+pa_status check_workspace(const void *workspace, size_t got, size_t need, const void *q, const void *out, size_t row_bytes);
+
+// Attention of `a`'s rows (q bf16 [num_tokens][num_q_heads][head_dim]) over the grid's
+// (tile pair, part), KV head, and sequence (1 for a shared prefix: the pairs of all groups lie
+// one after the other).
+pa_status launch_rows(const void *q, const void *k_cache, const void *v_cache, int head_dim, bool fp8, Args &a,
+                      int64_t pairs, int seqs, cudaStream_t stream);
+
+}  // namespace rows
+}  // namespace pa

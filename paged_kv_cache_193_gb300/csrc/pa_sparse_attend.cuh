@@ -18,6 +18,10 @@
 // 32: 575 MB in 100.6 us, 5.7 TB/s.  Over a list that is there the pages alone take
 // 80 us in both, 6.7 TB/s.  With few rows by latency: one sequence of 5,003 tokens,
 // top 64, 10.4 us.
+//
+// The same kernel attends to what a sequence has behind a prefix that it shares
+// (SUFFIX): the list is the pages from there on, and the parts that the prefix's
+// kernel left (pa_rows.cuh) join the warps' own at the end.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -25,10 +29,22 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "pa_rows.cuh"
 #include "pa_sparse_select.cuh"
 
 namespace pa {
 namespace sparse {
+
+// What attends to a whole sequence when part of it has been attended to before.
+struct Prefix {
+    const int32_t *group_start;    // [num_groups + 1] first sequence of each group
+    const int32_t *prefix_blocks;  // [num_groups]
+    int num_groups, max_blocks;    // no prefix counts for more pages than this
+    int parts;                     // of each prefix; 0: there are none
+    const float *o;                // [parts][rows][head_dim]
+    const float2 *ml;              // [parts][rows]
+    int64_t rows;
+};
 
 struct Args {
     const __nv_bfloat16 *q;
@@ -46,7 +62,11 @@ struct Args {
     int stall_first_wait;
     SelectArgs select;  // of the kernel that chooses the pages itself
     int longest_first;  // its clusters take the rows by length
+    Prefix prefix;      // of the kernel that attends behind a prefix
 };
+
+// A list of pages, pages that the kernel chooses, or the pages behind a prefix.
+enum Mode { kList, kChoose, kSuffix };
 
 pa_status launch_chosen(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
                         int num_rows, int splits, int warps, cudaStream_t stream);
@@ -128,13 +148,38 @@ __device__ __forceinline__ int longest_row(const int32_t *lens, int n, int z, vo
     return row;
 }
 
-// CHOOSE: the cluster first chooses the row's pages, in the ring's memory.
-template <int D, int BS, bool FP8, int NT, int NW, int SPW, bool CHOOSE>
+// Pages that sequence s, of n tokens, shares with its group: 0, or all of the
+// group's prefix.  Called by whole warps.  The loads pass by the first-level cache:
+// this runs before the kernel in front has ended.
+__device__ __forceinline__ int shared_pages(const Prefix &p, int s, int n, int block_size) {
+    if (p.parts == 0 || p.num_groups == 0) return 0;
+    const int lane = threadIdx.x & 31;
+    // the last group that starts at s or before, among 32 and then 32 of those between
+    int lo = 0, size = p.num_groups;
+    for (;;) {
+        const int step = (size + 31) / 32, at = lane * step;
+        const int v = at < size ? __ldcg(p.group_start + lo + at) : 0x7fffffff;
+        const int count = __popc(__ballot_sync(0xffffffffu, v <= s));
+        if (count == 0) return 0;
+        const int skip = min((count - 1) * step, size - 1);
+        lo += skip;
+        if (step == 1) break;
+        size = min(step, size - skip);
+    }
+    const int end = __ldcg(p.group_start + lo + 1), pages = min(__ldcg(p.prefix_blocks + lo), p.max_blocks);
+    return s < end && pages > 0 && n / block_size >= pages ? pages : 0;
+}
+
+// kChoose: the cluster first chooses the row's pages, in the ring's memory.
+// kSuffix: launched when the prefix's kernel is on the SMs, which has waited for
+// those before it; only the join waits for that kernel.
+template <int D, int BS, bool FP8, int NT, int NW, int SPW, int MODE>
 __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4 / NW)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const Args a) {
     using C = Shape<D, BS, FP8, NT, NW, SPW>;
     constexpr int PPI = C::PPI, MI = C::MI;
+    constexpr bool CHOOSE = MODE == kChoose, SUFFIX = MODE == kSuffix;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[C::NSTAGE];
     __shared__ __align__(8) uint64_t stall_bar;  // never completed (wait-limit test hook)
@@ -156,12 +201,14 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    dependent_wait();
+    if (!SUFFIX || a.prefix.parts == 0) dependent_wait();
     if constexpr (CHOOSE)
         if (a.longest_first) s = longest_row(a.context_lens, gridDim.z, s, join);
 
-    const float k_scale = FP8 ? (a.k_scales ? a.k_scales[h] : a.kv_scale) : 1.f;
-    const float v_scale = FP8 ? (a.v_scales ? a.v_scales[h] : a.kv_scale) : 1.f;
+    // plain loads; past the first-level cache where the kernel in front still runs
+    auto load = [](const auto *p) { return SUFFIX ? __ldcg(p) : *p; };
+    const float k_scale = FP8 ? (a.k_scales ? load(a.k_scales + h) : a.kv_scale) : 1.f;
+    const float v_scale = FP8 ? (a.v_scales ? load(a.v_scales + h) : a.kv_scale) : 1.f;
     const float score_scale = a.softmax_log2 * k_scale;
 
     Chosen chosen{0, nullptr};
@@ -185,12 +232,12 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
 #pragma unroll
             for (int kk = 0; kk < C::KSTEPS; ++kk) {
                 if constexpr (!FP8) {
-                    qf[kk][nt][0] = live ? *reinterpret_cast<const uint32_t *>(qg + kk * 16 + 2 * c) : 0u;
-                    qf[kk][nt][1] = live ? *reinterpret_cast<const uint32_t *>(qg + kk * 16 + 8 + 2 * c) : 0u;
+                    qf[kk][nt][0] = live ? load(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 2 * c)) : 0u;
+                    qf[kk][nt][1] = live ? load(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 8 + 2 * c)) : 0u;
                 } else {
                     // permuted order, as the K bytes below: this thread's dims
                     // are c*16*CPT + 4*kk + {0,1,2,3}
-                    const uint2 w = live ? *reinterpret_cast<const uint2 *>(qg + c * 16 * C::CPT + 4 * kk)
+                    const uint2 w = live ? load(reinterpret_cast<const uint2 *>(qg + c * 16 * C::CPT + 4 * kk))
                                          : make_uint2(0u, 0u);
                     const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.x));
                     const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w.y));
@@ -200,14 +247,18 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             }
         }
     }
-    int n = a.context_lens[s];
+    int n = load(a.context_lens + s);
     if (n > a.max_blocks * BS) {
         if (tid == 0 && rank == 0 && h == 0) set_device_error(a.err, PA_DEVERR_BAD_CONTEXT);
         n = a.max_blocks * BS;
     }
     const int nb = n > 0 ? (n + BS - 1) / BS : 0;
     __syncthreads();
-    if constexpr (!CHOOSE) {
+    int skip = 0;  // pages in front of the list's first
+    if constexpr (SUFFIX) {
+        skip = shared_pages(a.prefix, s, n, BS);
+        chosen = Chosen{nb - skip, nullptr};
+    } else if constexpr (!CHOOSE) {
         const int64_t row = static_cast<int64_t>(s) * a.num_kv_heads + h;
         chosen = Chosen{min(max(a.counts[row], 0), a.top_k), a.selected + row * a.top_k};
     }
@@ -218,7 +269,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     // logical page of the warp's k-th entry
     auto entry = [&](int k) -> int {
         const int i = first + k * step;
-        return chosen.list ? chosen.list[i] : i;
+        return SUFFIX ? skip + i : chosen.list ? chosen.list[i] : i;
     };
     const int32_t *table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
     const int my_pages = chosen.count > first ? (chosen.count - first + step - 1) / step : 0;
@@ -235,7 +286,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
             return rows_total;
         }
-        const int b = table[j];
+        const int b = load(table + j);
         if (b < 0 || b >= a.num_blocks) {
             set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
             return rows_total;
@@ -582,6 +633,43 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     auto weight = [](float m, float l, float top) {
         return m == -INFINITY ? (l == 0.f ? 0.f : l) : fast_exp2(m - top);
     };
+    // The prefix's parts of this row and KV head, and their weights beside the
+    // rest's (top, sum), which are brought up to date; the rest's own is returned.
+    __shared__ float pw[SUFFIX ? rows::kMaxParts : 1][SUFFIX ? C::NP : 1];
+    int parts = 0;
+    if constexpr (SUFFIX) {
+        if (a.prefix.parts) dependent_wait();
+        if (skip) parts = rows::live_parts((skip * BS + rows::kKeys - 1) / rows::kKeys, a.prefix.parts);
+    }
+    const int64_t part0 = static_cast<int64_t>(s) * a.num_q_heads + h * a.group;
+    auto with_prefix = [&](float top, float &sum) -> float {  // by thread g < group
+        const float2 *ml = a.prefix.ml + part0 + tid;
+        float all = top;
+        for (int p = 0; p < parts; ++p) all = fmaxf(all, ml[p * a.prefix.rows].x);
+        const float mine = weight(top, sum, all);
+        sum = mine == 0.f ? 0.f : sum * mine;
+        for (int p = 0; p < parts; ++p) {
+            const float2 x = ml[p * a.prefix.rows];
+            const float f = weight(x.x, x.y, all);
+            if (f != 0.f) sum += f * x.y;
+            pw[p][tid] = f;
+        }
+        return mine;
+    };
+    auto add_prefix = [&](int i, float4 &v) {  // four head dims of a head
+        const int g = i / (D / 4);
+        const float *o = a.prefix.o + part0 * D + 4 * i;
+        for (int p = 0; p < parts; ++p) {
+            const float f = pw[p][g];
+            const float4 x = *reinterpret_cast<const float4 *>(o + p * a.prefix.rows * D);
+            if (f != 0.f) {
+                v.x += f * x.x;
+                v.y += f * x.y;
+                v.z += f * x.z;
+                v.w += f * x.w;
+            }
+        }
+    };
     if (tid < C::NP) {
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -592,6 +680,12 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             sum += f * l;
             msm[w * C::NP + tid] = f;
         }
+        if constexpr (SUFFIX)
+            if (ranks == 1 && tid < a.group) {
+                const float mine = with_prefix(top, sum);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) msm[w * C::NP + tid] *= mine;
+            }
         mc[tid] = top;
         lc[tid] = sum;
     }
@@ -618,6 +712,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             }
         }
         if (ranks == 1) {
+            if constexpr (SUFFIX) add_prefix(i, v);
             const float sum = lc[g];
             put(i, v, sum != 0.f ? v_scale / sum : 0.f);
         } else {
@@ -643,9 +738,14 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             m[k] = weight(m[k], l[k], top);
             sum += m[k] * l[k];
         }
+        float mine = 1.f;
+        if constexpr (SUFFIX)
+            if (tid < a.group) mine = with_prefix(top, sum);
         const float inv = sum != 0.f ? v_scale / sum : 0.f;
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) fsm[k * C::NP + tid] = m[k] * inv;
+        for (uint32_t k = 0; k < 8; ++k) fsm[k * C::NP + tid] = m[k] * mine * inv;
+        if constexpr (SUFFIX)
+            for (int p = 0; p < parts; ++p) pw[p][tid] *= inv;
     }
     __syncthreads();
     for (int i = static_cast<int>(rank) * NW * 32 + tid; i < quads; i += static_cast<int>(ranks) * NW * 32) {
@@ -666,6 +766,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
                 v.w += f * __uint_as_float(x[k].w);
             }
         }
+        if constexpr (SUFFIX) add_prefix(i, v);
         put(i, v, 1.f);
     }
     // nobody leaves while another may still read its part
@@ -676,6 +777,20 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+
+// Four warps to a CTA: the most CTAs whose clusters are all resident at once and
+// whose warps have a page each.  An eighth of the CTAs' places is kept back:
+// clusters of three, six or eight leave some of a GPC's places empty (8 rows of
+// 8 heads, 16 queries each, 128K tokens: 62 us with 6, 71 with 4, 85 with 8).
+// Short lists are not shared out, or little (152 rows of 8 pages 4.8 us, 5.3 with two
+// CTAs, of 16 query heads 5.4 and 7.8; 72 rows of 24 pages 6.1 with two, 6.7 with six).
+inline int splits_of_four_warps(int64_t rows, int pages, int resident) {
+    const int most = pages < 16 ? 1 : pages < 32 && rows >= 48 ? 2 : 8;
+    int splits = 1;
+    for (int s : {2, 3, 4, 6, 8})
+        if (s <= most && rows * s <= resident * kSms * 7 / 8 && pages >= 4 * s) splits = s;
+    return splits;
+}
 
 // Steps of a warp's ring.  Up to 8 query heads at head dim 128 one step, 32 KB
 // to a CTA and four CTAs to an SM, against two steps and three CTAs: 112 and 116
@@ -693,10 +808,11 @@ constexpr int stages_per_warp() {
     return spw < 1 ? 1 : spw;
 }
 
-template <int D, int BS, bool FP8, int NT, int NW, bool CHOOSE>
+template <int D, int BS, bool FP8, int NT, int NW, int MODE>
 static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a0, int num_rows,
                                int splits, cudaStream_t stream) {
     constexpr int SPW = stages_per_warp<D, BS, FP8, NT>();
+    constexpr bool CHOOSE = MODE == kChoose;
     using C = Shape<D, BS, FP8, NT, NW, SPW>;
     // The choice works where the ring will be: copies of bounds, then keys.  Long
     // shares take more shared memory than the ring.
@@ -708,7 +824,7 @@ static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, con
         smem = std::max(smem, 1024 + copy_bytes(NW * 32, D, a.select.stages) + keys);
     }
     constexpr int kMostSmem = CHOOSE ? std::max(C::SMEM, 1024 + copy_bytes(NW * 32, D, 2) + (kMaxKeys + 4) * 4) : C::SMEM;
-    auto kern = attend_kernel<D, BS, FP8, NT, NW, SPW, CHOOSE>;
+    auto kern = attend_kernel<D, BS, FP8, NT, NW, SPW, MODE>;
     static std::atomic<uint64_t> raised{0};
     pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), kMostSmem, raised);
     if (st != PA_OK) return st;
@@ -717,21 +833,21 @@ static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, con
 }
 
 // Eight warps to a CTA: only for the kernel that chooses, up to 8 query heads.
-template <int D, int BS, bool FP8, bool CHOOSE>
+template <int D, int BS, bool FP8, int MODE>
 static pa_status launch_group(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int num_rows, int splits,
                               int warps, cudaStream_t stream) {
-    if (a.group > 8) return launch_attend<D, BS, FP8, 2, 4, CHOOSE>(tk, tv, a, num_rows, splits, stream);
-    if constexpr (CHOOSE)
-        if (warps == 8) return launch_attend<D, BS, FP8, 1, 8, CHOOSE>(tk, tv, a, num_rows, splits, stream);
-    return launch_attend<D, BS, FP8, 1, 4, CHOOSE>(tk, tv, a, num_rows, splits, stream);
+    if (a.group > 8) return launch_attend<D, BS, FP8, 2, 4, MODE>(tk, tv, a, num_rows, splits, stream);
+    if constexpr (MODE == kChoose)
+        if (warps == 8) return launch_attend<D, BS, FP8, 1, 8, MODE>(tk, tv, a, num_rows, splits, stream);
+    return launch_attend<D, BS, FP8, 1, 4, MODE>(tk, tv, a, num_rows, splits, stream);
 }
 
-template <bool CHOOSE>
+template <int MODE>
 static pa_status launch_any(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv,
                             const Args &a, int num_rows, int splits, int warps, cudaStream_t stream) {
     auto shape = [&](auto d, auto bs) {
-        return fp8 ? launch_group<d.value, bs.value, true, CHOOSE>(tk, tv, a, num_rows, splits, warps, stream)
-                   : launch_group<d.value, bs.value, false, CHOOSE>(tk, tv, a, num_rows, splits, warps, stream);
+        return fp8 ? launch_group<d.value, bs.value, true, MODE>(tk, tv, a, num_rows, splits, warps, stream)
+                   : launch_group<d.value, bs.value, false, MODE>(tk, tv, a, num_rows, splits, warps, stream);
     };
     using I64 = std::integral_constant<int, 64>;
     using I128 = std::integral_constant<int, 128>;

@@ -52,20 +52,6 @@ struct Launch {
     bool longest_first;
 };
 
-// Four warps to a CTA: the most CTAs whose clusters are all resident at once and
-// whose warps have a page each.  An eighth of the CTAs' places is kept back:
-// clusters of three, six or eight leave some of a GPC's places empty (8 rows of
-// 8 heads, 16 queries each, 128K tokens: 62 us with 6, 71 with 4, 85 with 8).
-// Short lists are not shared out, or little (152 rows of 8 pages 4.8 us, 5.3 with two
-// CTAs, of 16 query heads 5.4 and 7.8; 72 rows of 24 pages 6.1 with two, 6.7 with six).
-static int splits_of_four_warps(int64_t rows, int pages, int resident) {
-    const int most = pages < 16 ? 1 : pages < 32 && rows >= 48 ? 2 : 8;
-    int splits = 1;
-    for (int s : {2, 3, 4, 6, 8})
-        if (s <= most && rows * s <= resident * kSms * 7 / 8 && pages >= 4 * s) splits = s;
-    return splits;
-}
-
 // The kernel that chooses takes CTAs of eight warps while a CTA for every row
 // and KV head is resident (up to 8 query heads): half the cluster for the same
 // warps, and most of a choice's steps are waits for the whole cluster.
@@ -160,7 +146,7 @@ static pa_status run_attend(const Call &c, const SelectArgs *select, cudaStream_
         return launch_chosen(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, l.splits, l.warps, stream);
     }
     const int splits = c.splits ? c.splits : splits_of_four_warps(rows, c.top_k, resident);
-    return launch_any<false>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, 4, stream);
+    return launch_any<kList>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, 4, stream);
 }
 
 }  // namespace sparse

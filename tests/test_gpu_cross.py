@@ -1,0 +1,183 @@
+"""Cross attention over the paged cache against its definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import Guarded
+from paged_kv_cache_193_gb300 import _lib
+from rows_cases import Cross, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api(cuda_device):
+    from paged_kv_cache_193_gb300 import api as a
+    a._lib_handle()
+    return a
+
+
+CASES = [
+    dict(rows=[1], states=[1], Hq=1, Hkv=1, D=64),
+    dict(rows=[1], states=[1500], Hq=4, Hkv=4, D=64),
+    dict(rows=[1, 1, 1], states=[63, 64, 65], Hq=8, Hkv=2),
+    dict(rows=[5, 5], states=[700, 333], Hq=8, Hkv=2),
+    dict(rows=[0, 3, 0, 7], states=[10, 0, 0, 40], Hq=6, Hkv=2, B=32),
+    dict(rows=[33, 1, 129], states=[15, 16, 17], Hq=4, Hkv=1),
+    dict(rows=[64, 65, 31], states=[100, 48, 256], Hq=2, Hkv=1, D=64, B=32),
+    dict(rows=[18, 19, 37], states=[90, 5, 128], Hq=7, Hkv=1),                # 18 rows of 7 heads to a tile
+    dict(rows=[9, 17, 2], states=[64, 300, 2], Hq=16, Hkv=1, D=64),
+    dict(rows=[11, 40], states=[130, 31], Hq=10, Hkv=2, fp8=True),
+    dict(rows=[11, 40, 1], states=[130, 31, 900], Hq=6, Hkv=2, D=64, fp8=True, per_head=True),
+    dict(rows=[3, 70], states=[1000, 65], Hq=8, Hkv=2, B=32, fp8=True, per_head=True),
+    dict(rows=[0, 2, 5], states=[7, 0, 1], Hq=8, Hkv=2, D=64, B=32, fp8=True),
+    dict(rows=[2, 3], states=[40, 50], Hq=8, Hkv=2, gap=4),                   # rows of no sequence
+    dict(rows=[2, 3], states=[40, 50], Hq=8, Hkv=2, extra=300),               # a table wider than its states
+    dict(rows=[4, 1], states=[3000, 2999], Hq=8, Hkv=2),
+    dict(rows=[2] * 80, states=[(37 * i) % 90 for i in range(80)], Hq=4, Hkv=2, D=64),  # one part
+    dict(rows=[130] * 5, states=[200, 0, 64, 65, 1], Hq=16, Hkv=8, D=64),
+]
+
+
+@pytest.mark.parametrize("kw", CASES, ids=[f"{i}" for i in range(len(CASES))])
+def test_matches_the_definition(api, cuda_device, kw):
+    case = Cross(cuda_device, **kw)
+    T, Hq, D = case.q.shape
+    n = api.cross_workspace_size(T, len(case.rows), min(case.most, T), Hq, case.pool.Hkv, D, case.bt.shape[1], case.pool.B)
+    ws = Guarded((n,), torch.uint8, cuda_device)
+    out = Guarded(case.q.shape, torch.bfloat16, cuda_device, fill=-7.0)
+    k0, q0 = case.pool.kd.clone(), case.q.clone()
+    got = case.call(api, workspace=ws.tensor if n else None, out=out.tensor)
+    torch.cuda.synchronize()
+    assert got.data_ptr() == out.tensor.data_ptr() and api.device_errors() == 0
+    want = case.expected()
+    live = T - case.gap
+    within(got[:live], want)
+    assert (got[live:] == -7).all()
+    for i, s in enumerate(case.seq):
+        assert case.states[s] or (got[i] == 0).all()
+    ws.check("workspace")
+    out.check("out")
+    assert torch.equal(case.q, q0) and torch.equal(case.pool.kd.view(torch.uint8), k0.view(torch.uint8))
+    assert torch.equal(case.call(api)[:live], got[:live])
+    q = case.q.clone()
+    assert torch.equal(case.call(api, q=q, out=q)[:live], got[:live])
+    assert torch.equal(q[live:], q0[live:])
+    within(case.call(api, most=10 ** 6)[:live], want, "a bound far above the rows")
+
+
+def test_one_row_is_the_decode(api, cuda_device):
+    """One row a sequence is what the decode kernel computes over the same table."""
+    case = Cross(cuda_device, [1] * 5, [1, 20, 333, 64, 1000], 8, 2)
+    a = case.call(api)
+    b = api.decode(case.q, case.pool.kd, case.pool.vd, case.bt, case.sl, case.scale)
+    assert (a.float() - b.float()).abs().max() <= 2.0 ** -6
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [[3, 40], [300, 2]])
+def test_large_scores(api, cuda_device, fp8, rows):
+    case = Cross(cuda_device, rows, [900, 333], 8, 2, fp8=fp8, spread=30.0 if not fp8 else 20.0)
+    within(case.call(api), case.expected())
+
+
+def test_infinities_stay_where_they_are(api, cuda_device):
+    case = Cross(cuda_device, [3, 3], [200, 100], 4, 2)
+    want = case.expected()
+    case.pool.vd[int(case.tables[0, 2]), 1, 4, 9] = float("inf")
+    got = case.call(api).float().cpu()
+    assert torch.isinf(got[:3, 2:, 9]).all()
+    keep = np.ones(got.shape, bool)
+    keep[:3, 2:, 9] = False
+    assert (np.abs(got.numpy() - want[0]) <= want[1])[keep].all()
+
+
+def test_refused_rows_are_reported_and_left(api, cuda_device):
+    case = Cross(cuda_device, [3, 40, 2], [200, 100, 50], 4, 2)
+    want = case.expected()
+    out = Guarded(case.q.shape, torch.bfloat16, cuda_device, fill=-7.0)
+    got = case.call(api, most=39, out=out.tensor)  # one sequence has more
+    torch.cuda.synchronize()
+    assert api.device_errors() == _lib.PA_DEVERR_BAD_CONTEXT
+    assert (got[3:43] == -7).all()
+    within(got[:3], tuple(x[:3] for x in want))
+    within(got[43:], tuple(x[43:] for x in want))
+    for start in ([0, 3, 43, 46], [0, 3, 2, 45], [-1, 3, 43, 45], [2 ** 31 - 1, -2 ** 31, 43, 45]):
+        case.qs.copy_(torch.tensor(start, dtype=torch.int32))
+        case.call(api, out=out.tensor)
+        torch.cuda.synchronize()
+        assert api.device_errors() == _lib.PA_DEVERR_BAD_CONTEXT
+        out.check(str(start))
+
+
+def test_bad_blocks_and_lengths(api, cuda_device):
+    case = Cross(cuda_device, [3, 2], [200, 100], 4, 2)
+    case.bt[0, 2] = 10 ** 6
+    assert torch.isfinite(case.call(api)).all() and api.device_errors() == _lib.PA_DEVERR_BAD_BLOCK
+    case.bt.copy_(case.tables)
+    case.sl[1] = 10 ** 6
+    case.call(api)
+    assert api.device_errors() & _lib.PA_DEVERR_BAD_CONTEXT
+    case.sl[1] = -4
+    assert (case.call(api)[3:] == 0).all() and api.device_errors() == 0
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [300, 200]])
+def test_captured_and_replayed(api, cuda_device, rows):
+    case = Cross(cuda_device, rows, [700, 90], 8, 2, D=64)
+    want = case.expected()
+    out = torch.empty_like(case.q)
+    ws = api.alloc_cross_workspace(case.q, case.pool.kd, case.bt, case.most)
+    case.call(api, workspace=ws, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        case.call(api, workspace=ws, out=out)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        within(out, want)
+    case.sl[0], case.states = 77, [77, 90]
+    g.replay()
+    torch.cuda.synchronize()
+    within(out, case.expected())
+
+
+def test_on_another_stream_and_back_to_back(api, cuda_device):
+    case = Cross(cuda_device, [2, 3], [500, 900], 8, 2)
+    ws = api.alloc_cross_workspace(case.q, case.pool.kd, case.bt, case.most)
+
+    def chain(after, stream=None):
+        x, got = case.q.clone(), []
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            for _ in range(40):
+                y = case.call(api, q=x, workspace=ws, stream=stream)
+                after()
+                x = (y * 3).contiguous()
+                after()
+                got.append(y)
+        return got
+
+    want = chain(torch.cuda.synchronize)
+    for stream in (None, torch.cuda.Stream()):
+        got = chain(lambda: None, stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_wait_that_runs_out(api, cuda_device):
+    lib = _lib.load()
+    for fp8 in (False, True):
+        for rows in ([2, 3], [300, 3]):
+            case = Cross(cuda_device, rows, [500, 900], 8, 2, fp8=fp8)
+            assert lib.pa_test_set_wait(1_000_000, 1) == 0
+            try:
+                case.call(api)
+                torch.cuda.synchronize()
+            finally:
+                assert lib.pa_test_set_wait(0, 0) == 0
+            assert api.device_errors() & _lib.PA_DEVERR_TIMEOUT
+            within(case.call(api), case.expected())
+            assert api.device_errors() == 0
