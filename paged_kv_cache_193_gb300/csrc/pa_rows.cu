@@ -367,8 +367,6 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)  // as the copy's swizzle laid it: 128-byte rows, or 64-byte ones
                     e[c] = lds128(from + rs * L::kRaw + ((D == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3)) << 4));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&raw_empty[x][rs]));
                 const bool valid = kb * kKeys + r < left;
                 ok = ok && wait(kv_empty[st], (kb / kStages & 1) ^ 1);
 #pragma unroll
@@ -387,7 +385,12 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&kv_full[st]));
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&kv_full[st]));
+                    // Not before the stores, which wait for the loads: an arrival does not,
+                    // and the next page would land on what is still to be read.
+                    mbar_arrive(smem_addr(&raw_empty[x][rs]));
+                }
             }
             if (!ok && lane == 0) fail();
         }

@@ -181,3 +181,30 @@ def test_a_wait_that_runs_out(api, cuda_device):
             assert api.device_errors() & _lib.PA_DEVERR_TIMEOUT
             within(case.call(api), case.expected())
             assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_runs_give_the_same_bits_every_time(api, cuda_device, fp8, D):
+    """Enough rows that no run is cut into parts, so every ring of stages goes round many times, and enough CTAs that a page
+    landing too early would be seen; sampled rows against the definition."""
+    g = torch.Generator(device=cuda_device).manual_seed(3)
+    S, n, Hq, Hkv, B, rows = 40, 2029, 24, 8, 32, 126
+    MB = -(-n // B)
+    kv = torch.randn(2, S * MB, Hkv, B, D, generator=g, device=cuda_device)
+    kv = (kv * 16).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else kv.to(torch.bfloat16)
+    q = torch.randn(S * rows, Hq, D, generator=g, device=cuda_device).to(torch.bfloat16)
+    tables = torch.randperm(S * MB, generator=g, device=cuda_device).view(S, MB).to(torch.int32)
+    lens = torch.full((S,), n, dtype=torch.int32, device=cuda_device)
+    start = torch.arange(0, S * rows + 1, rows, dtype=torch.int32, device=cuda_device)
+    outs = [api.cross_attention(q, kv[0], kv[1], tables, lens, start, rows, kv_scale=1 / 16).clone() for _ in range(20)]
+    assert all(torch.equal(o, outs[0]) for o in outs) and api.device_errors() == 0
+    for s in (0, 17, 39):
+        k, v = ((c.view(torch.float8_e4m3fn).double() / 16 if fp8 else c.double())[tables[s].long()].transpose(0, 1).flatten(1, 2)[:, :n]
+                for c in kv)
+        x = q[s * rows:(s + 1) * rows].double().view(rows, Hkv, 3, D).permute(1, 2, 0, 3).flatten(1, 2)
+        p = torch.softmax(x @ k.transpose(1, 2) * D ** -0.5, -1)
+        want, mass = p @ v, p @ v.abs()
+        got = outs[0][s * rows:(s + 1) * rows].double().view(rows, Hkv, 3, D).permute(1, 2, 0, 3).flatten(1, 2)
+        # the output's rounding, and one of each probability (2^-8 of it in bf16, 2^-11 in fp16)
+        assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 if fp8 else 2.0 ** -8) * mass + 2.0 ** -14).all()
