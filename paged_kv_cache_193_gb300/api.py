@@ -634,9 +634,10 @@ def sparse_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
 
 
 def shared_prefix_workspace_size(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
-                                 head_dim: int, block_size: int, max_prefix_blocks: int) -> int:
+                                 head_dim: int, block_size: int, max_prefix_blocks: int,
+                                 kv_dtype: int = PA_KV_BF16) -> int:
     return int(_lib_handle().pa_shared_prefix_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads,
-                                                             head_dim, block_size, max_prefix_blocks))
+                                                             head_dim, block_size, max_prefix_blocks, kv_dtype))
 
 
 def alloc_shared_prefix_workspace(q: torch.Tensor, k_cache: torch.Tensor, group_start: torch.Tensor,
@@ -644,7 +645,7 @@ def alloc_shared_prefix_workspace(q: torch.Tensor, k_cache: torch.Tensor, group_
     """Workspace of shared_prefix_decode for these sizes (None: none needed)."""
     S, Hq, D = q.shape
     n = shared_prefix_workspace_size(S, group_start.shape[0] - 1, Hq, k_cache.shape[1], D, k_cache.shape[2],
-                                     max_prefix_blocks)
+                                     max_prefix_blocks, cache_dtype_of(k_cache))
     return _empty((n,), torch.uint8, q.device, stream) if n else None
 
 

@@ -5,16 +5,20 @@
 //
 // The rows' products are pa_rows.cu's.  With few rows to a batch a run of states
 // is cut into parts, so that all SMs read it, and the kernel here joins them:
-// a warp to a row, whose parts' weights are made once, a lane to a part.
+// a warp to a row, whose parts' weights are made once, a lane to a part.  Up to 16
+// rows of a KV head (one decoded token, some beams) go to pa_sparse_attend.cuh.
 #include <math.h>
 
-#include "pa_rows.cuh"
-#include "pa_sparse.cuh"
+#include "pa_sparse_attend.cuh"
 
 namespace pa {
 namespace rows {
 
 constexpr int kJoinWarps = 8;
+// Up to so many rows (a sequence's tokens times a KV head's group) go to the kernel
+// of the block-sparse decode, which attends to whole tables as well: its products
+// take the rows as they are, where a tile has 128, and it needs no workspace.
+constexpr int kFewRows = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, const float v_scale, __nv_bfloat16 *out) {
@@ -61,9 +65,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, con
         *reinterpret_cast<uint32_t *>(to) = pack2<false>(acc[0], acc[1]);
 }
 
-static int cross_parts(int64_t num_seqs, int max_query_len, int num_q_heads, int num_kv_heads, int max_blocks, int block_size) {
-    const int64_t ctas = tile_pairs(max_query_len, num_q_heads / num_kv_heads) * num_kv_heads * num_seqs;
-    return choose_parts(ctas, static_cast<int>((static_cast<int64_t>(max_blocks) * block_size + kKeys - 1) / kKeys));
+// How a call is launched: by its sizes alone, which the workspace's size goes by too.
+struct Plan {
+    bool few;   // one kernel for a handful of rows
+    int tiles;  // else: to a CTA
+    int parts;  // of each run
+};
+
+static Plan plan(int64_t num_seqs, int64_t num_tokens, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                 int max_blocks, int block_size) {
+    const int group = num_q_heads / num_kv_heads;
+    if (static_cast<int64_t>(max_query_len) * group <= kFewRows) return {true, 0, 1};
+    const int tiles = max_query_len <= tile_rows(1) / group ? 1 : 2;
+    const int64_t ctas = tile_ctas(max_query_len, group, tiles) * num_kv_heads * num_seqs;
+    const int blocks = static_cast<int>((static_cast<int64_t>(max_blocks) * block_size + kKeys - 1) / kKeys);
+    return {false, tiles, choose_parts(ctas, blocks, tiles, head_dim, num_tokens * num_q_heads, num_seqs == 1, true)};
 }
 
 }  // namespace rows
@@ -80,8 +96,9 @@ size_t pa_cross_workspace_size(int num_tokens, int num_seqs, int max_query_len, 
         num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16 || head_dim <= 0 || max_blocks_per_seq <= 0 || block_size <= 0 ||
         static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
         return 0;
-    const int parts = cross_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads, max_blocks_per_seq, block_size);
-    return parts == 1 ? 0 : workspace_bytes(parts, static_cast<int64_t>(num_tokens) * num_q_heads, head_dim);
+    if (max_query_len > num_tokens) max_query_len = num_tokens;
+    const Plan p = plan(num_seqs, num_tokens, max_query_len, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size);
+    return p.parts > 1 ? workspace_bytes(p.parts, static_cast<int64_t>(num_tokens) * num_q_heads, head_dim) : 0;
 }
 
 pa_status pa_cross_attention(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
@@ -102,15 +119,48 @@ pa_status pa_cross_attention(const void *q, const void *k_cache, const void *v_c
     if (!query_start) return fail(PA_ERR_INVALID_ARG, "null pointer");
     st = check_row_pointers(q, k_cache, v_cache, block_tables, state_lens, out, num_tokens, num_q_heads, head_dim);
     if (st != PA_OK) return st;
-    const int parts = cross_parts(num_seqs, max_query_len, num_q_heads, num_kv_heads, max_blocks_per_seq, block_size);
+    const Plan p = plan(num_seqs, num_tokens, max_query_len, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size);
     const int64_t num_rows = static_cast<int64_t>(num_tokens) * num_q_heads;
-    if (parts > 1) {
-        st = check_workspace(workspace, workspace_bytes, rows::workspace_bytes(parts, num_rows, head_dim), q, out,
+    if (p.parts > 1) {
+        st = check_workspace(workspace, workspace_bytes, rows::workspace_bytes(p.parts, num_rows, head_dim), q, out,
                              static_cast<size_t>(num_rows) * head_dim * 2);
         if (st != PA_OK) return st;
     }
     unsigned int *err = device_error_word();
     if (!err) return fail(PA_ERR_CUDA, "cannot resolve the device error word");
+    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
+    const int group = num_q_heads / num_kv_heads;
+    if (p.few) {
+        const int64_t pool_rows = static_cast<int64_t>(num_blocks) * num_kv_heads * block_size;
+        CUtensorMap tk, tv;
+        st = make_map(&tk, k_cache, fp8, head_dim, pool_rows, block_size);
+        if (st == PA_OK) st = make_map(&tv, v_cache, fp8, head_dim, pool_rows, block_size);
+        if (st != PA_OK) return st;
+        sparse::Args b = {};
+        b.q = static_cast<const __nv_bfloat16 *>(q);
+        b.block_tables = block_tables;
+        b.context_lens = state_lens;
+        b.out = static_cast<__nv_bfloat16 *>(out);
+        b.max_blocks = max_blocks_per_seq;
+        b.num_blocks = num_blocks;
+        b.num_q_heads = num_q_heads;
+        b.num_kv_heads = num_kv_heads;
+        b.group = group;
+        b.softmax_log2 = softmax_scale * 1.4426950408889634f;
+        b.kv_scale = kv_scale;
+        b.k_scales = k_scales;
+        b.v_scales = v_scales;
+        b.err = err;
+        b.wait_limit_ns = wait_limit_ns();
+        b.stall_first_wait = stall_first_wait();
+        b.query_start = query_start;
+        b.num_tokens = num_tokens;
+        b.max_query_len = max_query_len;
+        const int live = max_query_len * group;
+        const int splits = sparse::splits_of_four_warps(static_cast<int64_t>(num_seqs) * num_kv_heads, max_blocks_per_seq,
+                                                        sparse::resident_ctas(head_dim, block_size, fp8, live));
+        return sparse::launch_any<sparse::kRows>(head_dim, block_size, fp8, tk, tv, b, num_seqs, splits, 4, stream, live);
+    }
     a.block_tables = block_tables;
     a.lens = state_lens;
     a.max_blocks = max_blocks_per_seq;
@@ -118,7 +168,7 @@ pa_status pa_cross_attention(const void *q, const void *k_cache, const void *v_c
     a.block_size = block_size;
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = num_kv_heads;
-    a.group = num_q_heads / num_kv_heads;
+    a.group = group;
     a.num_tokens = num_tokens;
     a.num_seqs = num_seqs;
     a.max_query_len = max_query_len;
@@ -126,18 +176,17 @@ pa_status pa_cross_attention(const void *q, const void *k_cache, const void *v_c
     a.kv_scale = kv_scale;
     a.k_scales = k_scales;
     a.v_scales = v_scales;
-    a.parts = parts;
+    a.parts = p.parts;
     a.query_start = query_start;
     a.err = err;
-    if (parts == 1) {
+    if (p.parts == 1) {
         a.out = static_cast<__nv_bfloat16 *>(out);
     } else {
         a.part_o = static_cast<float *>(workspace);
-        a.part_ml = reinterpret_cast<float2 *>(a.part_o + parts * num_rows * head_dim);
+        a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.parts * num_rows * head_dim);
     }
-    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
-    st = launch_rows(q, k_cache, v_cache, head_dim, fp8, a, tile_pairs(max_query_len, a.group), num_seqs, stream);
-    if (st != PA_OK || parts == 1) return st;
+    st = launch_rows(q, k_cache, v_cache, head_dim, fp8, a, p.tiles, tile_ctas(max_query_len, group, p.tiles), num_seqs, stream);
+    if (st != PA_OK || p.parts == 1) return st;
     const int64_t join = (static_cast<int64_t>(max_query_len) * num_q_heads + kJoinWarps - 1) / kJoinWarps;
     const dim3 grid(static_cast<unsigned>(join), num_seqs);
     const float v_scale = fp8 ? kv_scale : 1.f;

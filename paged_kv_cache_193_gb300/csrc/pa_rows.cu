@@ -26,7 +26,10 @@
 #include <limits.h>
 #include <math.h>
 
+#include <cmath>
+
 #include <atomic>
+#include <type_traits>
 
 #include "pa_prefill.cuh"
 #include "pa_rows.cuh"
@@ -36,10 +39,8 @@ namespace pa {
 
 namespace rows {
 
-constexpr int kLoadK = 8, kLoadV = 10, kMma0 = 9, kMma1 = 11, kWiden = 12;  // warps
-constexpr int kQSlab = kRows * 128;   // 64 dims of a tile's queries
 constexpr int kKVSlab = kKeys * 128;  // 64 dims of a block's keys or values
-constexpr int kTmemCols = 512;        // a tile: S at 0 and 64, O at 128
+constexpr int kTileCols = 256;        // of tensor memory: S at 0 and 64, O at 128
 constexpr int kOCol = 128;
 constexpr float kLazy = 8.f;
 // fp16 probabilities are taken times 2^7: up to 2^15 against the reference's
@@ -47,20 +48,55 @@ constexpr float kLazy = 8.f;
 constexpr float kRaise = 128.f;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
-template <int D, bool FP8>
+// Two tiles of 128 rows, one CTA to an SM; or one of up to 64, two CTAs to an SM:
+// then the rows are few, the pages' copies are what takes the time, and one CTA's
+// begin and end go by under the other's.  (Both kinds' products have 128 rows: of the
+// small tile's, the upper ones are whatever lies behind it in shared memory, and
+// nobody reads them.)
+template <int D, bool FP8, int TILES>
 struct Layout {
-    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kTileRows = tile_rows(TILES);
+    static constexpr int kCtas = TILES == 1 ? 2 : 1;
+    // warps: the softmax's, 32 rows to each; the copies of K and of V (one warp for
+    // both where a tile is alone); the products; the widening of E4M3
+    static constexpr int kSoft = TILES * kTileRows / 32;
+    static constexpr int kLoadK = kSoft, kMma0 = kSoft + 1;
+    static constexpr int kLoadV = TILES == 2 ? kSoft + 2 : kLoadK, kMma1 = TILES == 2 ? kSoft + 3 : -1;
+    static constexpr int kWiden = kSoft + 2 * TILES;
+    static constexpr int kThreads = 32 * (kWiden + (FP8 ? 4 : 0));
+    // Where 512 threads leave 128 registers to each, a row's scores do not stay in them:
+    // half of a block's are read again for their powers.  (E4M3, 40 sequences: 148 us,
+    // 187 with all of them held and some of them spilled.)
+    static constexpr bool kReread = kThreads * kCtas == 512;
     static constexpr int kSlabs = D / 64;
+    static constexpr int kQSlab = kTileRows * 128;  // 64 dims of a tile's queries
     static constexpr int kQTile = kSlabs * kQSlab;
     static constexpr int kStage = kSlabs * kKVSlab;  // a block of K, or of V, as 16-bit rows
-    static constexpr int kStages = (FP8 ? 3 : 5) * 2 / kSlabs;
+    static constexpr int kStages = (TILES == 2 ? (FP8 ? 6 : 10) : FP8 ? 4 : 6) / kSlabs;
     static constexpr int kRaw = kKeys * D;  // a block of E4M3 K, or V
-    static constexpr int kRawStages = FP8 ? 4 * 2 / kSlabs : 0;
-    static constexpr int kK = kTiles * kQTile;
+    static constexpr int kRawStages = !FP8 ? 0 : (TILES == 2 ? 8 : 4) / kSlabs;
+    static constexpr int kK = TILES * kQTile;
     static constexpr int kV = kK + kStages * kStage;
     static constexpr int kRawK = kV + kStages * kStage;
     static constexpr int kRawV = kRawK + kRawStages * kRaw;
-    static constexpr int kSmem = kRawV + kRawStages * kRaw + 1024;
+    static constexpr int kBars = kRawV + kRawStages * kRaw;  // the barriers behind it all
+    static constexpr int kSmem = kBars + 768;
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+// Barriers.  kv_full, kv_empty: a stage's K and V are in place, have been read by the
+// products of all tiles.  raw_full, raw_empty: E4M3 K (0) and V (1) pages have landed,
+// have been read.  q_conv: a tile's queries are fp16.  Of each tile: S(j) is in buffer
+// j % 2, P(j) is over it, PV(j) is done, all is done.  stall: never completed.
+template <class L, int TILES>
+struct Bars {
+    static constexpr int kRawStages = L::kRawStages > 0 ? L::kRawStages : 1;
+    uint64_t q_full, v_zeroed, stall;
+    uint64_t kv_full[L::kStages], kv_empty[L::kStages];
+    uint64_t raw_full[2][kRawStages], raw_empty[2][kRawStages];
+    uint64_t q_conv[TILES], s_full[TILES][2], p_full[TILES][2], pv_done[TILES], drain[TILES];
+    uint32_t tmem_base;
+    int failed;
 };
 
 // Which rows and which keys a CTA has.
@@ -74,6 +110,7 @@ struct Work {
 };
 
 // Called by whole warps; every warp comes to the same answer.  False: nothing to do.
+template <int TILES>
 __device__ __forceinline__ bool find_work(const Args &a, Work &w) {
     const int lane = threadIdx.x & 31;
     const int cap = a.max_blocks * a.block_size;
@@ -82,7 +119,7 @@ __device__ __forceinline__ bool find_work(const Args &a, Work &w) {
     if (!a.group_start) {
         const int s = blockIdx.z;
         const bool good = query_range(a, s, w.token0, w.tokens);
-        w.at = kTiles * pair * a.tile_tokens;
+        w.at = TILES * pair * a.tile_tokens;
         w.table = s;
         w.keys = max(a.lens[s], 0);
         if (!good || w.keys > cap) {
@@ -102,7 +139,7 @@ __device__ __forceinline__ bool find_work(const Args &a, Work &w) {
             hi = min(max(a.group_start[g + 1], lo), a.num_seqs);
             n = min(max(a.prefix_blocks[g], 0), a.max_prefix_blocks);
         }
-        const int mine = (hi - lo + kTiles * a.tile_tokens - 1) / (kTiles * a.tile_tokens);
+        const int mine = (hi - lo + TILES * a.tile_tokens - 1) / (TILES * a.tile_tokens);
         int before = mine;  // sum of the lanes' up to and with this one
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -125,11 +162,11 @@ __device__ __forceinline__ bool find_work(const Args &a, Work &w) {
     if (!found || pages == 0) return false;
     w.token0 = first;
     w.tokens = end - first;
-    w.at = kTiles * pair * a.tile_tokens;
+    w.at = TILES * pair * a.tile_tokens;
     w.keys = pages * a.block_size;
     // The table row of the pair's first sequence that has the whole prefix; the
     // others have none of it to themselves, and their rows here are not read.
-    const int s0 = first + w.at, s1 = min(end, s0 + kTiles * a.tile_tokens);
+    const int s0 = first + w.at, s1 = min(end, s0 + TILES * a.tile_tokens);
     w.table = -1;
     for (int s = s0; s < s1 && w.table < 0; s += 32) {
         const int len = s + lane < s1 ? a.lens[s + lane] : 0;
@@ -139,25 +176,20 @@ __device__ __forceinline__ bool find_work(const Args &a, Work &w) {
     return w.table >= 0;
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
+template <int D, bool FP8, int TILES>
+__global__ void __launch_bounds__(Layout<D, FP8, TILES>::kThreads, Layout<D, FP8, TILES>::kCtas)
     rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const Args a) {
-    using L = Layout<D, FP8>;
-    constexpr int kStages = L::kStages, kRawStages = FP8 ? L::kRawStages : 1;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t q_full, v_zeroed, stall_bar;
-    // a stage's K and V are in place (kv_full); both tiles' products have read it (kv_empty)
-    __shared__ __align__(8) uint64_t kv_full[kStages], kv_empty[kStages];
-    // E4M3 K (0) and V (1) pages have landed, have been read; a tile's queries are fp16
-    __shared__ __align__(8) uint64_t raw_full[2][kRawStages], raw_empty[2][kRawStages], q_conv[kTiles];
-    // per tile: S(j) is in buffer j % 2, P(j) is over it, PV(j) is done, all is done
-    __shared__ __align__(8) uint64_t s_full[kTiles][2], p_full[kTiles][2], pv_done[kTiles], drain[kTiles];
-    __shared__ uint32_t tmem_base_s;
-    __shared__ int failed_s;
+    using L = Layout<D, FP8, TILES>;
+    constexpr int kLoadK = L::kLoadK, kLoadV = L::kLoadV, kMma0 = L::kMma0, kMma1 = L::kMma1, kWiden = L::kWiden;
+    constexpr uint32_t kTmemCols = TILES * kTileCols;
+    constexpr int kStages = L::kStages, kRawStages = FP8 ? L::kRawStages : 1, kQSlab = L::kQSlab;
+    // No static shared memory lies in front, so the base is where the swizzle wants it.
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Bars<L, TILES> &bar = *reinterpret_cast<Bars<L, TILES> *>(smem_raw + L::kBars);
+    static_assert(sizeof(Bars<L, TILES>) <= L::kSmem - L::kBars, "room for the barriers");
 
-    const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t base = smem_addr(smem_raw);
     const uint64_t limit = a.wait_limit_ns;
     const int h = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -167,15 +199,15 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
     // them, and waits for this one's end itself.
     if (a.group_start) dependent_release();
     Work w;
-    if (!find_work(a, w)) return;
+    if (!find_work<TILES>(a, w)) return;
     const int all = (w.keys + kKeys - 1) / kKeys, each = blocks_per_part(all, a.parts);
     const int first = w.part * each, nkb = min(each, all - first);  // this part's blocks
-    const int ntiles = w.at + a.tile_tokens < w.tokens ? 2 : 1;
+    const int ntiles = TILES == 2 && w.at + a.tile_tokens < w.tokens ? 2 : 1;
     auto tokens_of = [&](int T) { return min(a.tile_tokens, w.tokens - w.at - T * a.tile_tokens); };
     auto warps_of = [&](int T) { return (tokens_of(T) * a.group + 31) / 32; };  // with a live row
     if (nkb <= 0) {
         if (a.out && w.keys == 0) {  // nothing to attend to
-            const int n = min(w.tokens - w.at, kTiles * a.tile_tokens) * a.group * (D / 8);
+            const int n = min(w.tokens - w.at, TILES * a.tile_tokens) * a.group * (D / 8);
             for (int i = tid; i < n; i += L::kThreads) {
                 const int row = i / (D / 8), t = row / a.group;
                 __nv_bfloat16 *to = a.out + ((static_cast<int64_t>(w.token0) + w.at + t) * a.num_q_heads + h * a.group + row % a.group) * D;
@@ -192,47 +224,45 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
     const int32_t *table = a.block_tables + static_cast<int64_t>(w.table) * a.max_blocks;
     constexpr int kBehind = INT_MIN;
     auto page_entry = [&](int kb) {
-        const int page = (first + kb) * pages + lane;
-        return lane < pages && page * a.block_size < w.keys ? table[page] : kBehind;
+        const int at = TILES == 1 && lane >= pages ? lane - pages : lane;  // K's, then V's
+        const int page = (first + kb) * pages + at;
+        return at < pages && page * a.block_size < w.keys ? table[page] : kBehind;
     };
     const bool loader = warp == kLoadK || warp == kLoadV;
     const int e_first = loader ? page_entry(0) : kBehind;
 
-    if (tid == 0) {
-        mbar_init(smem_addr(&q_full), 1);
-        mbar_init(smem_addr(&v_zeroed), 1);
-        mbar_init(smem_addr(&stall_bar), 1);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_addr(&kv_full[i]), FP8 ? 4 : 2);  // the widening warps, or the loaders
-            mbar_init(smem_addr(&kv_empty[i]), ntiles);
+    if (warp == 0) {  // a barrier to a lane: one lane alone takes as long as the first table entry
+        auto init = [&](uint64_t *bars, int n, int count) {
+            if (lane < n) mbar_init(smem_addr(bars + lane), count);
+        };
+        init(&bar.q_full, 3, 1);  // and v_zeroed, stall
+        init(bar.kv_full, kStages, FP8 ? 4 : TILES);  // the widening warps, or the loaders
+        init(bar.kv_empty, kStages, ntiles);          // those that read the block
+        if constexpr (FP8) {
+            init(bar.raw_full[0], 2 * kRawStages, 1);
+            init(bar.raw_empty[0], 2 * kRawStages, 2);
         }
-        if constexpr (FP8)
-            for (int i = 0; i < 2 * kRawStages; ++i) {
-                mbar_init(smem_addr(&raw_full[i & 1][i >> 1]), 1);
-                mbar_init(smem_addr(&raw_empty[i & 1][i >> 1]), 2);
-            }
-        for (int t = 0; t < ntiles; ++t) {
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_addr(&s_full[t][b]), 1);
-                mbar_init(smem_addr(&p_full[t][b]), warps_of(t));
-            }
-            mbar_init(smem_addr(&pv_done[t]), 1);
-            mbar_init(smem_addr(&drain[t]), 1);
-            mbar_init(smem_addr(&q_conv[t]), warps_of(t));
-        }
-        failed_s = 0;
+        init(bar.s_full[0], 2 * TILES, 1);
+        for (int T = 0; T < TILES; ++T) init(bar.p_full[T], 2, T < ntiles ? warps_of(T) : 1);
+        init(bar.pv_done, TILES, 1);
+        init(bar.drain, TILES, 1);
+        for (int T = 0; T < TILES; ++T) init(bar.q_conv + T, 1, T < ntiles ? warps_of(T) : 1);
         fence_barrier_init();
+        __syncwarp();
+    }
+    if (tid == 0) {
+        bar.failed = 0;
         const int q_box = D * 2 * a.group * a.tile_tokens;
-        mbar_arrive_expect_tx(smem_addr(&q_full), ntiles * q_box);
+        mbar_arrive_expect_tx(smem_addr(&bar.q_full), ntiles * q_box);
         for (int T = 0; T < ntiles; ++T)
             for (int sl = 0; sl < L::kSlabs; ++sl)
                 tma_load_3d(base + T * L::kQTile + sl * kQSlab, &tmQ, sl * 64, h * a.group,
-                            w.token0 + w.at + T * a.tile_tokens, smem_addr(&q_full));
+                            w.token0 + w.at + T * a.tile_tokens, smem_addr(&bar.q_full));
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
     if (warp == kMma0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base_s)),
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bar.tmem_base)),
                      "r"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -240,26 +270,27 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base_s;
+    const uint32_t tmem = bar.tmem_base;
     auto fail = [&]() {
         set_device_error(a.err, PA_DEVERR_TIMEOUT);
-        atomicExch(&failed_s, 1);
+        atomicExch(&bar.failed, 1);
     };
     // a whole warp waits
-    auto wait = [&](uint64_t &bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_suspend(smem_addr(&bar), parity, limit)) != 0;
+    auto wait = [&](uint64_t &b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_suspend(smem_addr(&b), parity, limit)) != 0;
     };
 
     if (loader) {
         // ---------------- copies of pages ----------------
-        const bool is_k = warp == kLoadK;
+        // K (0) or V (1), or the first and the second half of the lanes that have a page
+        constexpr bool kBoth = TILES == 1;
+        const int x = kBoth ? (lane >= pages) : warp != kLoadK, page = kBoth && lane >= pages ? lane - pages : lane;
         const int rows_total = a.num_blocks * a.num_kv_heads * a.block_size;
-        const CUtensorMap *map = is_k ? &tmK : &tmV;
+        const CUtensorMap *map = x == 0 ? &tmK : &tmV;
         const uint64_t policy = l2_evict_first_policy();
         constexpr int kRing = FP8 ? kRawStages : kStages;
         constexpr int kBytes = FP8 ? L::kRaw : L::kStage;
-        const uint32_t ring = base + (FP8 ? (is_k ? L::kRawK : L::kRawV) : (is_k ? L::kK : L::kV));
-        uint64_t *full = FP8 ? raw_full[is_k ? 0 : 1] : kv_full, *empty = FP8 ? raw_empty[is_k ? 0 : 1] : kv_empty;
+        const uint32_t ring = base + (FP8 ? (x == 0 ? L::kRawK : L::kRawV) : (x == 0 ? L::kK : L::kV));
         int entry = e_first;
         for (int kb = 0; kb < nkb; ++kb) {
             const int st = kb % kRing;
@@ -271,36 +302,53 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
             else if (entry != kBehind)
                 set_device_error(a.err, PA_DEVERR_BAD_BLOCK);
             if (kb + 1 < nkb) entry = page_entry(kb + 1);
-            const bool freed = wait(empty[st], (kb / kRing & 1) ^ 1);
+            const uint32_t parity = (kb / kRing & 1) ^ 1;
+            bool freed;
+            uint64_t *full;  // of this lane's page
+            if constexpr (FP8) {
+                freed = wait(bar.raw_empty[kBoth ? 0 : x][st], parity);
+                if (kBoth) freed = wait(bar.raw_empty[1][st], parity) && freed;
+                full = &bar.raw_full[x][st];
+            } else {
+                freed = wait(bar.kv_empty[st], parity);
+                full = &bar.kv_full[st];
+            }
             if (lane == 0) {
                 if (!freed) fail();
-                mbar_arrive_expect_tx(smem_addr(&full[st]), kBytes);
+                mbar_arrive_expect_tx(smem_addr(full), kBoth && !FP8 ? 2 * kBytes : kBytes);
+                if (kBoth && FP8) mbar_arrive_expect_tx(smem_addr(&bar.raw_full[1][st]), kBytes);
             }
             __syncwarp();
-            if (lane < pages) {
+            if (lane < (kBoth ? 2 * pages : pages)) {
                 if constexpr (FP8) {
-                    tma_load_2d(ring + st * kBytes + lane * a.block_size * D, map, 0, y, smem_addr(&full[st]), policy);
+                    tma_load_2d(ring + st * kBytes + page * a.block_size * D, map, 0, y, smem_addr(full), policy);
                 } else {
                     for (int sl = 0; sl < L::kSlabs; ++sl)
-                        tma_load_2d(ring + st * kBytes + sl * kKVSlab + lane * a.block_size * 128, map, sl * 64, y,
-                                    smem_addr(&full[st]), policy);
+                        tma_load_2d(ring + st * kBytes + sl * kKVSlab + page * a.block_size * 128, map, sl * 64, y,
+                                    smem_addr(full), policy);
                 }
             }
         }
-        if (!FP8 && !is_k && partial) {
+        if (!FP8 && warp == kLoadV && partial) {
             const int kb = nkb - 1, st = kb % kStages;
-            if (!wait(kv_full[st], kb / kStages & 1) && lane == 0) fail();
+            if (!wait(bar.kv_full[st], kb / kStages & 1) && lane == 0) fail();
             for (int r = left - kb * kKeys + lane; r < kKeys; r += 32)
                 for (int sl = 0; sl < L::kSlabs; ++sl)
-                    for (int c = 0; c < 8; ++c) st_shared_zero16(ring + st * kBytes + sl * kKVSlab + r * 128 + c * 16);
+                    for (int c = 0; c < 8; ++c) st_shared_zero16(base + L::kV + st * L::kStage + sl * kKVSlab + r * 128 + c * 16);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&v_zeroed));
+            if (lane == 0) mbar_arrive(smem_addr(&bar.v_zeroed));
         }
         // whatever gave up, the CTA ends after its copies: those of the last blocks may be in flight
         if (lane == 0)
-            for (int kb = max(0, nkb - kRing); kb < nkb; ++kb)
-                mbar_wait_suspend(smem_addr(&full[kb % kRing]), kb / kRing & 1, kDrainNs);
+            for (int kb = max(0, nkb - kRing); kb < nkb; ++kb) {
+                if constexpr (FP8) {
+                    mbar_wait_suspend(smem_addr(&bar.raw_full[kBoth ? 0 : x][kb % kRing]), kb / kRing & 1, kDrainNs);
+                    if (kBoth) mbar_wait_suspend(smem_addr(&bar.raw_full[1][kb % kRing]), kb / kRing & 1, kDrainNs);
+                } else {
+                    mbar_wait_suspend(smem_addr(&bar.kv_full[kb % kRing]), kb / kRing & 1, kDrainNs);
+                }
+            }
     } else if (warp == kMma0 || warp == kMma1) {
         // ---------------- products ----------------
         const int T = warp == kMma0 ? 0 : 1;
@@ -310,13 +358,13 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
             const uint64_t q_desc = tc_smem_desc(base + T * L::kQTile, 16, 1024, 2);
             const uint64_t k_desc = tc_smem_desc(base + L::kK, 16, 1024, 2);
             const uint64_t v_desc = tc_smem_desc(base + L::kV, kKVSlab, 1024, 2);
-            const uint32_t tS = tmem + T * 256, tO = tS + kOCol;
+            const uint32_t tS = tmem + T * kTileCols, tO = tS + kOCol;
             // test hook: give up on a barrier that nothing completes
-            bool ok = !a.stall_first_wait || wait(stall_bar, 0);
-            ok = ok && (FP8 ? wait(q_conv[T], 0) : wait(q_full, 0));
+            bool ok = !a.stall_first_wait || wait(bar.stall, 0);
+            ok = ok && (FP8 ? wait(bar.q_conv[T], 0) : wait(bar.q_full, 0));
             auto qk = [&](int kb) {
                 const int st = kb % kStages;
-                ok = ok && wait(kv_full[st], kb / kStages & 1);
+                ok = ok && wait(bar.kv_full[st], kb / kStages & 1);
                 tc_fence_after();
                 if (ok) {
                     const uint64_t b0 = k_desc + ((st * L::kStage) >> 4);
@@ -326,14 +374,14 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                         tc_mma_bf16_elect(tS + (kb & 1) * kKeys, q_desc + (qoff >> 4), b0 + (koff >> 4), idesc_qk, kk > 0);
                     }
                 }
-                tc_commit_elect(smem_addr(&s_full[T][kb & 1]));
+                tc_commit_elect(smem_addr(&bar.s_full[T][kb & 1]));
             };
             qk(0);
             if (nkb > 1) qk(1);
             for (int kb = 0; kb < nkb; ++kb) {
                 const int st = kb % kStages;
-                ok = ok && wait(p_full[T][kb & 1], kb >> 1 & 1);
-                if (!FP8 && kb == nkb - 1 && partial) ok = ok && wait(v_zeroed, 0);
+                ok = ok && wait(bar.p_full[T][kb & 1], kb >> 1 & 1);
+                if (!FP8 && kb == nkb - 1 && partial) ok = ok && wait(bar.v_zeroed, 0);
                 tc_fence_after();
                 if (ok) {
                     const uint64_t b0 = v_desc + ((st * L::kStage) >> 4);
@@ -342,33 +390,33 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                     for (int kk = 0; kk < kKeys / 16; ++kk)
                         tc_mma_bf16_ts_elect(tO, tP + kk * 8, b0 + ((kk * 16 * 128) >> 4), idesc_pv, kb > 0 || kk > 0);
                 }
-                tc_commit_elect(smem_addr(&pv_done[T]));
-                tc_commit_elect(smem_addr(&kv_empty[st]));
+                tc_commit_elect(smem_addr(&bar.pv_done[T]));
+                tc_commit_elect(smem_addr(&bar.kv_empty[st]));
                 if (kb + 2 < nkb) qk(kb + 2);
             }
             if (!ok && lane == 0) fail();
             if (!a.group_start) dependent_release();
             // all is done before the tensor memory is given back
-            tc_commit_elect(smem_addr(&drain[T]));
-            mbar_wait_suspend(smem_addr(&drain[T]), 0, kDrainNs);
+            tc_commit_elect(smem_addr(&bar.drain[T]));
+            mbar_wait_suspend(smem_addr(&bar.drain[T]), 0, kDrainNs);
             __syncwarp();
         }
     } else if (warp >= kWiden) {
         if constexpr (FP8) {
             // ---------------- E4M3 to fp16, a row to a thread ----------------
             const int x = warp >= kWiden + 2;  // K or V
-            const int r = (warp & 1) * 32 + lane;
+            const int r = (warp - kWiden & 1) * 32 + lane;
             const uint32_t from = base + (x ? L::kRawV : L::kRawK) + r * D, to = base + (x ? L::kV : L::kK) + r * 128;
             bool ok = true;
             for (int kb = 0; kb < nkb; ++kb) {
                 const int rs = kb % kRawStages, st = kb % kStages;
-                ok = ok && wait(raw_full[x][rs], kb / kRawStages & 1);
+                ok = ok && wait(bar.raw_full[x][rs], kb / kRawStages & 1);
                 uint4 e[D / 16];
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)  // as the copy's swizzle laid it: 128-byte rows, or 64-byte ones
                     e[c] = lds128(from + rs * L::kRaw + ((D == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3)) << 4));
                 const bool valid = kb * kKeys + r < left;
-                ok = ok && wait(kv_empty[st], (kb / kStages & 1) ^ 1);
+                ok = ok && wait(bar.kv_empty[st], (kb / kStages & 1) ^ 1);
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
                     uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
@@ -386,26 +434,25 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_addr(&kv_full[st]));
+                    mbar_arrive(smem_addr(&bar.kv_full[st]));
                     // Not before the stores, which wait for the loads: an arrival does not,
                     // and the next page would land on what is still to be read.
-                    mbar_arrive(smem_addr(&raw_empty[x][rs]));
+                    mbar_arrive(smem_addr(&bar.raw_empty[x][rs]));
                 }
             }
             if (!ok && lane == 0) fail();
         }
     } else {
         // ---------------- softmax: a row to a thread ----------------
-        const int T = warp >> 2;
-        const int row = (warp & 3) * 32 + lane;
-        if (T < ntiles && (warp & 3) < warps_of(T)) {
+        const int T = TILES == 1 ? 0 : warp >> 2, quarter = TILES == 1 ? warp : warp & 3;
+        const int row = quarter * 32 + lane;
+        if (T < ntiles && quarter < warps_of(T)) {
             const int t = row / a.group, g = row - t * a.group;
-            const bool live = t < tokens_of(T);
-            const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + T * 256, tO = tS + kOCol;
+            const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + T * kTileCols, tO = tS + kOCol;
             float scale = a.softmax_log2;
             if constexpr (FP8) scale *= a.k_scales ? a.k_scales[h] : a.kv_scale;
             float m_ref = -INFINITY, l_run = 0.f;
-            bool ok = mbar_wait_suspend(smem_addr(&q_full), 0, limit);
+            bool ok = mbar_wait_suspend(smem_addr(&bar.q_full), 0, limit);
             if constexpr (FP8) {  // the row's query to fp16, in place
                 for (int sl = 0; sl < L::kSlabs; ++sl)
                     for (int c = 0; c < 8; ++c) {
@@ -419,40 +466,53 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                     }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&q_conv[T]));
+                if (lane == 0) mbar_arrive(smem_addr(&bar.q_conv[T]));
             }
             for (int kb = 0; kb < nkb; ++kb) {
                 const uint32_t tSb = tS + (kb & 1) * kKeys;  // S(kb), then P(kb)
-                ok = ok && mbar_wait_suspend(smem_addr(&s_full[T][kb & 1]), kb >> 1 & 1, limit);
+                ok = ok && mbar_wait_suspend(smem_addr(&bar.s_full[T][kb & 1]), kb >> 1 & 1, limit);
                 __syncwarp();
                 tc_fence_after();
-                float v[64];
-                {
-                    float lo[32], hi[32];
+                // scores 32 half .. of the row, masked behind the run's end
+                auto scores = [&](int half, float (&x)[32]) {
+                    tc_ld32(tSb + 32 * half, x);
+                    tc_wait_ld();
+                    if (partial && kb == nkb - 1) {
+                        const int n = left - kb * kKeys - 32 * half;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -INFINITY;
+                    }
+                };
+                // their largest: two chains of three-input maxima
+                auto largest = [](const float (&x)[32]) {
+                    float m[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        m[q] = fmax3(x[16 * q], x[16 * q + 1], x[16 * q + 2]);
+#pragma unroll
+                        for (int i = 3; i < 15; i += 2) m[q] = fmax3(m[q], x[16 * q + i], x[16 * q + i + 1]);
+                    }
+                    return fmax3(m[0], m[1], fmaxf(x[15], x[31]));
+                };
+                float lo[32], hi[32];
+                if constexpr (L::kReread) {
+                    scores(0, lo);
+                } else {  // both loads in flight
                     tc_ld32(tSb, lo);
                     tc_ld32(tSb + 32, hi);
                     tc_wait_ld();
+                    if (partial && kb == nkb - 1) {
+                        const int n = left - kb * kKeys;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        v[i] = lo[i];
-                        v[32 + i] = hi[i];
+                        for (int i = 0; i < 32; ++i) {
+                            lo[i] = i < n ? lo[i] : -INFINITY;
+                            hi[i] = 32 + i < n ? hi[i] : -INFINITY;
+                        }
                     }
                 }
-                if (partial && kb == nkb - 1) {
-                    const int n = left - kb * kKeys;
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) v[i] = i < n ? v[i] : -INFINITY;
-                }
-                // the largest of the block: four chains of three-input maxima
-                float mq[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    mq[q] = fmax3(v[16 * q], v[16 * q + 1], v[16 * q + 2]);
-#pragma unroll
-                    for (int i = 3; i < 15; i += 2) mq[q] = fmax3(mq[q], v[16 * q + i], v[16 * q + i + 1]);
-                    mq[q] = fmaxf(mq[q], v[16 * q + 15]);
-                }
-                const float top = fmaxf(fmax3(mq[0], mq[1], mq[2]), mq[3]) * scale;  // scale > 0
+                float top = largest(lo);
+                if constexpr (L::kReread) scores(1, hi);
+                top = fmaxf(top, largest(hi)) * scale;  // scale > 0
                 bool rescale = false;
                 float alpha = 1.f;
                 if (top - m_ref > kLazy) {  // the difference: a large score's sum would round
@@ -464,7 +524,7 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                 if (__any_sync(0xffffffffu, rescale)) {
                     // O holds PV(kb - 1) before it is scaled; PV(kb) waits for this
                     // block's P, so the barrier is at most a phase away
-                    ok = ok && mbar_wait_suspend(smem_addr(&pv_done[T]), (kb - 1) & 1, limit);
+                    ok = ok && mbar_wait_suspend(smem_addr(&bar.pv_done[T]), (kb - 1) & 1, limit);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll
@@ -480,36 +540,56 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                 }
                 // no finite score so far: any reference will do for the zeros
                 const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    ffma2(v[i], v[i + 1], scale, neg);
-                    v[i] = fast_exp2(v[i]);
-                    v[i + 1] = fast_exp2(v[i + 1]);
-                    fadd2(sa[(i >> 1) & 3], sb[(i >> 1) & 3], v[i], v[i + 1]);
-                }
-                fadd2(sa[0], sb[0], sa[1], sb[1]);
-                fadd2(sa[2], sb[2], sa[3], sb[3]);
-                fadd2(sa[0], sb[0], sa[2], sb[2]);
-                l_run += sa[0] + sb[0];
                 uint32_t pk[32];
+                auto powers = [&](int half, float (&x)[32]) {
+                    float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    pk[i] = FP8 ? pack2<true>(v[2 * i] * kRaise, v[2 * i + 1] * kRaise) : pack2<false>(v[2 * i], v[2 * i + 1]);
+                    for (int i = 0; i < 32; i += 2) {
+                        ffma2(x[i], x[i + 1], scale, neg);
+                        x[i] = fast_exp2(x[i]);
+                        x[i + 1] = fast_exp2(x[i + 1]);
+                        fadd2(sa[(i >> 1) & 1], sb[(i >> 1) & 1], x[i], x[i + 1]);
+                        pk[16 * half + i / 2] = FP8 ? pack2<true>(x[i] * kRaise, x[i + 1] * kRaise) : pack2<false>(x[i], x[i + 1]);
+                    }
+                    fadd2(sa[0], sb[0], sa[1], sb[1]);
+                    l_run += sa[0] + sb[0];
+                };
+                powers(1, hi);
+                if constexpr (L::kReread) scores(0, lo);
+                powers(0, lo);
                 tc_st32(tSb, pk);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&p_full[T][kb & 1]));
+                if (lane == 0) mbar_arrive(smem_addr(&bar.p_full[T][kb & 1]));
             }
-            ok = ok && mbar_wait_suspend(smem_addr(&drain[T]), 0, limit);
+            ok = ok && mbar_wait_suspend(smem_addr(&bar.drain[T]), 0, limit);
             __syncwarp();
             tc_fence_after();
             if (!ok) fail();
             if (FP8) l_run *= kRaise;
-            const int64_t token = static_cast<int64_t>(w.token0) + w.at + T * a.tile_tokens + t;
-            const int64_t at = token * a.num_q_heads + h * a.group + g;
-            const bool write = live && !failed_s;
+            const int64_t first_row = (static_cast<int64_t>(w.token0) + w.at + T * a.tile_tokens) * a.num_q_heads + h * a.group;
+            const int mine = t * a.num_q_heads + g;  // from there to this lane's row
+            // Rows leave through shared memory, each warp's 32 through the space of their
+            // queries: whole rows to a store instruction (a row to a lane would be
+            // 32 pieces of 16 bytes in as many lines).  The tile's products are done with it.
+            const uint32_t stage = base + T * L::kQTile + quarter * (L::kQTile * 32 / L::kTileRows);
+            constexpr int kRowBytes = 2 * D, kPieces = kRowBytes / 16, kAtOnce = 32 / kPieces;
+            const int rows_here = bar.failed ? 0 : min(32, tokens_of(T) * a.group - quarter * 32);
+            auto put = [&](int c, const uint4 &x) {  // 16-byte piece c of this lane's row
+                st_shared16(stage + lane * kRowBytes + (((c & ~7) | ((c ^ lane) & 7)) << 4), x);
+            };
+            auto flush = [&](char *to, int64_t row_stride) {  // the warp's rows, each to its place from `to` on
+                __syncwarp();
+#pragma unroll 4
+                for (int r0 = 0; r0 < rows_here; r0 += kAtOnce) {
+                    const int r = r0 + lane / kPieces, c = lane % kPieces;
+                    const int64_t row = __shfl_sync(0xffffffffu, mine, r);
+                    const uint4 x = lds128(stage + r * kRowBytes + (((c & ~7) | ((c ^ r) & 7)) << 4));
+                    if (r < rows_here) *reinterpret_cast<uint4 *>(to + row * row_stride + c * 16) = x;
+                }
+                __syncwarp();
+            };
             if (a.out) {
                 float v_scale = 1.f;
                 if constexpr (FP8) v_scale = a.v_scales ? a.v_scales[h] : a.kv_scale;
@@ -521,29 +601,32 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
                     tc_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
-                        if (write)
-                            *reinterpret_cast<uint4 *>(a.out + at * D + c + i) =
-                                make_uint4(pack2<false>(o[i] * inv, o[i + 1] * inv), pack2<false>(o[i + 2] * inv, o[i + 3] * inv),
-                                           pack2<false>(o[i + 4] * inv, o[i + 5] * inv), pack2<false>(o[i + 6] * inv, o[i + 7] * inv));
+                        put((c + i) / 8, make_uint4(pack2<false>(o[i] * inv, o[i + 1] * inv), pack2<false>(o[i + 2] * inv, o[i + 3] * inv),
+                                                    pack2<false>(o[i + 4] * inv, o[i + 5] * inv), pack2<false>(o[i + 6] * inv, o[i + 7] * inv)));
                 }
+                flush(reinterpret_cast<char *>(a.out + first_row * D), kRowBytes);
             } else {
-                const int64_t slot = w.part * static_cast<int64_t>(a.num_tokens) * a.num_q_heads + at;
-                if (write) a.part_ml[slot] = make_float2(m_ref, l_run);
+                const int64_t slot = w.part * static_cast<int64_t>(a.num_tokens) * a.num_q_heads + first_row;
+                if (lane < rows_here) a.part_ml[slot + mine] = make_float2(m_ref, l_run);
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tc_ld32(tO + c, o);
-                    tc_wait_ld();
+                for (int half = 0; half < 2; ++half) {  // 2 D bytes are half a row's
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        if (write)
-                            *reinterpret_cast<float4 *>(a.part_o + slot * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int c = 0; c < D / 2; c += 32) {
+                        float o[32];
+                        tc_ld32(tO + half * (D / 2) + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            put((c + i) / 4, make_uint4(__float_as_uint(o[i]), __float_as_uint(o[i + 1]), __float_as_uint(o[i + 2]),
+                                                        __float_as_uint(o[i + 3])));
+                    }
+                    flush(reinterpret_cast<char *>(a.part_o + slot * D + half * (D / 2)), 4 * D);
                 }
             }
         }
     }
     // the queries have landed before the CTA ends
-    if (tid == 0) mbar_wait_suspend(smem_addr(&q_full), 0, kDrainNs);
+    if (tid == 0) mbar_wait_suspend(smem_addr(&bar.q_full), 0, kDrainNs);
     tc_fence_before();
     __syncthreads();
     if (warp == kMma0) {
@@ -552,25 +635,31 @@ __global__ void __launch_bounds__(Layout<D, FP8>::kThreads, 1)
     }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int TILES>
 static pa_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, dim3 grid,
                         cudaStream_t stream) {
-    using L = Layout<D, FP8>;
+    using L = Layout<D, FP8, TILES>;
     static std::atomic<uint64_t> raised{0};
-    pa_status st = sparse::raise_smem_limit(reinterpret_cast<const void *>(rows_kernel<D, FP8>), L::kSmem, raised);
+    pa_status st = sparse::raise_smem_limit(reinterpret_cast<const void *>(rows_kernel<D, FP8, TILES>), L::kSmem, raised);
     if (st != PA_OK) return st;
-    return cuda_check(launch_dependent(rows_kernel<D, FP8>, grid, L::kThreads, L::kSmem, 0, stream, tq, tk, tv, a),
+    return cuda_check(launch_dependent(rows_kernel<D, FP8, TILES>, grid, L::kThreads, L::kSmem, 0, stream, tq, tk, tv, a),
                       "rows launch");
 }
 
-// Least of waves times (a CTA's blocks and its start and end): a block of two full
-// tiles takes about 1.1 us, a start and an end 4 us.
-int choose_parts(int64_t ctas, int blocks) {
+// Least of an estimate in microseconds: a CTA's start and end, its blocks, and what
+// writing and reading the parts takes.  Runs of one length (`even`) end in whole
+// waves; of others, of which 0.6 of the longest is taken for the average, the work
+// is shared out and the last CTA is half done when the others end.
+int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_rows, bool even, bool direct) {
+    const int64_t places = tiles == 1 ? 2 * kSms : kSms;
+    const double start = tiles == 1 ? 3.0 : 4.0, block = (tiles == 1 ? 1.4 : 1.0) * (head_dim == 64 ? 0.6 : 1.0);
     int best = 1;
     double least = INFINITY;
     for (int parts = 1; parts <= kMaxParts && (parts == 1 || (parts - 1) * kLeastBlocks < blocks); ++parts) {
-        const int64_t waves = (ctas * parts + kSms - 1) / kSms;
-        const double cost = waves * (4.0 + 1.1 * blocks_per_part(blocks, parts));
+        const double one = start + block * blocks_per_part(blocks, parts), n = static_cast<double>(ctas) * parts;
+        double cost = even ? std::ceil(n / places) * one
+                           : std::max(one, (n * start + ctas * block * blocks * 0.6) / places + one / 2);
+        if (parts > 1 || !direct) cost += parts * (static_cast<double>(num_rows) * head_dim * 8) / 5e6;
         if (cost < least) {
             least = cost;
             best = parts;
@@ -580,8 +669,8 @@ int choose_parts(int64_t ctas, int blocks) {
 }
 
 pa_status launch_rows(const void *q, const void *k_cache, const void *v_cache, int head_dim, bool fp8, Args &a,
-                      int64_t pairs, int seqs, cudaStream_t stream) {
-    a.tile_tokens = kRows / a.group;
+                      int tiles, int64_t ctas, int seqs, cudaStream_t stream) {
+    a.tile_tokens = tile_rows(tiles) / a.group;
     a.wait_limit_ns = wait_limit_ns();
     a.stall_first_wait = stall_first_wait();
     const int64_t pool_rows = static_cast<int64_t>(a.num_blocks) * a.num_kv_heads * a.block_size;
@@ -590,11 +679,18 @@ pa_status launch_rows(const void *q, const void *k_cache, const void *v_cache, i
     if (st == PA_OK) st = make_map(&tk, k_cache, fp8, head_dim, pool_rows, a.block_size);
     if (st == PA_OK) st = make_map(&tv, v_cache, fp8, head_dim, pool_rows, a.block_size);
     if (st != PA_OK) return st;
-    if (pairs * a.parts > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many rows for one launch");
-    const dim3 grid(static_cast<unsigned>(pairs * a.parts), a.num_kv_heads, seqs);
-    if (head_dim == 128)
-        return fp8 ? launch<128, true>(tq, tk, tv, a, grid, stream) : launch<128, false>(tq, tk, tv, a, grid, stream);
-    return fp8 ? launch<64, true>(tq, tk, tv, a, grid, stream) : launch<64, false>(tq, tk, tv, a, grid, stream);
+    if (ctas * a.parts > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many rows for one launch");
+    const dim3 grid(static_cast<unsigned>(ctas * a.parts), a.num_kv_heads, seqs);
+    auto shape = [&](auto d, auto t) {
+        return fp8 ? launch<d.value, true, t.value>(tq, tk, tv, a, grid, stream)
+                   : launch<d.value, false, t.value>(tq, tk, tv, a, grid, stream);
+    };
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    if (head_dim == 128) return tiles == 1 ? shape(I128{}, I1{}) : shape(I128{}, I2{});
+    return tiles == 1 ? shape(I64{}, I1{}) : shape(I64{}, I2{});
 }
 
 }  // namespace rows

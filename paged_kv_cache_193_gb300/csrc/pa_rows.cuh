@@ -3,7 +3,7 @@
 // batch's decode have in common.  Here the parts that both sides of a launch
 // agree on; the kernel is in pa_rows.cu.
 //
-// Rows are (token, query head of one KV head) pairs, 128 to a tile; a run of
+// Rows are (token, query head of one KV head) pairs, up to 128 to a tile; a run of
 // keys may be cut into parts, each with its own
 //   m = max_t s_t (or what the kernel takes for it), l = sum_t 2^(s_t - m),
 //   o = sum_t 2^(s_t - m) V[t],   s_t = softmax_scale * log2(e) * q . K[t],
@@ -18,12 +18,14 @@ namespace pa {
 namespace rows {
 
 constexpr int kSms = 152;
-constexpr int kRows = 128;     // query rows of a tile (lanes of tensor memory)
-constexpr int kTiles = 2;      // tiles of a CTA: both read every stage of keys
+constexpr int kRows = 128;     // rows of a product (lanes of tensor memory)
 constexpr int kKeys = 64;      // keys of a block
 constexpr int kMaxParts = 32;  // of a run of keys
 // A part has at least so many blocks: its start and end cost about as much.
 constexpr int kLeastBlocks = 4;
+
+// Query rows of a tile, for CTAs of one or of two.
+__host__ __device__ constexpr int tile_rows(int tiles) { return tiles == 1 ? kRows / 2 : kRows; }
 
 // Blocks of each part of a run of `blocks`; parts from ceil(blocks / that) on
 // have none, and nothing is written for them.
@@ -48,7 +50,7 @@ struct Args {
     int num_q_heads, num_kv_heads, group;
     int num_tokens, num_seqs;
     int max_query_len;   // cross attention: rows of a sequence, at most
-    int tile_tokens;     // 128 / group
+    int tile_tokens;     // of a tile's rows
     float softmax_log2;  // softmax_scale * log2(e)
     float kv_scale;      // E4M3: one scale, or one of K and V for each head
     const float *k_scales, *v_scales;
@@ -67,14 +69,16 @@ struct Args {
     unsigned int *err;
 };
 
-// Tile pairs of `tokens` tokens of a KV head's group.
-inline int64_t tile_pairs(int64_t tokens, int group) {
-    const int each = kTiles * (kRows / group);
+// CTAs of `tiles` tiles (1 or 2, which read the same stages) for `tokens` tokens of
+// a KV head's group.
+inline int64_t tile_ctas(int64_t tokens, int group, int tiles) {
+    const int each = tiles * (tile_rows(tiles) / group);
     return (tokens + each - 1) / each;
 }
 
-// Into how many parts to cut runs of up to `blocks` blocks for `ctas` CTAs to a part.
-int choose_parts(int64_t ctas, int blocks);
+// Into how many parts to cut runs of up to `blocks` blocks for `ctas` CTAs to a part;
+// `even`: all runs are as long as that; `direct`: one part needs no joining.
+int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_rows, bool even, bool direct);
 
 // Rows of sequence s: false for what is no range of the tokens, or longer than it may be.
 __device__ __forceinline__ bool query_range(const Args &a, int s, int &first, int &count) {
@@ -94,10 +98,10 @@ pa_status check_row_pointers(const void *q, const void *k_cache, const void *v_c
 pa_status check_workspace(const void *workspace, size_t got, size_t need, const void *q, const void *out, size_t row_bytes);
 
 // Attention of `a`'s rows (q bf16 [num_tokens][num_q_heads][head_dim]) over the grid's
-// (tile pair, part), KV head, and sequence (1 for a shared prefix: the pairs of all groups lie
+// (tile or two, part), KV head, and sequence (1 for a shared prefix: the tiles of all groups lie
 // one after the other).
 pa_status launch_rows(const void *q, const void *k_cache, const void *v_cache, int head_dim, bool fp8, Args &a,
-                      int64_t pairs, int seqs, cudaStream_t stream);
+                      int tiles, int64_t ctas, int seqs, cudaStream_t stream);
 
 }  // namespace rows
 }  // namespace pa

@@ -18,12 +18,66 @@
 namespace pa {
 namespace rows {
 
-static int prefix_parts(int64_t num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int max_prefix_blocks, int block_size) {
+// How a prefix's kernel is launched: by a call's sizes alone, which the workspace's
+// size goes by too.
+struct Plan {
+    bool shared;   // or each sequence by itself
+    int tiles;     // to a CTA: one where a group mostly has no more
+    int64_t ctas;  // to a part and KV head: every group may have one that is not full
+    int parts;
+};
+
+// A prefix's kernel costs some 6 us beside its work; up to 64 MB of prefixes, each
+// counted for every sequence, are read faster than that, from the second-level cache
+// but for the first time (8 KV heads of 128 dims, microseconds with and without it:
+// 4 sequences of 1,024 tokens 10.0 and 7.4, 4 of 4,096 11.7 and 12.4, 32 of 1,024 in
+// E4M3 11.6 and 12.7, 16 of 1,024 in bf16 10.5 and 10.3).
+constexpr int64_t kShareBytes = 64000000;
+static std::atomic<int64_t> g_share_bytes{kShareBytes};  // pa_test_set_share_bytes
+
+static Plan plan(int64_t num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim, int max_prefix_blocks,
+                 int block_size, bool fp8) {
+    const double all = static_cast<double>(num_seqs) * max_prefix_blocks * block_size * num_kv_heads * head_dim * (fp8 ? 2 : 4);
+    if (num_groups == 0 || max_prefix_blocks == 0 || all <= static_cast<double>(g_share_bytes.load(std::memory_order_relaxed))) return {false, 0, 0, 0};
     const int group = num_q_heads / num_kv_heads;
-    // every group may have a pair that is not full
-    const int64_t pairs = tile_pairs(num_seqs, group) + num_groups - 1;
-    return choose_parts(std::min(pairs, num_seqs) * num_kv_heads,
-                        static_cast<int>((static_cast<int64_t>(max_prefix_blocks) * block_size + kKeys - 1) / kKeys));
+    const int tiles = num_seqs <= static_cast<int64_t>(tile_rows(1) / group) * num_groups ? 1 : 2;
+    const int64_t ctas = std::min(tile_ctas(num_seqs, group, tiles) + num_groups - 1, num_seqs);
+    const int blocks = static_cast<int>((static_cast<int64_t>(max_prefix_blocks) * block_size + kKeys - 1) / kKeys);
+    return {true, tiles, ctas, choose_parts(ctas * num_kv_heads, blocks, tiles, head_dim, num_seqs * num_q_heads, num_groups == 1, false)};
+}
+
+// How the rest is launched: at most `pages` pages behind the prefix of each of
+// `num_seqs` sequences.
+struct Suffix {
+    bool heads;          // a warp to a KV head, not a CTA
+    bool longest_first;
+    int splits;          // CTAs to a sequence and KV head
+};
+
+// A CTA for every KV head costs about 3.6 us, however little it reads, so few pages
+// are better read by a warp to a head (1,024 rows of up to 100 tokens: 16.1 us, 22.1
+// with a CTA to each; of up to 500 43 and 29), where all CTAs are on the SMs at once
+// also some more.  With as many rows as places or a few more, the longest go first
+// (512 rows of up to 1,000 tokens, E4M3: 19.5 us, 28.9 in their order); who is
+// longest is known for one group, whose prefix is the same for all.  Long lists are
+// shared out while 512 CTAs hold them (128 rows of up to 2,000 tokens in bf16: 36.7 us
+// with one, 24.0 with two, 18.7 with four; of up to 1,000 in E4M3 11.9, 13.5, 14.4),
+// and to twice that when very long (512 rows of up to 4,000, longest first: 97 with
+// one, 85 with two).
+static Suffix suffix_launch(int64_t num_seqs, int num_groups, int num_kv_heads, bool shared, int pages, int head_dim, int block_size,
+                            bool fp8, int group) {
+    const int64_t rows = num_seqs * num_kv_heads;
+    if (!shared)
+        return {false, false, sparse::splits_of_four_warps(rows, pages, sparse::resident_ctas(head_dim, block_size, fp8, group))};
+    const int at_once = fp8 && block_size == 16 ? 2 : 1;  // pages of a warp's step
+    const int steps = (pages + at_once - 1) / at_once;    // of one warp
+    if ((rows >= 512 && pages <= 8) || (rows >= 2048 && steps <= 16)) return {true, false, 1};
+    Suffix l{false, num_groups == 1 && num_seqs > 1 && num_seqs <= sparse::kMaxSorted && pages >= 16, 1};
+    if (steps >= 48)
+        for (int s : {2, 4, 8})
+            if (rows * s <= 512) l.splits = s;
+    if (l.splits == 1 && l.longest_first && rows <= 512 && steps >= 96) l.splits = 2;
+    return l;
 }
 
 pa_status check_rows(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
@@ -72,14 +126,21 @@ using namespace pa;
 
 extern "C" {
 
+pa_status pa_test_set_share_bytes(int64_t bytes) {
+    clear_error();
+    rows::g_share_bytes.store(bytes < 0 ? rows::kShareBytes : bytes, std::memory_order_relaxed);
+    return PA_OK;
+}
+
 size_t pa_shared_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
-                                       int block_size, int max_prefix_blocks) {
+                                       int block_size, int max_prefix_blocks, pa_kv_dtype kv_dtype) {
     if (num_seqs <= 0 || num_groups <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
         num_q_heads / num_kv_heads > 16 || head_dim <= 0 || block_size <= 0 || max_prefix_blocks <= 0 ||
         static_cast<int64_t>(max_prefix_blocks) * block_size > 0x7fffffffLL)
         return 0;
-    return rows::workspace_bytes(rows::prefix_parts(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_blocks, block_size),
-                                 static_cast<int64_t>(num_seqs) * num_q_heads, head_dim);
+    const rows::Plan p = rows::plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_prefix_blocks, block_size,
+                                    kv_dtype == PA_KV_FP8_E4M3);
+    return rows::workspace_bytes(p.parts, static_cast<int64_t>(num_seqs) * num_q_heads, head_dim);
 }
 
 pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
@@ -100,24 +161,23 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     if (num_groups > num_seqs)
         return fail(PA_ERR_INVALID_ARG, "%d groups of %d sequences", num_groups, num_seqs);
     if (num_seqs == 0) return PA_OK;
-    const bool shared = num_groups > 0 && max_prefix_blocks > 0;
     st = rows::check_row_pointers(q, k_cache, v_cache, block_tables, context_lens, out, num_seqs, num_q_heads, head_dim);
     if (st != PA_OK) return st;
     const int64_t num_rows = static_cast<int64_t>(num_seqs) * num_q_heads;
-    int parts = 0;
+    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
+    const rows::Plan p = rows::plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_prefix_blocks, block_size, fp8);
+    const bool shared = p.shared;
     if (shared) {
         if (!group_start || !prefix_blocks) return fail(PA_ERR_INVALID_ARG, "null pointer");
-        parts = rows::prefix_parts(num_seqs, num_groups, num_q_heads, num_kv_heads, max_prefix_blocks, block_size);
-        st = rows::check_workspace(workspace, workspace_bytes, rows::workspace_bytes(parts, num_rows, head_dim), q, out,
+        st = rows::check_workspace(workspace, workspace_bytes, rows::workspace_bytes(p.parts, num_rows, head_dim), q, out,
                                    static_cast<size_t>(num_rows) * head_dim * 2);
         if (st != PA_OK) return st;
     }
     unsigned int *err = device_error_word();
     if (!err) return fail(PA_ERR_CUDA, "cannot resolve the device error word");
-    const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
     const int group = num_q_heads / num_kv_heads;
     float *part_o = static_cast<float *>(workspace);
-    float2 *part_ml = reinterpret_cast<float2 *>(part_o + parts * num_rows * head_dim);
+    float2 *part_ml = reinterpret_cast<float2 *>(part_o + p.parts * num_rows * head_dim);
 
     if (shared) {
         rows::Args a = {};
@@ -134,7 +194,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
         a.kv_scale = kv_scale;
         a.k_scales = k_scales;
         a.v_scales = v_scales;
-        a.parts = parts;
+        a.parts = p.parts;
         a.part_o = part_o;
         a.part_ml = part_ml;
         a.group_start = group_start;
@@ -142,8 +202,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
         a.num_groups = num_groups;
         a.max_prefix_blocks = max_prefix_blocks;
         a.err = err;
-        const int64_t pairs = std::min<int64_t>(rows::tile_pairs(num_seqs, group) + num_groups - 1, num_seqs);
-        st = rows::launch_rows(q, k_cache, v_cache, head_dim, fp8, a, pairs, 1, stream);
+        st = rows::launch_rows(q, k_cache, v_cache, head_dim, fp8, a, p.tiles, p.ctas, 1, stream);
         if (st != PA_OK) return st;
     }
 
@@ -169,11 +228,14 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     b.err = err;
     b.wait_limit_ns = wait_limit_ns();
     b.stall_first_wait = stall_first_wait();
-    b.prefix = {group_start, prefix_blocks, num_groups, max_prefix_blocks, parts, part_o, part_ml, num_rows};
-    const int pages = max_blocks_per_seq - max_prefix_blocks;  // that the longest has behind the longest prefix
-    const int splits = sparse::splits_of_four_warps(static_cast<int64_t>(num_seqs) * num_kv_heads, pages,
-                                                    sparse::resident_ctas(head_dim, block_size, fp8, group));
-    return sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, splits, 4, stream);
+    b.prefix = {group_start, prefix_blocks, num_groups, max_prefix_blocks, p.parts, part_o, part_ml, num_rows};
+    // behind the prefix: of several groups, the shortest may be none
+    const int pages = max_blocks_per_seq - (shared && num_groups == 1 ? max_prefix_blocks : 0);
+    const rows::Suffix suffix = rows::suffix_launch(num_seqs, num_groups, num_kv_heads, shared, pages, head_dim, block_size, fp8, group);
+    b.longest_first = suffix.longest_first;
+    if (suffix.heads)
+        return sparse::launch_any<sparse::kSuffixHeads>(head_dim, block_size, fp8, tk, tv, b, num_seqs, 1, 4, stream, group);
+    return sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, suffix.splits, 4, stream, group);
 }
 
 }  // extern "C"

@@ -63,10 +63,15 @@ struct Args {
     SelectArgs select;  // of the kernel that chooses the pages itself
     int longest_first;  // its clusters take the rows by length
     Prefix prefix;      // of the kernel that attends behind a prefix
+    // of several tokens' rows (kRows): sequence s's are query_start[s] .. query_start[s + 1] - 1
+    const int32_t *query_start;
+    int num_tokens, max_query_len;
 };
 
-// A list of pages, pages that the kernel chooses, or the pages behind a prefix.
-enum Mode { kList, kChoose, kSuffix };
+// A list of pages, pages that the kernel chooses, the pages behind a prefix
+// (kSuffix; kSuffixHeads: a warp to a KV head), or all pages, for up to 16 rows
+// (tokens times query heads of a KV head).
+enum Mode { kList, kChoose, kSuffix, kSuffixHeads, kRows };
 
 pa_status launch_chosen(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
                         int num_rows, int splits, int warps, cudaStream_t stream);
@@ -136,7 +141,7 @@ constexpr int kMaxSorted = 128;
 __device__ __forceinline__ int longest_row(const int32_t *lens, int n, int z, void *room) {
     int32_t *len = static_cast<int32_t *>(room);
     const int i = threadIdx.x;
-    const int32_t mine = i < n ? lens[i] : 0;
+    const int32_t mine = i < n ? __ldcg(lens + i) : 0;
     if (i < n) len[i] = mine;
     __syncthreads();
     int before = 0;
@@ -154,20 +159,25 @@ __device__ __forceinline__ int longest_row(const int32_t *lens, int n, int z, vo
 __device__ __forceinline__ int shared_pages(const Prefix &p, int s, int n, int block_size) {
     if (p.parts == 0 || p.num_groups == 0) return 0;
     const int lane = threadIdx.x & 31;
-    // the last group that starts at s or before, among 32 and then 32 of those between
     int lo = 0, size = p.num_groups;
-    for (;;) {
+    // the last group that starts at s or before, among 32 and then 32 of those between
+    while (size > 32) {
         const int step = (size + 31) / 32, at = lane * step;
         const int v = at < size ? __ldcg(p.group_start + lo + at) : 0x7fffffff;
         const int count = __popc(__ballot_sync(0xffffffffu, v <= s));
         if (count == 0) return 0;
         const int skip = min((count - 1) * step, size - 1);
         lo += skip;
-        if (step == 1) break;
         size = min(step, size - skip);
     }
-    const int end = __ldcg(p.group_start + lo + 1), pages = min(__ldcg(p.prefix_blocks + lo), p.max_blocks);
-    return s < end && pages > 0 && n / block_size >= pages ? pages : 0;
+    // at last all that may be wanted is on its way at once
+    const bool has = lane < size;
+    const int begin = has ? __ldcg(p.group_start + lo + lane) : 0x7fffffff, end = has ? __ldcg(p.group_start + lo + lane + 1) : 0;
+    const int blocks = has ? min(__ldcg(p.prefix_blocks + lo + lane), p.max_blocks) : 0;
+    const int count = __popc(__ballot_sync(0xffffffffu, begin <= s));
+    if (count == 0) return 0;
+    const int pages = __shfl_sync(0xffffffffu, blocks, count - 1);
+    return s < __shfl_sync(0xffffffffu, end, count - 1) && pages > 0 && n / block_size >= pages ? pages : 0;
 }
 
 // kChoose: the cluster first chooses the row's pages, in the ring's memory.
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
                   const Args a) {
     using C = Shape<D, BS, FP8, NT, NW, SPW>;
     constexpr int PPI = C::PPI, MI = C::MI;
-    constexpr bool CHOOSE = MODE == kChoose, SUFFIX = MODE == kSuffix;
+    constexpr bool CHOOSE = MODE == kChoose, HEADS = MODE == kSuffixHeads, SUFFIX = MODE == kSuffix || HEADS, ROWS = MODE == kRows;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[C::NSTAGE];
     __shared__ __align__(8) uint64_t stall_bar;  // never completed (wait-limit test hook)
@@ -190,7 +200,8 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, c = lane & 3;
-    const int h = blockIdx.y;
+    const bool idle = HEADS && static_cast<int>(blockIdx.y) * NW + warp >= a.num_kv_heads;  // a warp without a head
+    const int h = !HEADS ? blockIdx.y : idle ? 0 : blockIdx.y * NW + warp;
     int s = blockIdx.z;
 
     if (tid == 0) {
@@ -202,7 +213,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         prefetch_tensormap(&tmV);
     }
     if (!SUFFIX || a.prefix.parts == 0) dependent_wait();
-    if constexpr (CHOOSE)
+    if constexpr (CHOOSE || SUFFIX)
         if (a.longest_first) s = longest_row(a.context_lens, gridDim.z, s, join);
 
     // plain loads; past the first-level cache where the kernel in front still runs
@@ -220,15 +231,35 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         fence_proxy_async_smem();  // this memory is next written by page copies
     }
 
+    // Rows of queries, and where each begins: the group's heads, or those of several tokens.
+    int num_live = a.group, token0 = s;
+    if constexpr (ROWS) {
+        const int end = a.query_start[s + 1];
+        token0 = a.query_start[s];
+        if (token0 < 0 || end < token0 || end > a.num_tokens || end - token0 > a.max_query_len) {
+            if (tid == 0 && rank == 0) set_device_error(a.err, PA_DEVERR_BAD_CONTEXT);
+            num_live = 0;
+        } else {
+            num_live = (end - token0) * a.group;
+        }
+    }
+    auto row_at = [&](int g) -> int64_t {
+        if constexpr (ROWS) {
+            const int t = g / a.group;
+            return ((static_cast<int64_t>(token0) + t) * a.num_q_heads + h * a.group + (g - t * a.group)) * D;
+        } else {
+            return (static_cast<int64_t>(token0) * a.num_q_heads + h * a.group + g) * D;
+        }
+    };
+
     // query fragments (B operand of S^T = K Q^T), resident in registers
     uint32_t qf[C::KSTEPS][NT][2];
     {
-        const __nv_bfloat16 *qh = a.q + (static_cast<int64_t>(s) * a.num_q_heads + h * a.group) * D;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int g = nt * 8 + r;
-            const bool live = g < a.group;
-            const __nv_bfloat16 *qg = qh + g * D;
+            const bool live = g < num_live;
+            const __nv_bfloat16 *qg = a.q + row_at(live ? g : 0);
 #pragma unroll
             for (int kk = 0; kk < C::KSTEPS; ++kk) {
                 if constexpr (!FP8) {
@@ -257,19 +288,21 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     int skip = 0;  // pages in front of the list's first
     if constexpr (SUFFIX) {
         skip = shared_pages(a.prefix, s, n, BS);
-        chosen = Chosen{nb - skip, nullptr};
+        chosen = Chosen{idle ? 0 : nb - skip, nullptr};
+    } else if constexpr (ROWS) {
+        chosen = Chosen{num_live ? nb : 0, nullptr};
     } else if constexpr (!CHOOSE) {
         const int64_t row = static_cast<int64_t>(s) * a.num_kv_heads + h;
         chosen = Chosen{min(max(a.counts[row], 0), a.top_k), a.selected + row * a.top_k};
     }
 
     // ---- this warp's entries of the list ----------------------------------------
-    const int step = NW * static_cast<int>(ranks);
-    const int first = static_cast<int>(rank) * NW + warp;
+    const int step = HEADS ? 1 : NW * static_cast<int>(ranks);
+    const int first = HEADS ? 0 : static_cast<int>(rank) * NW + warp;
     // logical page of the warp's k-th entry
     auto entry = [&](int k) -> int {
         const int i = first + k * step;
-        return SUFFIX ? skip + i : chosen.list ? chosen.list[i] : i;
+        return SUFFIX ? skip + i : ROWS ? i : chosen.list ? chosen.list[i] : i;
     };
     const int32_t *table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
     const int my_pages = chosen.count > first ? (chosen.count - first + step - 1) / step : 0;
@@ -599,6 +632,78 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             l_run[nt][j] = l;
         }
+    if constexpr (HEADS) {
+        // A warp has a head to itself: its part joins the prefix's and leaves, through its
+        // own share of the ring.
+        static_assert(C::NP * (C::OSTR + rows::kMaxParts) * 4 <= SPW * C::STAGE, "a warp's output in its share of the ring");
+        if (a.prefix.parts) dependent_wait();
+        if (idle) return;
+        __syncwarp();  // the ring's last stage has been read by all lanes
+        float *osm = join + warp * (SPW * C::STAGE / 4);
+#pragma unroll
+        for (int dt = 0; dt < C::DT; ++dt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    osm[(nt * 8 + 2 * c + (e & 1)) * C::OSTR + dt * 16 + r + (e >> 1) * 8] = o[dt][nt][e];
+        __syncwarp();
+        // lane g (and g + 16 or so) takes query head g's maximum and sum: those of row g are
+        // in lane g / 2 (with r = 0) of column pair g % 2
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float m = __shfl_sync(0xffffffffu, m_ref[nt][j], (lane & 7) >> 1), l = __shfl_sync(0xffffffffu, l_run[nt][j], (lane & 7) >> 1);
+                if (((lane >> 3) & (NT - 1)) == nt && (lane & 1) == j) {
+                    top = m;
+                    sum = l;
+                }
+            }
+        const int g = lane & (C::NP - 1);
+        const int parts = skip ? rows::live_parts((skip * BS + rows::kKeys - 1) / rows::kKeys, a.prefix.parts) : 0;
+        const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + h * a.group;
+        const float2 *ml = a.prefix.ml + row + min(g, a.group - 1);
+        float *pw = osm + C::NP * C::OSTR;  // [parts][NP] the prefix's weights
+        auto weight = [](float m, float l, float best) { return m == -INFINITY ? (l == 0.f ? 0.f : l) : fast_exp2(m - best); };
+        float all = top;
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) all = fmaxf(all, ml[p * a.prefix.rows].x);
+        float mine = weight(top, sum, all);
+        float total = mine == 0.f ? 0.f : mine * sum;
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) {
+            const float2 x = ml[p * a.prefix.rows];
+            const float f = weight(x.x, x.y, all);
+            if (f != 0.f) total += f * x.y;
+            if (lane < C::NP) pw[p * C::NP + g] = f;
+        }
+        const float inv = total != 0.f ? v_scale / total : 0.f;
+        __syncwarp();
+        // four head dims of a query head at a time; whole passes of the warp, for the shuffles
+        const int quads = a.group * (D / 4);
+        for (int i0 = 0; i0 < quads; i0 += 32) {
+            const int i = min(i0 + lane, quads - 1), gi = i / (D / 4);
+            const float f0 = __shfl_sync(0xffffffffu, mine, gi), scale = __shfl_sync(0xffffffffu, inv, gi);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto add = [&](float f, const float4 &x) {
+                if (f != 0.f) {  // an empty part's accumulator may be anything
+                    v.x += f * x.x;
+                    v.y += f * x.y;
+                    v.z += f * x.z;
+                    v.w += f * x.w;
+                }
+            };
+            add(f0, *reinterpret_cast<const float4 *>(osm + gi * C::OSTR + i % (D / 4) * 4));
+            const float *part = a.prefix.o + row * D + 4 * i;
+#pragma unroll 4
+            for (int p = 0; p < parts; ++p) add(pw[p * C::NP + gi], *reinterpret_cast<const float4 *>(part + p * a.prefix.rows * D));
+            if (i0 + lane < quads)
+                *reinterpret_cast<uint2 *>(a.out + row * D + 4 * i) = make_uint2(pack2<false>(v.x * scale, v.y * scale), pack2<false>(v.z * scale, v.w * scale));
+        }
+        return;
+    }
     __syncthreads();  // every warp is done with the page ring
     float *osm = join;                        // [NW][NP][OSTR]
     float *msm = osm + NW * C::NP * C::OSTR;  // [NW][NP] reference
@@ -641,15 +746,17 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         if (a.prefix.parts) dependent_wait();
         if (skip) parts = rows::live_parts((skip * BS + rows::kKeys - 1) / rows::kKeys, a.prefix.parts);
     }
-    const int64_t part0 = static_cast<int64_t>(s) * a.num_q_heads + h * a.group;
+    const int64_t part0 = static_cast<int64_t>(s) * a.num_q_heads + h * a.group, part_stride = a.prefix.rows;
     auto with_prefix = [&](float top, float &sum) -> float {  // by thread g < group
         const float2 *ml = a.prefix.ml + part0 + tid;
         float all = top;
-        for (int p = 0; p < parts; ++p) all = fmaxf(all, ml[p * a.prefix.rows].x);
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) all = fmaxf(all, ml[p * part_stride].x);
         const float mine = weight(top, sum, all);
         sum = mine == 0.f ? 0.f : sum * mine;
+#pragma unroll 4
         for (int p = 0; p < parts; ++p) {
-            const float2 x = ml[p * a.prefix.rows];
+            const float2 x = ml[p * part_stride];
             const float f = weight(x.x, x.y, all);
             if (f != 0.f) sum += f * x.y;
             pw[p][tid] = f;
@@ -659,9 +766,10 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     auto add_prefix = [&](int i, float4 &v) {  // four head dims of a head
         const int g = i / (D / 4);
         const float *o = a.prefix.o + part0 * D + 4 * i;
+#pragma unroll 4
         for (int p = 0; p < parts; ++p) {
             const float f = pw[p][g];
-            const float4 x = *reinterpret_cast<const float4 *>(o + p * a.prefix.rows * D);
+            const float4 x = *reinterpret_cast<const float4 *>(o + p * part_stride * D);
             if (f != 0.f) {
                 v.x += f * x.x;
                 v.y += f * x.y;
@@ -691,11 +799,10 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     }
     __syncthreads();
     // four head dims of a head at a time
-    const int64_t out0 = (static_cast<int64_t>(s) * a.num_q_heads + h * a.group) * D;
-    const int quads = a.group * (D / 4);
+    const int quads = num_live * (D / 4);
     auto put = [&](int i, const float4 &v, float f) {
         const uint2 w = make_uint2(pack2<false>(v.x * f, v.y * f), pack2<false>(v.z * f, v.w * f));
-        *reinterpret_cast<uint2 *>(a.out + out0 + 4 * i) = w;
+        *reinterpret_cast<uint2 *>(a.out + row_at(i / (D / 4)) + i % (D / 4) * 4) = w;
     };
     for (int i = tid; i < quads; i += NW * 32) {
         const int g = i / (D / 4), d = i % (D / 4) * 4;
@@ -828,26 +935,28 @@ static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, con
     static std::atomic<uint64_t> raised{0};
     pa_status st = raise_smem_limit(reinterpret_cast<const void *>(kern), kMostSmem, raised);
     if (st != PA_OK) return st;
-    return cuda_check(launch_dependent(kern, dim3(splits, a.num_kv_heads, num_rows), NW * 32, smem, splits, stream, tk, tv, a),
+    const int heads = MODE == kSuffixHeads ? (a.num_kv_heads + NW - 1) / NW : a.num_kv_heads;
+    return cuda_check(launch_dependent(kern, dim3(splits, heads, num_rows), NW * 32, smem, splits, stream, tk, tv, a),
                       "sparse decode launch");
 }
 
 // Eight warps to a CTA: only for the kernel that chooses, up to 8 query heads.
 template <int D, int BS, bool FP8, int MODE>
 static pa_status launch_group(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int num_rows, int splits,
-                              int warps, cudaStream_t stream) {
-    if (a.group > 8) return launch_attend<D, BS, FP8, 2, 4, MODE>(tk, tv, a, num_rows, splits, stream);
+                              int warps, cudaStream_t stream, int live) {
+    if (live > 8) return launch_attend<D, BS, FP8, 2, 4, MODE>(tk, tv, a, num_rows, splits, stream);
     if constexpr (MODE == kChoose)
         if (warps == 8) return launch_attend<D, BS, FP8, 1, 8, MODE>(tk, tv, a, num_rows, splits, stream);
     return launch_attend<D, BS, FP8, 1, 4, MODE>(tk, tv, a, num_rows, splits, stream);
 }
 
+// `live`: rows of queries to a cluster (the group, but for kRows).
 template <int MODE>
 static pa_status launch_any(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv,
-                            const Args &a, int num_rows, int splits, int warps, cudaStream_t stream) {
+                            const Args &a, int num_rows, int splits, int warps, cudaStream_t stream, int live) {
     auto shape = [&](auto d, auto bs) {
-        return fp8 ? launch_group<d.value, bs.value, true, MODE>(tk, tv, a, num_rows, splits, warps, stream)
-                   : launch_group<d.value, bs.value, false, MODE>(tk, tv, a, num_rows, splits, warps, stream);
+        return fp8 ? launch_group<d.value, bs.value, true, MODE>(tk, tv, a, num_rows, splits, warps, stream, live)
+                   : launch_group<d.value, bs.value, false, MODE>(tk, tv, a, num_rows, splits, warps, stream, live);
     };
     using I64 = std::integral_constant<int, 64>;
     using I128 = std::integral_constant<int, 128>;

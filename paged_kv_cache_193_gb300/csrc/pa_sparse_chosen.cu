@@ -7,7 +7,7 @@ namespace sparse {
 
 pa_status launch_chosen(int head_dim, int block_size, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a,
                         int num_rows, int splits, int warps, cudaStream_t stream) {
-    return launch_any<kChoose>(head_dim, block_size, fp8, tk, tv, a, num_rows, splits, warps, stream);
+    return launch_any<kChoose>(head_dim, block_size, fp8, tk, tv, a, num_rows, splits, warps, stream, a.group);
 }
 
 }  // namespace sparse

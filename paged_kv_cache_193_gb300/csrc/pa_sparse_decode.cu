@@ -146,7 +146,7 @@ static pa_status run_attend(const Call &c, const SelectArgs *select, cudaStream_
         return launch_chosen(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, l.splits, l.warps, stream);
     }
     const int splits = c.splits ? c.splits : splits_of_four_warps(rows, c.top_k, resident);
-    return launch_any<kList>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, 4, stream);
+    return launch_any<kList>(c.head_dim, c.block_size, fp8, tk, tv, a, c.num_rows, splits, 4, stream, a.group);
 }
 
 }  // namespace sparse

@@ -17,6 +17,15 @@ def api(cuda_device):
     return a
 
 
+@pytest.fixture(autouse=True)
+def every_prefix_is_shared():
+    """Small batches would be attended to sequence by sequence; the tests of that restore it."""
+    lib = _lib.load()
+    assert lib.pa_test_set_share_bytes(0) == 0
+    yield
+    assert lib.pa_test_set_share_bytes(-1) == 0
+
+
 CASES = [
     dict(groups=[(1, [1])], Hq=1, Hkv=1, D=64),
     dict(groups=[(1, [0, 1])], Hq=8, Hkv=2),
@@ -38,6 +47,16 @@ CASES = [
     dict(groups=[(150, [900, 3])], Hq=8, Hkv=2),
     dict(groups=[(2 + i % 5, [i % 7]) for i in range(70)], Hq=2, Hkv=2, D=64),  # more groups than lanes
     dict(groups=[(8, [20, 30])], Hq=8, Hkv=2, extra=200),           # tables wider than the sequences
+    # a warp to a KV head: many rows and short lists
+    dict(groups=[(9, [i % 113 for i in range(86)])], Hq=6, Hkv=6),
+    dict(groups=[(9, [i % 60 for i in range(175)])], Hq=9, Hkv=3, D=64, B=32),   # and a warp without one
+    dict(groups=[(5, [i % 120 for i in range(130)])], Hq=64, Hkv=4),
+    dict(groups=[(40, [i % 101 for i in range(110)])], Hq=20, Hkv=5, fp8=True, per_head=True),
+    dict(groups=[(9, [i % 90 for i in range(260)] + [-1, None, -100])], Hq=2, Hkv=2, D=64, fp8=True),
+    # longest first, and several CTAs to a row
+    dict(groups=[(12, [(37 * i) % 400 for i in range(30)])], Hq=8, Hkv=2),
+    dict(groups=[(12, [(211 * i) % 1100 for i in range(9)] + [None, -3])], Hq=8, Hkv=2),
+    dict(groups=[(12, [3, 2500, 1, 1000])], Hq=4, Hkv=1, fp8=True),
 ]
 
 
@@ -45,7 +64,7 @@ CASES = [
 def test_matches_the_definition(api, cuda_device, kw):
     case = Shared(cuda_device, **kw)
     S, Hq, D = case.q.shape
-    n = api.shared_prefix_workspace_size(S, len(case.pb), Hq, case.pool.Hkv, D, case.pool.B, case.most)
+    n = api.shared_prefix_workspace_size(S, len(case.pb), Hq, case.pool.Hkv, D, case.pool.B, case.most, int(case.pool.fp8))
     ws = Guarded((n,), torch.uint8, cuda_device)
     out = Guarded(case.q.shape, torch.bfloat16, cuda_device, fill=float("nan"))
     k0, v0, q0 = case.pool.kd.clone(), case.pool.vd.clone(), case.q.clone()
@@ -68,6 +87,9 @@ def test_matches_the_definition(api, cuda_device, kw):
     within(case.call(api, max_prefix_blocks=None), want, "no bound")
     within(case.call(api, max_prefix_blocks=min(3, case.bt.shape[1])), want, "a bound below the prefix")
     within(case.call(api, max_prefix_blocks=0), want, "nothing shared")
+    _lib.load().pa_test_set_share_bytes(1 << 60)
+    assert api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, case.most) is None
+    within(case.call(api), want, "too little to share")
 
 
 def test_no_groups_and_no_sequences(api, cuda_device):

@@ -52,7 +52,7 @@ def test_norm_rope_append_of_nothing_is_a_no_op(lib):
 
 
 def _shared(lib, **kw):
-    a = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, mb=64, cl=FAKE, S=4, gs=FAKE, pb=FAKE, G=2, mp=32, Hq=8, Hkv=2, D=128, NB=64, B=16,
+    a = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, mb=4096, cl=FAKE, S=8, gs=FAKE, pb=FAKE, G=2, mp=4096, Hq=8, Hkv=2, D=128, NB=64, B=16,
              dt=0, kvs=1.0, ksc=None, vsc=None, sm=0.088, ws=FARTHER, wsb=1 << 30, out=FAR)
     a.update(kw)
     return lib.pa_shared_prefix_decode(a["q"], a["kc"], a["vc"], a["bt"], a["mb"], a["cl"], a["S"], a["gs"], a["pb"], a["G"], a["mp"],
@@ -86,7 +86,7 @@ def test_both_attentions_reject_on_host(lib, call, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(G=-1), 1), (dict(G=5), 1), (dict(mp=-1), 1), (dict(mp=65), 1), (dict(gs=None), 1), (dict(pb=None), 1),
+    (dict(G=-1), 1), (dict(G=9), 1), (dict(mp=-1), 1), (dict(mp=4097), 1), (dict(gs=None), 1), (dict(pb=None), 1),
 ])
 def test_shared_prefix_rejects_on_host(lib, kw, status):
     assert _shared(lib, **kw) == status
@@ -107,16 +107,26 @@ def test_workspace_sizes(lib):
     size = api.shared_prefix_workspace_size
     assert size(4, 0, 8, 2, 128, 16, 32) == 0 == size(4, 1, 8, 2, 128, 16, 0)  # nothing shared
     assert size(4, 1, 9, 2, 128, 16, 32) == 0                                  # the call refuses such heads
-    for n in (1, 4, 256, 65535):
-        row = n * 32 * (128 + 2) * 4
-        got = size(n, 1, 32, 8, 128, 16, 2048)
-        assert got % row == 0 and 1 <= got // row <= 32
-    assert size(65535, 1, 32, 8, 128, 16, 128) == 65535 * 32 * 130 * 4         # enough tiles: one part
+    assert size(4, 1, 32, 8, 128, 16, 63) == 0                                 # little to share: 16.5 MB
+    assert size(15, 1, 32, 8, 128, 16, 65) == 0 != size(16, 1, 32, 8, 128, 16, 62)  # 63.9 and 65.0 MB
+    assert size(31, 1, 32, 8, 128, 16, 62, 1) == 0 != size(32, 1, 32, 8, 128, 16, 62, 1)  # E4M3: half of that each
+    try:
+        assert lib.pa_test_set_share_bytes(0) == 0
+        for n in (1, 4, 256, 65535):
+            row = n * 32 * (128 + 2) * 4
+            got = size(n, 1, 32, 8, 128, 16, 2048)
+            assert got % row == 0 and 1 <= got // row <= 32
+        assert size(65535, 1, 32, 8, 128, 16, 128) == 65535 * 32 * 130 * 4     # enough tiles: one part
+        assert size(4, 0, 8, 2, 128, 16, 32) == 0 == size(4, 1, 8, 2, 128, 16, 0)
+    finally:
+        assert lib.pa_test_set_share_bytes(-1) == 0
     size = api.cross_workspace_size
     assert size(8192, 16, 512, 32, 8, 128, 128, 16) == 0                       # one part, which needs none
-    row = 16 * (64 + 2) * 4
-    got = size(1, 1, 1, 16, 16, 64, 94, 16)
+    assert size(1, 1, 1, 16, 16, 64, 94, 16) == 0                              # a handful of rows: a kernel that needs none
+    row = 20 * 16 * (64 + 2) * 4
+    got = size(20, 1, 20, 16, 16, 64, 94, 16)
     assert got % row == 0 and 2 <= got // row <= 32
+    assert size(20, 1, 10 ** 6, 16, 16, 64, 94, 16) == got                     # no more rows than there are
     assert size(0, 1, 1, 16, 16, 64, 94, 16) == 0
 
 
@@ -195,9 +205,11 @@ def test_attention_bindings_refuse(lib, fns, change, err, match):
 
 def test_a_step_holds_its_buffers():
     kc = z(4, 2, 16, 64, dtype=bf)
-    step = api.SharedPrefixDecodeStep(kc, kc, z(3, 8), z(3), z(3), z(32, dtype=torch.float64), 4, z(2), z(1), 5)
+    wide = 3, 20000  # 320,000 tokens of prefix: enough to share
+    step = api.SharedPrefixDecodeStep(kc, kc, z(*wide), z(3), z(3), z(32, dtype=torch.float64), 4, z(2), z(1))
     assert step.launches() == 4 and not step.norm
-    assert step.workspace.numel() == api.shared_prefix_workspace_size(3, 1, 4, 2, 64, 16, 5)
+    assert step.workspace.numel() == api.shared_prefix_workspace_size(3, 1, 4, 2, 64, 16, 20000)
+    assert api.SharedPrefixDecodeStep(kc, kc, z(3, 8), z(3), z(3), z(32, dtype=torch.float64), 4, z(2), z(1), 5).launches() == 3
     assert api.SharedPrefixDecodeStep(kc, kc, z(3, 8), z(3), z(3), z(32, dtype=torch.float64), 4, z(2), z(1), 0).launches() == 3
     assert api.SharedPrefixDecodeStep(kc, kc, z(3, 8), z(3), z(3), z(32, dtype=torch.float64), 4, z(2), z(1), k_weight=z(64, dtype=bf)).norm
 
