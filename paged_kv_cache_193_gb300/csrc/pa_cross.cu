@@ -27,8 +27,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, con
     const int lane = threadIdx.x & 31, s = blockIdx.y;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
     const int t = static_cast<int>(row / a.num_q_heads), hq = static_cast<int>(row - static_cast<int64_t>(t) * a.num_q_heads);
-    int first, count;
-    if (!query_range(a, s, first, count) || t >= count) return;
+    const int first = a.query_start[s], end = a.query_start[s + 1];
+    if (!query_range(a, first, end) || t >= end - first) return;
     const int keys = min(max(a.lens[s], 0), a.max_blocks * a.block_size);
     const int parts = live_parts((keys + kKeys - 1) / kKeys, a.parts);
     const int64_t at = (static_cast<int64_t>(first) + t) * a.num_q_heads + hq, stride = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;

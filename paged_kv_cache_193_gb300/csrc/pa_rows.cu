@@ -47,6 +47,7 @@ constexpr float kLazy = 8.f;
 // 2^8, and whole bits down to 2^-21.
 constexpr float kRaise = 128.f;
 constexpr uint64_t kDrainNs = 2000000000ull;
+constexpr int kMaxSorted = 256;       // sequences that a CTA ranks by length
 
 // Two tiles of 128 rows, one CTA to an SM; or one of up to 64, two CTAs to an SM:
 // then the rows are few, the pages' copies are what takes the time, and one CTA's
@@ -107,27 +108,104 @@ struct Work {
     int table;   // whose table row leads to the keys
     int keys;    // of the whole run
     int part;
+    int head;
 };
 
-// Called by whole warps; every warp comes to the same answer.  False: nothing to do.
+// Cross attention over runs of unlike lengths: `unit` counts the CTAs that the
+// sequences' rows need, those of the longest run first, so that the last to start
+// are the shortest, and a sequence without rows has none.  (40 sequences of 0 to 301
+// rows and 0 to 2,999 states: a grid of every sequence's most CTAs, in order, left a
+// fifth of the SMs' time unused.)  Called by all threads with 4 KB of shared memory;
+// every thread comes to the same answer: the sequence, its rows and states, and the
+// CTA's place among its CTAs; false for none.  One round of loads for all of it.
 template <int TILES>
-__device__ __forceinline__ bool find_work(const Args &a, Work &w) {
+__device__ __forceinline__ bool longest_unit(const Args &a, int unit, void *room, int &place, Work &w) {
+    int *len = static_cast<int *>(room), *order = len + kMaxSorted, *start = order + kMaxSorted;  // kMaxSorted each, and one more
+    const int each = TILES * a.tile_tokens, padded = (a.num_seqs + 3) & ~3;
+    for (int i = threadIdx.x; i <= a.num_seqs; i += blockDim.x) {
+        start[i] = a.query_start[i];
+        if (i < a.num_seqs) len[i] = max(a.lens[i], 0);
+    }
+    for (int i = a.num_seqs + threadIdx.x; i < padded; i += blockDim.x) len[i] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x) {
+        const int mine = len[i];
+        int before = 0;
+        for (int j = 0; j < padded; j += 4) {
+            const int4 x = *reinterpret_cast<const int4 *>(len + j);
+            before += (x.x > mine || (x.x == mine && j < i)) + (x.y > mine || (x.y == mine && j + 1 < i)) +
+                      (x.z > mine || (x.z == mine && j + 2 < i)) + (x.w > mine || (x.w == mine && j + 3 < i));
+        }
+        int count = 0;
+        if (query_range(a, start[i], start[i + 1]))
+            count = (start[i + 1] - start[i] + each - 1) / each;
+        else
+            set_device_error(a.err, PA_DEVERR_BAD_CONTEXT);
+        order[before] = i | count << 9;  // kMaxSorted is 2^8
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    int s = -1;
+    for (int i0 = 0; i0 < a.num_seqs && s < 0; i0 += 32) {
+        const int x = i0 + lane < a.num_seqs ? order[i0 + lane] : 0;
+        int before = x >> 9;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d) before += y;
+        }
+        const unsigned has = __ballot_sync(0xffffffffu, before > unit);
+        const int pick = has ? __ffs(has) - 1 : 31;
+        unit -= __shfl_sync(0xffffffffu, before, pick);
+        if (has) {
+            const int y = __shfl_sync(0xffffffffu, x, pick);
+            s = y & 511;
+            place = unit + (y >> 9);
+        }
+    }
+    if (s >= 0) {
+        w.table = s;
+        w.token0 = start[s];
+        w.tokens = start[s + 1] - w.token0;
+        w.keys = len[s];
+    }
+    __syncthreads();  // the room is used again
+    return s >= 0;
+}
+
+// Called by all threads, which come to the same answer.  False: nothing to do.
+template <int TILES>
+__device__ __forceinline__ bool find_work(const Args &a, void *room, Work &w) {
     const int lane = threadIdx.x & 31;
     const int cap = a.max_blocks * a.block_size;
-    int pair = blockIdx.x / a.parts;
-    w.part = blockIdx.x - pair * a.parts;
+    w.head = blockIdx.y;
     if (!a.group_start) {
-        const int s = blockIdx.z;
-        const bool good = query_range(a, s, w.token0, w.tokens);
-        w.at = TILES * pair * a.tile_tokens;
-        w.table = s;
-        w.keys = max(a.lens[s], 0);
+        int place;
+        bool good = true;
+        if (a.sorted) {
+            const int x = blockIdx.x / a.num_kv_heads, unit = x / a.parts;
+            w.head = blockIdx.x - x * a.num_kv_heads;
+            w.part = x - unit * a.parts;
+            if (!longest_unit<TILES>(a, unit, room, place, w)) return false;
+        } else {
+            place = blockIdx.x / a.parts;
+            w.part = blockIdx.x - place * a.parts;
+            w.table = blockIdx.z;
+            w.token0 = a.query_start[w.table];
+            const int end = a.query_start[w.table + 1];
+            good = query_range(a, w.token0, end);
+            w.tokens = end - w.token0;
+            w.keys = max(a.lens[w.table], 0);
+        }
+        w.at = TILES * place * a.tile_tokens;
         if (!good || w.keys > cap) {
             if (threadIdx.x == 0) set_device_error(a.err, PA_DEVERR_BAD_CONTEXT);
             w.keys = min(w.keys, cap);
         }
         return good && w.at < w.tokens;
     }
+    int pair = blockIdx.x / a.parts;
+    w.part = blockIdx.x - pair * a.parts;
     // The pair's group: the groups' pairs lie one after the other.
     int first = 0, end = 0, pages = 0;
     bool found = false;
@@ -191,7 +269,6 @@ __global__ void __launch_bounds__(Layout<D, FP8, TILES>::kThreads, Layout<D, FP8
 
     const uint32_t base = smem_addr(smem_raw);
     const uint64_t limit = a.wait_limit_ns;
-    const int h = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     dependent_wait();
@@ -199,7 +276,8 @@ __global__ void __launch_bounds__(Layout<D, FP8, TILES>::kThreads, Layout<D, FP8
     // them, and waits for this one's end itself.
     if (a.group_start) dependent_release();
     Work w;
-    if (!find_work<TILES>(a, w)) return;
+    if (!find_work<TILES>(a, smem_raw, w)) return;
+    const int h = w.head;
     const int all = (w.keys + kKeys - 1) / kKeys, each = blocks_per_part(all, a.parts);
     const int first = w.part * each, nkb = min(each, all - first);  // this part's blocks
     const int ntiles = TILES == 2 && w.at + a.tile_tokens < w.tokens ? 2 : 1;
@@ -679,8 +757,17 @@ pa_status launch_rows(const void *q, const void *k_cache, const void *v_cache, i
     if (st == PA_OK) st = make_map(&tk, k_cache, fp8, head_dim, pool_rows, a.block_size);
     if (st == PA_OK) st = make_map(&tv, v_cache, fp8, head_dim, pool_rows, a.block_size);
     if (st != PA_OK) return st;
-    if (ctas * a.parts > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many rows for one launch");
-    const dim3 grid(static_cast<unsigned>(ctas * a.parts), a.num_kv_heads, seqs);
+    dim3 grid(1, a.num_kv_heads, seqs);
+    int64_t x = ctas * a.parts;
+    // A few waves or more of CTAs, of sequences that a CTA can sort: by length.
+    a.sorted = !a.group_start && seqs > 1 && seqs <= kMaxSorted && x * a.num_kv_heads * seqs > kSms;
+    if (a.sorted) {
+        const int64_t each = static_cast<int64_t>(tiles) * a.tile_tokens;
+        x = std::min(ctas * seqs, a.num_tokens / each + seqs) * a.parts * a.num_kv_heads;
+        grid.y = grid.z = 1;
+    }
+    if (x > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "too many rows for one launch");
+    grid.x = static_cast<unsigned>(x);
     auto shape = [&](auto d, auto t) {
         return fp8 ? launch<d.value, true, t.value>(tq, tk, tv, a, grid, stream)
                    : launch<d.value, false, t.value>(tq, tk, tv, a, grid, stream);

@@ -62,6 +62,7 @@ struct Args {
     float2 *part_ml;     // [parts][rows]
     // cross attention: sequence s's rows are tokens query_start[s] .. query_start[s + 1] - 1
     const int32_t *query_start;
+    int sorted;  // the longest runs first (found by the launch)
     // shared prefix: group g's sequences are group_start[g] .. group_start[g + 1] - 1
     const int32_t *group_start;
     const int32_t *prefix_blocks;
@@ -80,13 +81,9 @@ inline int64_t tile_ctas(int64_t tokens, int group, int tiles) {
 // `even`: all runs are as long as that; `direct`: one part needs no joining.
 int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_rows, bool even, bool direct);
 
-// Rows of sequence s: false for what is no range of the tokens, or longer than it may be.
-__device__ __forceinline__ bool query_range(const Args &a, int s, int &first, int &count) {
-    first = a.query_start[s];
-    const int end = a.query_start[s + 1];
-    if (first < 0 || end < first || end > a.num_tokens || end - first > a.max_query_len) return false;
-    count = end - first;
-    return true;
+// Whether `first` .. `end` - 1 is a range of the tokens, and no longer than it may be.
+__device__ __forceinline__ bool query_range(const Args &a, int first, int end) {
+    return first >= 0 && end >= first && end <= a.num_tokens && end - first <= a.max_query_len;
 }
 
 // Checks of arguments, for both (pa_shared.cu).
