@@ -86,19 +86,37 @@ struct Args {
 constexpr int kThreads = 256;
 constexpr int kMaxTile = 8;
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &w, float2 (&x)[4]) {
     const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) x[i] = __bfloat1622float2(h[i]);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]), pack2<false>(x[4], x[5]),
-                      pack2<false>(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+    return make_uint4(pack2<false>(x[0].x, x[0].y), pack2<false>(x[1].x, x[1].y), pack2<false>(x[2].x, x[2].y),
+                      pack2<false>(x[3].x, x[3].y));
+}
+
+// Two fp32 products, sums or fused multiply-adds in one instruction, each rounded
+// as by itself.
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) { return __fmul2_rn(x, y); }
+__device__ __forceinline__ float2 add2(float2 x, float2 y) { return __fadd2_rn(x, y); }
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) { return __ffma2_rn(x, y, z); }
+
+// Where entry p of a table in shared memory lies: the first halves of all groups of
+// eight, then the second, so that lanes that read a group each find their 16 bytes
+// side by side.
+template <int N>
+__device__ __forceinline__ constexpr int spread(int p) {
+    return (p & 4) * (N / 8) + (p >> 3) * 4 + (p & 3);
+}
+template <int N>
+__device__ __forceinline__ void take8(const float *table, int group, float2 (&x)[4]) {
+    const float4 lo = *reinterpret_cast<const float4 *>(table + 4 * group), hi = *reinterpret_cast<const float4 *>(table + N / 2 + 4 * group);
+    x[0] = make_float2(lo.x, lo.y);
+    x[1] = make_float2(lo.z, lo.w);
+    x[2] = make_float2(hi.x, hi.y);
+    x[3] = make_float2(hi.z, hi.w);
 }
 
 // f / 2 pi modulo one turn, as a 64-bit fraction of a turn, from the bits of f
@@ -119,12 +137,12 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
 
 // Eight fp32 values as E4M3 codes of x / scale: one rounding from fp32 (the
 // rotated row is not rounded to bf16 on the way).
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divisor &by) {
+__device__ __forceinline__ uint2 codes8(const float2 (&x)[4], const Divisor &by) {
     uint32_t w[2] = {0, 0};
     uint32_t least = 0xffffffffu;  // of the endings, plus 4, in the upper 19 bits
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        const float2 y = make_float2(__fmul_rn(x[i], by.inverse), __fmul_rn(x[i + 1], by.inverse));
+        const float2 y = make_float2(__fmul_rn(x[i / 2].x, by.inverse), __fmul_rn(x[i / 2].y, by.inverse));
         least = min(least, min(__float_as_uint(y.x) * 8192u + 32768u, __float_as_uint(y.y) * 8192u + 32768u));
         w[i / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << 8 * (i % 4);
     }
@@ -132,7 +150,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divisor &by) 
         w[0] = w[1] = 0;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float2 y = make_float2(__fdiv_rn(x[i], by.scale), __fdiv_rn(x[i + 1], by.scale));
+            const float2 y = make_float2(__fdiv_rn(x[i / 2].x, by.scale), __fdiv_rn(x[i / 2].y, by.scale));
             w[i / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << 8 * (i % 4);
         }
     }
@@ -143,12 +161,17 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divisor &by) 
 // (i, i + R/2) elements 8j .. 8j+7 and their partners, with adjacent pairs
 // elements 16j .. 16j+15; either way pairs 8j .. 8j+7, and two 16-byte loads.
 // Its j is the same for every row it takes.
-// CTAS: of the kernel to an SM, which caps its registers.
-template <int D, bool FP8, bool ADJACENT, bool NORM, int CTAS>
+// NORM: none, with weights (or none) that all heads share, which are kept in shared
+// memory, or with each head's own.  CTAS: of the kernel to an SM, which caps its
+// registers.
+enum { kNone, kShared, kHeads };
+template <int D, bool FP8, bool ADJACENT, int NORM, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
     constexpr int VPR = D / 16;  // threads to a row
     __shared__ __align__(16) float cs[kMaxTile][D / 2], sn[kMaxTile][D / 2];
     __shared__ int64_t row_s[kMaxTile];  // the slot's row of head 0, or -1
+    // weights that all heads have, with the offset: q's, then k's
+    __shared__ __align__(16) float weight_s[NORM == kShared ? 2 : 1][NORM == kShared ? D : 1];
     dependent_wait();
     const int t0 = blockIdx.x * a.tile;
     const int live = min(a.tile, a.num_tokens - t0);
@@ -193,9 +216,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
         float s, c;
         sincospif(half_turns, &s, &c);
-        cs[tok][p] = c * a.magnitude;
-        sn[tok][p] = s * a.magnitude;
+        cs[tok][spread<D / 2>(p)] = c * a.magnitude;
+        sn[tok][spread<D / 2>(p)] = s * a.magnitude;
     }
+    if constexpr (NORM == kShared)
+        for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+            const __nv_bfloat16 *weight = x < D ? a.q_weight : a.k_weight;
+            weight_s[x / D][spread<D>(x % D)] = weight ? __bfloat162float(weight[x % D]) + a.weight_offset : 1.f;
+        }
     if (threadIdx.x < live) {
         int32_t slot = a.slots[t0 + threadIdx.x];
         if (slot >= a.num_slots) {
@@ -219,66 +247,78 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
             *reinterpret_cast<uint4 *>(to + dst + db) = wb;
             return;
         }
-        float xa[8], xb[8];
+        float2 xa[4], xb[4];
         unpack8(wa, xa);
         unpack8(wb, xb);
         if constexpr (NORM) {
             if (!is_v) {
+                uint4 ra, rb;
                 const __nv_bfloat16 *weight = is_q ? a.q_weight : a.k_weight;
-                uint4 ga, gb;
-                if (weight) {
+                if (NORM == kHeads && weight) {
                     weight += h * (is_q ? a.q_weight_stride : a.k_weight_stride);
-                    ga = *reinterpret_cast<const uint4 *>(weight + ea);
-                    gb = *reinterpret_cast<const uint4 *>(weight + eb);
+                    ra = *reinterpret_cast<const uint4 *>(weight + ea);
+                    rb = *reinterpret_cast<const uint4 *>(weight + eb);
                 }
-                float sum[2] = {0.f, 0.f};
+                float2 sum = mul2(xa[0], xa[0]), more = mul2(xb[0], xb[0]);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    sum[0] = fmaf(xa[u], xa[u], sum[0]);
-                    sum[1] = fmaf(xb[u], xb[u], sum[1]);
+                for (int u = 1; u < 4; ++u) {
+                    sum = fma2(xa[u], xa[u], sum);
+                    more = fma2(xb[u], xb[u], more);
                 }
-                sum[0] += sum[1];
+                sum = add2(sum, more);
+                float all = sum.x + sum.y;
                 const unsigned lanes = ((1u << VPR) - 1u) << (threadIdx.x & 31 & ~(VPR - 1));  // the row's
 #pragma unroll
-                for (int d = 1; d < VPR; d *= 2) sum[0] += __shfl_xor_sync(lanes, sum[0], d);
-                const float r = rsqrtf(sum[0] * (1.f / D) + a.eps);
+                for (int d = 1; d < VPR; d *= 2) all += __shfl_xor_sync(lanes, all, d);
+                const float r = rsqrtf(all * (1.f / D) + a.eps);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    xa[u] *= r;
-                    xb[u] *= r;
+                for (int u = 0; u < 4; ++u) {
+                    xa[u] = mul2(xa[u], make_float2(r, r));
+                    xb[u] = mul2(xb[u], make_float2(r, r));
                 }
-                if (weight) {
-                    float g[8];
-                    unpack8(ga, g);
+                float2 g[4];
+                auto scale = [&](float2 (&x)[4], int e, const uint4 &raw) {  // elements e .. e + 7
+                    if constexpr (NORM == kShared) {
+                        take8<D>(weight_s[is_q ? 0 : 1], e / 8, g);
+                    } else {
+                        if (!weight) return;
+                        unpack8(raw, g);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) xa[u] *= g[u] + a.weight_offset;
-                    unpack8(gb, g);
+                        for (int u = 0; u < 4; ++u) g[u] = add2(g[u], make_float2(a.weight_offset, a.weight_offset));
+                    }
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) xb[u] *= g[u] + a.weight_offset;
-                }
+                    for (int u = 0; u < 4; ++u) x[u] = mul2(x[u], g[u]);
+                };
+                scale(xa, ea, ra);
+                scale(xb, eb, rb);
             }
         }
         if (rotate) {
-            float c[8], s[8];
-#pragma unroll
-            for (int u = 0; u < 8; u += 4) {
-                *reinterpret_cast<float4 *>(c + u) = *reinterpret_cast<const float4 *>(&cs[tt][8 * j + u]);
-                *reinterpret_cast<float4 *>(s + u) = *reinterpret_cast<const float4 *>(&sn[tt][8 * j + u]);
-            }
-            auto rot = [&](float &u, float &w, int i8) {
-                const float p = u, r = w;
-                u = fmaf(p, c[i8], -(r * s[i8]));
-                w = fmaf(p, s[i8], r * c[i8]);
+            float2 c[4], s[4];
+            take8<D / 2>(cs[tt], j, c);
+            take8<D / 2>(sn[tt], j, s);
+            // (p, r) of a pair become (p c - r s, p s + r c): the inner product is rounded,
+            // then a fused multiply-add
+            auto turn2 = [](float2 &p, float2 &r, float2 co, float2 si) {
+                const float2 u = mul2(r, si), w = mul2(r, co), x = p;
+                p = fma2(x, co, make_float2(-u.x, -u.y));
+                r = fma2(x, si, w);
             };
             if constexpr (ADJACENT) {
+                auto turn4 = [&](float2 (&x)[4], int first) {  // pairs first .. first + 3 of c, s
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    rot(xa[2 * u], xa[2 * u + 1], u);
-                    rot(xb[2 * u], xb[2 * u + 1], 4 + u);
-                }
+                    for (int u = 0; u < 4; u += 2) {
+                        float2 p = make_float2(x[u].x, x[u + 1].x), r = make_float2(x[u].y, x[u + 1].y);
+                        turn2(p, r, c[(first + u) / 2], s[(first + u) / 2]);
+                        x[u] = make_float2(p.x, r.x);
+                        x[u + 1] = make_float2(p.y, r.y);
+                    }
+                };
+                turn4(xa, 0);
+                turn4(xb, 4);
             } else {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) rot(xa[u], xb[u], u);
+                for (int u = 0; u < 4; ++u) turn2(xa[u], xb[u], c[u], s[u]);
             }
         }
         if (is_q) {
@@ -333,23 +373,24 @@ static int tokens_per_cta(int num_tokens, int rows, int head_dim) {
     return best;
 }
 
-template <int D, bool FP8, bool ADJACENT, bool NORM>
+template <int D, bool FP8, bool ADJACENT, int NORM>
 static cudaError_t launch_ctas(const Args &a, dim3 grid, cudaStream_t stream) {
-    if constexpr (D == 128)
+    if constexpr (D == 128 && NORM != kHeads)
         if (five_to_an_sm(D, static_cast<int64_t>(grid.x) * grid.y))
             return launch_dependent(append_kernel<D, FP8, ADJACENT, NORM, 5>, grid, kThreads, 0, 0, stream, a);
     return launch_dependent(append_kernel<D, FP8, ADJACENT, NORM, 4>, grid, kThreads, 0, 0, stream, a);
 }
 
-template <int D, bool FP8, bool NORM>
+template <int D, bool FP8, int NORM>
 static cudaError_t launch_adjacent(const Args &a, bool adjacent, dim3 grid, cudaStream_t stream) {
     return adjacent ? launch_ctas<D, FP8, true, NORM>(a, grid, stream) : launch_ctas<D, FP8, false, NORM>(a, grid, stream);
 }
 
 template <int D, bool FP8>
-static cudaError_t launch(const Args &a, bool adjacent, bool norm, dim3 grid, cudaStream_t stream) {
-    return norm ? launch_adjacent<D, FP8, true>(a, adjacent, grid, stream)
-                : launch_adjacent<D, FP8, false>(a, adjacent, grid, stream);
+static cudaError_t launch(const Args &a, bool adjacent, int norm, dim3 grid, cudaStream_t stream) {
+    return norm == kNone     ? launch_adjacent<D, FP8, kNone>(a, adjacent, grid, stream)
+           : norm == kShared ? launch_adjacent<D, FP8, kShared>(a, adjacent, grid, stream)
+                             : launch_adjacent<D, FP8, kHeads>(a, adjacent, grid, stream);
 }
 
 // What the norm adds to a call.
@@ -473,10 +514,11 @@ static pa_status append(const void *q, int64_t q_stride, const void *k, int64_t 
     a.err = err;
     a.q_weight = norm ? static_cast<const __nv_bfloat16 *>(norm->q_weight) : nullptr;
     a.k_weight = norm ? static_cast<const __nv_bfloat16 *>(norm->k_weight) : nullptr;
-    a.q_weight_stride = norm ? norm->q_weight_stride : 0;
-    a.k_weight_stride = norm ? norm->k_weight_stride : 0;
+    a.q_weight_stride = a.q_weight ? norm->q_weight_stride : 0;
+    a.k_weight_stride = a.k_weight ? norm->k_weight_stride : 0;
     a.weight_offset = norm ? norm->weight_offset : 0.f;
     a.eps = norm ? norm->eps : 0.f;
+    const int kind = !norm ? kNone : a.q_weight_stride || a.k_weight_stride ? kHeads : kShared;
     const int rows = num_q_heads + 2 * num_kv_heads;
     a.tile = tokens_per_cta(num_tokens, rows, head_dim);
     const int at_once = kThreads / (head_dim / 16);  // rows of one pass of the CTA's threads
@@ -485,10 +527,10 @@ static pa_status append(const void *q, int64_t q_stride, const void *k, int64_t 
     a.rows_per_y = (rows + shares - 1) / shares;
     const dim3 grid((static_cast<unsigned>(num_tokens) + a.tile - 1) / a.tile, (rows + a.rows_per_y - 1) / a.rows_per_y);
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3, adj = adjacent != 0;
-    const cudaError_t e = head_dim == 128 ? (fp8 ? launch<128, true>(a, adj, norm, grid, stream)
-                                                 : launch<128, false>(a, adj, norm, grid, stream))
-                                          : (fp8 ? launch<64, true>(a, adj, norm, grid, stream)
-                                                 : launch<64, false>(a, adj, norm, grid, stream));
+    const cudaError_t e = head_dim == 128 ? (fp8 ? launch<128, true>(a, adj, kind, grid, stream)
+                                                 : launch<128, false>(a, adj, kind, grid, stream))
+                                          : (fp8 ? launch<64, true>(a, adj, kind, grid, stream)
+                                                 : launch<64, false>(a, adj, kind, grid, stream));
     return cuda_check(e, "rope append launch");
 }
 
