@@ -602,13 +602,18 @@ pa_status pa_norm_rope_append(const void *q, int64_t q_stride, const void *k, in
  *                 one each.
  *   Cache types and scales as pa_rope_append; softmax_scale > 0; group 1..16.
  *   out may be q itself and may not overlap it otherwise.  With an E4M3 cache
- *   the query is rounded to fp16 as in pa_decode_partitions.  Two kernels; one,
- *   and no workspace, when nothing is shared or the prefixes are so short that
- *   reading them again costs less than the second kernel.
+ *   the query is rounded to fp16 as in pa_decode_partitions.  Two kernels; three
+ *   where the prefixes and the rest both take long; one, and no workspace, when
+ *   nothing is shared or the prefixes are so short that reading them again costs
+ *   less than a second kernel.
  */
 size_t pa_shared_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads,
                                        int num_kv_heads, int head_dim, int block_size,
                                        int max_prefix_blocks, pa_kv_dtype kv_dtype);
+/* Kernels that a call of these sizes launches: 1, 2 or 3 (0 for no sequences). */
+int pa_shared_prefix_launches(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                              int head_dim, int block_size, int max_blocks_per_seq,
+                              int max_prefix_blocks, pa_kv_dtype kv_dtype);
 pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void *v_cache,
                                   const int32_t *block_tables, int max_blocks_per_seq,
                                   const int32_t *context_lens, int num_seqs,
@@ -717,14 +722,15 @@ pa_status pa_device_errors(unsigned int *flags, int clear);
 pa_status pa_test_set_wait(uint64_t limit_ns, int stall_first_wait);
 
 /*
- * pa_test_set_share_bytes -- TEST HOOK for pa_shared_prefix_decode; not for
+ * pa_test_set_share -- TEST HOOK for pa_shared_prefix_decode; not for
  * production use.  The pages have no counterpart.  A batch whose prefixes, each
- * counted for every sequence, take up to so many bytes is attended to sequence by
+ * counted for every sequence, take up to `bytes` is attended to sequence by
  * sequence (that is faster for small ones); 0: every prefix is taken once,
- * however short; below 0: the default.  Process-wide; read on the host by the
- * call and by pa_shared_prefix_workspace_size.
+ * however short; below 0: the default.  apart: whether the join is a kernel of its
+ * own, 0 or 1; -1: by the call's sizes.  Process-wide; read on the host by the call
+ * and by pa_shared_prefix_workspace_size.
  */
-pa_status pa_test_set_share_bytes(int64_t bytes);
+pa_status pa_test_set_share(int64_t bytes, int apart);
 
 /* Static description of a status code (never NULL). */
 const char *pa_status_string(pa_status status);

@@ -71,6 +71,7 @@ SIGNATURES = {
     "pa_norm_rope_append": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _F, _F, _P, _I, _P, _P, _I, _I, _F, _P, _I,
                                  _I, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
     "pa_shared_prefix_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_shared_prefix_launches": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_shared_prefix_decode": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                      _P, _F, _P, _SZ, _P, _P]),
     "pa_cross_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
@@ -78,7 +79,7 @@ SIGNATURES = {
                                 _P, _SZ, _P, _P]),
     "pa_decode_static_workspace": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                         _F, _I, _P, _P]),
-    "pa_test_set_share_bytes": (_I, [_L]),
+    "pa_test_set_share": (_I, [_L, _I]),
     "pa_test_set_wait": (_I, [ctypes.c_uint64, _I]),
     "pa_device_errors": (_I, [ctypes.POINTER(ctypes.c_uint), _I]),
     "pa_status_string": (ctypes.c_char_p, [_I]),

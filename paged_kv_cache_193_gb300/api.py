@@ -754,7 +754,10 @@ class SharedPrefixDecodeStep:
 
     def launches(self) -> int:
         """Kernels one call launches."""
-        return 3 if self.workspace is None else 4
+        S, Hq, D = self.out.shape
+        return 2 + int(_lib_handle().pa_shared_prefix_launches(
+            S, self.prefix_blocks.shape[0], Hq, self.k_cache.shape[1], D, self.B, self.block_tables.shape[1],
+            self.max_prefix_blocks, cache_dtype_of(self.k_cache)))
 
     def __call__(self, q, k_new, v_new, stream=None):
         slot_mapping(self.block_tables, self.context_lens, self.B, out=self.slots, stream=stream)

@@ -22,7 +22,6 @@ constexpr int kFewRows = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, const float v_scale, __nv_bfloat16 *out) {
-    constexpr int E = D / 32;  // head dims of a lane
     dependent_wait();
     const int lane = threadIdx.x & 31, s = blockIdx.y;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
@@ -31,38 +30,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, con
     if (!query_range(a, first, end) || t >= end - first) return;
     const int keys = min(max(a.lens[s], 0), a.max_blocks * a.block_size);
     const int parts = live_parts((keys + kKeys - 1) / kKeys, a.parts);
-    const int64_t at = (static_cast<int64_t>(first) + t) * a.num_q_heads + hq, stride = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
-    const float2 ml = lane < parts ? a.part_ml[lane * stride + at] : make_float2(-INFINITY, 0.f);
-    float top = ml.x;
-#pragma unroll
-    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    // a part that saw no finite score is left out, one with a NaN in its sum keeps it
-    float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : fast_exp2(ml.x - top);
-    float sum = f != 0.f ? f * ml.y : 0.f;
-#pragma unroll
-    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const float scale = a.v_scales ? a.v_scales[hq / a.group] : v_scale;
-    f *= sum != 0.f ? scale / sum : 0.f;
-    dependent_release();
-    float acc[E] = {};
-    const float *o = a.part_o + at * D + lane * E;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-        float x[E];
-        if constexpr (E == 4)
-            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(o + p * stride * D);
-        else
-            *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(o + p * stride * D);
-        const float w = __shfl_sync(0xffffffffu, f, p);
-        if (w != 0.f)
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] += w * x[i];
-    }
-    __nv_bfloat16 *to = out + at * D + lane * E;
-    if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<false>(acc[0], acc[1]), pack2<false>(acc[2], acc[3]));
-    else
-        *reinterpret_cast<uint32_t *>(to) = pack2<false>(acc[0], acc[1]);
+    const int64_t at = (static_cast<int64_t>(first) + t) * a.num_q_heads + hq, rows = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+    const float2 ml = lane < parts ? a.part_ml[lane * rows + at] : make_float2(-INFINITY, 0.f);
+    join_row<D>(ml, parts, a.part_o + at * D, rows * D, nullptr, a.v_scales ? a.v_scales[hq / a.group] : v_scale, out + at * D);
 }
 
 // How a call is launched: by its sizes alone, which the workspace's size goes by too.

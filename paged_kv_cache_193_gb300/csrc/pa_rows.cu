@@ -724,20 +724,28 @@ static pa_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUte
                       "rows launch");
 }
 
-// Least of an estimate in microseconds: a CTA's start and end, its blocks, and what
-// writing and reading the parts takes.  Runs of one length (`even`) end in whole
-// waves; of others, of which 0.6 of the longest is taken for the average, the work
-// is shared out and the last CTA is half done when the others end.
+// Microseconds of a CTA over `blocks` blocks, its start and end among them.
+double cta_time(int blocks, int tiles, int head_dim) {
+    return tiles == 1 ? 3.0 + (head_dim == 64 ? 0.85 : 1.4) * blocks : 4.0 + (head_dim == 64 ? 0.6 : 0.9) * blocks;
+}
+
+// Writing and reading `parts` parts.
+double join_time(int parts, int head_dim, int64_t num_rows) {
+    return parts * (static_cast<double>(num_rows) * head_dim * 8) / 5e6;
+}
+
+// Least of an estimated time.  Runs of one length (`even`) end in whole waves; of
+// others, of which 0.6 of the longest is taken for the average, the work is shared
+// out and the last CTA is half done when the others end.
 int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_rows, bool even, bool direct) {
     const int64_t places = tiles == 1 ? 2 * kSms : kSms;
-    const double start = tiles == 1 ? 3.0 : 4.0, block = (tiles == 1 ? 1.4 : 1.0) * (head_dim == 64 ? 0.6 : 1.0);
     int best = 1;
     double least = INFINITY;
     for (int parts = 1; parts <= kMaxParts && (parts == 1 || (parts - 1) * kLeastBlocks < blocks); ++parts) {
-        const double one = start + block * blocks_per_part(blocks, parts), n = static_cast<double>(ctas) * parts;
-        double cost = even ? std::ceil(n / places) * one
-                           : std::max(one, (n * start + ctas * block * blocks * 0.6) / places + one / 2);
-        if (parts > 1 || !direct) cost += parts * (static_cast<double>(num_rows) * head_dim * 8) / 5e6;
+        const double one = cta_time(blocks_per_part(blocks, parts), tiles, head_dim), n = static_cast<double>(ctas) * parts;
+        const double start = cta_time(0, tiles, head_dim), work = ctas * (cta_time(blocks, tiles, head_dim) - start);
+        double cost = even ? std::ceil(n / places) * one : std::max(one, (n * start + work * 0.6) / places + one / 2);
+        if (parts > 1 || !direct) cost += join_time(parts, head_dim, num_rows);
         if (cost < least) {
             least = cost;
             best = parts;

@@ -10,6 +10,8 @@
 // which join as M = max m, sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
 #pragma once
 
+#include <math.h>
+
 #include <algorithm>
 
 #include "pa_launch.cuh"
@@ -77,6 +79,10 @@ inline int64_t tile_ctas(int64_t tokens, int group, int tiles) {
     return (tokens + each - 1) / each;
 }
 
+// Estimates in microseconds: of a CTA, and of the parts' way through memory.
+double cta_time(int blocks, int tiles, int head_dim);
+double join_time(int parts, int head_dim, int64_t num_rows);
+
 // Into how many parts to cut runs of up to `blocks` blocks for `ctas` CTAs to a part;
 // `even`: all runs are as long as that; `direct`: one part needs no joining.
 int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_rows, bool even, bool direct);
@@ -84,6 +90,45 @@ int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_
 // Whether `first` .. `end` - 1 is a range of the tokens, and no longer than it may be.
 __device__ __forceinline__ bool query_range(const Args &a, int first, int end) {
     return first >= 0 && end >= first && end <= a.num_tokens && end - first <= a.max_query_len;
+}
+
+// Joins the parts of one row and writes it: by a warp whose lane p has part p's
+// (m, l), and whose last lane has those of `rest` (or of part 31, or none); part p's
+// o is at o + p * stride.  Fewer than 32 parts with a rest.
+template <int D>
+__device__ __forceinline__ void join_row(float2 ml, int parts, const float *o, int64_t stride, const float *rest,
+                                         float v_scale, __nv_bfloat16 *out) {
+    constexpr int E = D / 32;  // head dims of a lane
+    const int lane = threadIdx.x & 31;
+    float top = ml.x;
+#pragma unroll
+    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    // a part that saw no finite score is left out, one with a NaN in its sum keeps it
+    float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : fast_exp2(ml.x - top);
+    float sum = f != 0.f ? f * ml.y : 0.f;
+#pragma unroll
+    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    f *= sum != 0.f ? v_scale / sum : 0.f;
+    dependent_release();
+    float acc[E] = {};
+    auto add = [&](const float *from, float w) {
+        float x[E];
+        if constexpr (E == 4)
+            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(from + lane * E);
+        else
+            *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(from + lane * E);
+        if (w != 0.f)  // an empty part's accumulator may be anything
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] += w * x[i];
+    };
+    if (rest) add(rest, __shfl_sync(0xffffffffu, f, 31));
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) add(o + p * stride, __shfl_sync(0xffffffffu, f, p));
+    __nv_bfloat16 *to = out + lane * E;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<false>(acc[0], acc[1]), pack2<false>(acc[2], acc[3]));
+    else
+        *reinterpret_cast<uint32_t *>(to) = pack2<false>(acc[0], acc[1]);
 }
 
 // Checks of arguments, for both (pa_shared.cu).

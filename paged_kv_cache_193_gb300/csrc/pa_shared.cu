@@ -4,22 +4,39 @@
 // pages).
 //
 // Two kernels.  The first takes a group's prefix once: the queries of all its
-// sequences, 128 rows to a tile, against the prefix's keys (pa_rows.cu), and
+// sequences, up to 128 rows to a tile, against the prefix's keys (pa_rows.cu), and
 // leaves each row's maximum, sum and accumulator.  The second attends to what
 // each sequence has of its own, a cluster of CTAs to a (sequence, KV head)
 // (pa_sparse_attend.cuh), and joins the two at its end.  It is on the SMs as
-// soon as there is room beside the first's last CTAs: only its join waits for
-// the prefix.
+// soon as there is room beside the first's CTAs: only its join waits for the
+// prefix.  Where both have much to do the prefix takes a part of the SMs, the rest
+// goes on beside it without waiting, and a third kernel joins them.
 //
 // A sequence that does not hold the whole prefix of its group attends to all it
 // has in the second kernel.
+//
+// Bound: a prefix's products by the tensor cores and the chain of its softmax (64
+// sequences of 64 heads over 32,768 tokens: 69 GFLOP in 55 us alone), the rest by
+// memory.  Both, with up to 2,048 tokens more each: 90.6 us, where the decode that
+// reads every prefix again takes 570.
+#include <math.h>
+
 #include "pa_sparse_attend.cuh"
 
 namespace pa {
 namespace rows {
 
-// How a prefix's kernel is launched: by a call's sizes alone, which the workspace's
-// size goes by too.
+// What a call's sizes say; the launches go by it.
+struct Sizes {
+    int64_t num_seqs;
+    int num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks;
+    bool fp8;
+    int group() const { return num_q_heads / num_kv_heads; }
+    int64_t rows() const { return num_seqs * num_q_heads; }
+    double page_bytes() const { return static_cast<double>(block_size) * num_kv_heads * head_dim * (fp8 ? 2 : 4); }
+};
+
+// How a prefix is taken.  The workspace's size goes by it.
 struct Plan {
     bool shared;   // or each sequence by itself
     int tiles;     // to a CTA: one where a group mostly has no more
@@ -33,25 +50,36 @@ struct Plan {
 // 4 sequences of 1,024 tokens 10.0 and 7.4, 4 of 4,096 11.7 and 12.4, 32 of 1,024 in
 // E4M3 11.6 and 12.7, 16 of 1,024 in bf16 10.5 and 10.3).
 constexpr int64_t kShareBytes = 64000000;
-static std::atomic<int64_t> g_share_bytes{kShareBytes};  // pa_test_set_share_bytes
+static std::atomic<int64_t> g_share_bytes{kShareBytes};  // pa_test_set_share
+static std::atomic<int> g_apart{-1};
 
-static Plan plan(int64_t num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim, int max_prefix_blocks,
-                 int block_size, bool fp8) {
-    const double all = static_cast<double>(num_seqs) * max_prefix_blocks * block_size * num_kv_heads * head_dim * (fp8 ? 2 : 4);
-    if (num_groups == 0 || max_prefix_blocks == 0 || all <= static_cast<double>(g_share_bytes.load(std::memory_order_relaxed))) return {false, 0, 0, 0};
-    const int group = num_q_heads / num_kv_heads;
-    const int tiles = num_seqs <= static_cast<int64_t>(tile_rows(1) / group) * num_groups ? 1 : 2;
-    const int64_t ctas = std::min(tile_ctas(num_seqs, group, tiles) + num_groups - 1, num_seqs);
-    const int blocks = static_cast<int>((static_cast<int64_t>(max_prefix_blocks) * block_size + kKeys - 1) / kKeys);
-    return {true, tiles, ctas, choose_parts(ctas * num_kv_heads, blocks, tiles, head_dim, num_seqs * num_q_heads, num_groups == 1, false)};
+static int prefix_blocks_of(const Sizes &z) {
+    return static_cast<int>((static_cast<int64_t>(z.max_prefix_blocks) * z.block_size + kKeys - 1) / kKeys);
 }
 
-// How the rest is launched: at most `pages` pages behind the prefix of each of
-// `num_seqs` sequences.
+static Plan plan(const Sizes &z) {
+    const double all = z.num_seqs * z.max_prefix_blocks * z.page_bytes();
+    if (z.num_groups == 0 || z.max_prefix_blocks == 0 ||
+        all <= static_cast<double>(g_share_bytes.load(std::memory_order_relaxed)))
+        return {false, 0, 0, 0};
+    const int tiles = z.num_seqs <= static_cast<int64_t>(tile_rows(1) / z.group()) * z.num_groups ? 1 : 2;
+    const int64_t ctas = std::min(tile_ctas(z.num_seqs, z.group(), tiles) + z.num_groups - 1, z.num_seqs);
+    return {true, tiles, ctas,
+            choose_parts(ctas * z.num_kv_heads, prefix_blocks_of(z), tiles, z.head_dim, z.rows(), z.num_groups == 1, false)};
+}
+
+// The prefix's parts, and one of the rest.
+static size_t plan_bytes(const Sizes &z, const Plan &p) {
+    return p.shared ? workspace_bytes(p.parts + 1, z.rows(), z.head_dim) : 0;
+}
+
+// How the rest is launched.
 struct Suffix {
     bool heads;          // a warp to a KV head, not a CTA
     bool longest_first;
     int splits;          // CTAs to a sequence and KV head
+    bool apart;          // the join is a kernel of its own, and the prefix has so many parts
+    int parts;
 };
 
 // A CTA for every KV head costs about 3.6 us, however little it reads, so few pages
@@ -64,20 +92,69 @@ struct Suffix {
 // with one, 24.0 with two, 18.7 with four; of up to 1,000 in E4M3 11.9, 13.5, 14.4),
 // and to twice that when very long (512 rows of up to 4,000, longest first: 97 with
 // one, 85 with two).
-static Suffix suffix_launch(int64_t num_seqs, int num_groups, int num_kv_heads, bool shared, int pages, int head_dim, int block_size,
-                            bool fp8, int group) {
-    const int64_t rows = num_seqs * num_kv_heads;
-    if (!shared)
-        return {false, false, sparse::splits_of_four_warps(rows, pages, sparse::resident_ctas(head_dim, block_size, fp8, group))};
-    const int at_once = fp8 && block_size == 16 ? 2 : 1;  // pages of a warp's step
-    const int steps = (pages + at_once - 1) / at_once;    // of one warp
-    if ((rows >= 512 && pages <= 8) || (rows >= 2048 && steps <= 16)) return {true, false, 1};
-    Suffix l{false, num_groups == 1 && num_seqs > 1 && num_seqs <= sparse::kMaxSorted && pages >= 16, 1};
+//
+// The join is made apart where an estimate of both ways says so: then the prefix's CTAs
+// may leave SMs to the rest's, and neither waits for the other (64 sequences, 32,768
+// tokens of prefix and up to 2,048 more: 99.5 us joined by the rest's kernel, 90.6
+// apart; 256 in E4M3, 2,048 and up to 512: 49.2 and 45.2; a few sequences of a few
+// thousand tokens take 2 us more apart).
+static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
+    const int64_t rows = z.num_seqs * z.num_kv_heads;
+    // pages behind the prefix: of several groups, the shortest may be none
+    const int pages = max_blocks - (p.shared && z.num_groups == 1 ? z.max_prefix_blocks : 0);
+    if (!p.shared)
+        return {false, false, sparse::splits_of_four_warps(rows, pages, sparse::resident_ctas(z.head_dim, z.block_size, z.fp8, z.group())),
+                false, 0};
+    const int at_once = z.fp8 && z.block_size == 16 ? 2 : 1;  // pages of a warp's step
+    const int steps = (pages + at_once - 1) / at_once;        // of one warp
+    if (rows >= 512 && pages <= 8) return {true, false, 1, false, p.parts};
+    Suffix l{false, z.num_groups == 1 && z.num_seqs > 1 && z.num_seqs <= sparse::kMaxSorted && pages >= 16, 1, false, p.parts};
     if (steps >= 48)
         for (int s : {2, 4, 8})
             if (rows * s <= 512) l.splits = s;
     if (l.splits == 1 && l.longest_first && rows <= 512 && steps >= 96) l.splits = 2;
-    return l;
+
+    const int mode = g_apart.load(std::memory_order_relaxed);
+    const bool heads = rows >= 2048 && steps <= 16;
+    // Half of the pages that the tables have room for, at 6.2 TB/s; many short lists go
+    // a little slower.
+    const double rest = z.num_seqs * (max_blocks - z.max_prefix_blocks) * 0.5 * z.page_bytes() / 6.2e6 * (pages < 64 ? 1.3 : 1.0);
+    const int64_t ctas = p.ctas * z.num_kv_heads, places = (p.tiles == 1 ? 2 : 1) * kSms;
+    const int blocks = prefix_blocks_of(z);
+    const double average = z.num_groups == 1 ? 1.0 : 0.6;  // of runs of unlike lengths, beside the longest
+    auto one = [&](int parts) { return cta_time(blocks_per_part(blocks, parts), p.tiles, z.head_dim); };
+    auto waves = [&](int parts) { return std::ceil(static_cast<double>(ctas) * parts / places); };
+    const double together = waves(p.parts) * one(p.parts) * average + join_time(p.parts, z.head_dim, z.rows()) + rest;
+    double least = INFINITY;
+    for (int parts = 1; parts <= p.parts && parts < kMaxParts; ++parts) {
+        const double cost = std::max(waves(parts) * one(parts), ctas * parts * one(parts) * average / places + rest) +
+                            join_time(parts + 1, z.head_dim, z.rows()) + 3.0;
+        if (cost < least) {
+            least = cost;
+            l.parts = parts;
+        }
+    }
+    l.apart = mode == 1 || (mode < 0 && least < together);
+    if (l.apart) return l;
+    return heads ? Suffix{true, false, 1, false, p.parts} : Suffix{false, l.longest_first, l.splits, false, p.parts};
+}
+
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    join_prefix_kernel(const sparse::Args a, const int num_seqs, const int block_size, const float v_scale) {
+    dependent_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5), seq = row / a.num_q_heads;
+    if (seq >= num_seqs) return;
+    const int s = static_cast<int>(seq), hq = static_cast<int>(row - seq * a.num_q_heads);
+    const int skip = sparse::shared_pages(a.prefix, s, min(a.context_lens[s], a.max_blocks * block_size), block_size);
+    const int parts = skip ? live_parts((skip * block_size + kKeys - 1) / kKeys, a.prefix.parts) : 0;
+    const float2 ml = lane < parts ? a.prefix.ml[lane * a.prefix.rows + row]
+                                   : lane == 31 ? a.prefix.rest_ml[row] : make_float2(-INFINITY, 0.f);
+    join_row<D>(ml, parts, a.prefix.o + row * D, a.prefix.rows * D, a.prefix.rest_o + row * D,
+                a.v_scales ? a.v_scales[hq / a.group] : v_scale, a.out + row * D);
 }
 
 pa_status check_rows(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
@@ -126,21 +203,32 @@ using namespace pa;
 
 extern "C" {
 
-pa_status pa_test_set_share_bytes(int64_t bytes) {
+pa_status pa_test_set_share(int64_t bytes, int apart) {
     clear_error();
+    if (apart < -1 || apart > 1) return fail(PA_ERR_INVALID_ARG, "apart %d (-1, 0 or 1)", apart);
     rows::g_share_bytes.store(bytes < 0 ? rows::kShareBytes : bytes, std::memory_order_relaxed);
+    rows::g_apart.store(apart, std::memory_order_relaxed);
     return PA_OK;
 }
 
 size_t pa_shared_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
                                        int block_size, int max_prefix_blocks, pa_kv_dtype kv_dtype) {
     if (num_seqs <= 0 || num_groups <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
-        num_q_heads / num_kv_heads > 16 || head_dim <= 0 || block_size <= 0 || max_prefix_blocks <= 0 ||
+        num_q_heads / num_kv_heads > 16 || (head_dim != 64 && head_dim != 128) || block_size <= 0 || max_prefix_blocks <= 0 ||
         static_cast<int64_t>(max_prefix_blocks) * block_size > 0x7fffffffLL)
         return 0;
-    const rows::Plan p = rows::plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_prefix_blocks, block_size,
-                                    kv_dtype == PA_KV_FP8_E4M3);
-    return rows::workspace_bytes(p.parts, static_cast<int64_t>(num_seqs) * num_q_heads, head_dim);
+    const rows::Sizes z{num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks, kv_dtype == PA_KV_FP8_E4M3};
+    return rows::plan_bytes(z, rows::plan(z));
+}
+
+int pa_shared_prefix_launches(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                              int max_blocks_per_seq, int max_prefix_blocks, pa_kv_dtype kv_dtype) {
+    if (num_seqs <= 0) return 0;
+    if (pa_shared_prefix_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks,
+                                        kv_dtype) == 0)
+        return 1;
+    const rows::Sizes z{num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks, kv_dtype == PA_KV_FP8_E4M3};
+    return rows::suffix_launch(z, rows::plan(z), max_blocks_per_seq).apart ? 3 : 2;
 }
 
 pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
@@ -163,23 +251,25 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     if (num_seqs == 0) return PA_OK;
     st = rows::check_row_pointers(q, k_cache, v_cache, block_tables, context_lens, out, num_seqs, num_q_heads, head_dim);
     if (st != PA_OK) return st;
-    const int64_t num_rows = static_cast<int64_t>(num_seqs) * num_q_heads;
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
-    const rows::Plan p = rows::plan(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_prefix_blocks, block_size, fp8);
-    const bool shared = p.shared;
-    if (shared) {
+    const rows::Sizes z{num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks, fp8};
+    const rows::Plan p = rows::plan(z);
+    const rows::Suffix l = rows::suffix_launch(z, p, max_blocks_per_seq);
+    const int64_t num_rows = z.rows();
+    if (p.shared) {
         if (!group_start || !prefix_blocks) return fail(PA_ERR_INVALID_ARG, "null pointer");
-        st = rows::check_workspace(workspace, workspace_bytes, rows::workspace_bytes(p.parts, num_rows, head_dim), q, out,
+        st = rows::check_workspace(workspace, workspace_bytes, rows::plan_bytes(z, p), q, out,
                                    static_cast<size_t>(num_rows) * head_dim * 2);
         if (st != PA_OK) return st;
     }
     unsigned int *err = device_error_word();
     if (!err) return fail(PA_ERR_CUDA, "cannot resolve the device error word");
-    const int group = num_q_heads / num_kv_heads;
+    const int group = z.group();
+    // the prefix's parts, then the rest's; all their (m, l) behind all their o
     float *part_o = static_cast<float *>(workspace);
-    float2 *part_ml = reinterpret_cast<float2 *>(part_o + p.parts * num_rows * head_dim);
+    float2 *part_ml = reinterpret_cast<float2 *>(part_o + (l.parts + 1) * num_rows * head_dim);
 
-    if (shared) {
+    if (p.shared) {
         rows::Args a = {};
         a.block_tables = block_tables;
         a.lens = context_lens;
@@ -194,7 +284,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
         a.kv_scale = kv_scale;
         a.k_scales = k_scales;
         a.v_scales = v_scales;
-        a.parts = p.parts;
+        a.parts = l.parts;
         a.part_o = part_o;
         a.part_ml = part_ml;
         a.group_start = group_start;
@@ -228,14 +318,20 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     b.err = err;
     b.wait_limit_ns = wait_limit_ns();
     b.stall_first_wait = stall_first_wait();
-    b.prefix = {group_start, prefix_blocks, num_groups, max_prefix_blocks, p.parts, part_o, part_ml, num_rows};
-    // behind the prefix: of several groups, the shortest may be none
-    const int pages = max_blocks_per_seq - (shared && num_groups == 1 ? max_prefix_blocks : 0);
-    const rows::Suffix suffix = rows::suffix_launch(num_seqs, num_groups, num_kv_heads, shared, pages, head_dim, block_size, fp8, group);
-    b.longest_first = suffix.longest_first;
-    if (suffix.heads)
+    b.longest_first = l.longest_first;
+    b.prefix = {group_start, prefix_blocks, num_groups, max_prefix_blocks, l.parts, part_o, part_ml, num_rows, nullptr, nullptr};
+    if (l.heads)
         return sparse::launch_any<sparse::kSuffixHeads>(head_dim, block_size, fp8, tk, tv, b, num_seqs, 1, 4, stream, group);
-    return sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, suffix.splits, 4, stream, group);
+    if (l.apart) {
+        b.prefix.rest_o = part_o + l.parts * num_rows * head_dim;
+        b.prefix.rest_ml = part_ml + l.parts * num_rows;
+    }
+    st = sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, l.splits, 4, stream, group);
+    if (st != PA_OK || !l.apart) return st;
+    const dim3 grid(static_cast<unsigned>((num_rows + rows::kJoinWarps - 1) / rows::kJoinWarps));
+    auto *join = head_dim == 128 ? rows::join_prefix_kernel<128> : rows::join_prefix_kernel<64>;
+    return cuda_check(launch_dependent(join, grid, rows::kJoinWarps * 32, 0, 0, stream, b, num_seqs, block_size, fp8 ? kv_scale : 1.f),
+                      "shared prefix join launch");
 }
 
 }  // extern "C"

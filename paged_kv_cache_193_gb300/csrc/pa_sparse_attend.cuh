@@ -44,6 +44,10 @@ struct Prefix {
     const float *o;                // [parts][rows][head_dim]
     const float2 *ml;              // [parts][rows]
     int64_t rows;
+    // Null: the rest's kernel makes the join, and waits for the prefix's.  Else it leaves
+    // a part of its own, [rows][head_dim] and [rows], for another kernel to join.
+    float *rest_o;
+    float2 *rest_ml;
 };
 
 struct Args {
@@ -743,8 +747,8 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
     __shared__ float pw[SUFFIX ? rows::kMaxParts : 1][SUFFIX ? C::NP : 1];
     int parts = 0;
     if constexpr (SUFFIX) {
-        if (a.prefix.parts) dependent_wait();
-        if (skip) parts = rows::live_parts((skip * BS + rows::kKeys - 1) / rows::kKeys, a.prefix.parts);
+        if (a.prefix.parts && !a.prefix.rest_o) dependent_wait();
+        if (skip && !a.prefix.rest_o) parts = rows::live_parts((skip * BS + rows::kKeys - 1) / rows::kKeys, a.prefix.parts);
     }
     const int64_t part0 = static_cast<int64_t>(s) * a.num_q_heads + h * a.group, part_stride = a.prefix.rows;
     auto with_prefix = [&](float top, float &sum) -> float {  // by thread g < group
@@ -796,6 +800,8 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             }
         mc[tid] = top;
         lc[tid] = sum;
+        if constexpr (SUFFIX)
+            if (a.prefix.rest_o && ranks == 1 && tid < a.group) a.prefix.rest_ml[part0 + tid] = make_float2(top, sum);
     }
     __syncthreads();
     // four head dims of a head at a time
@@ -819,13 +825,21 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
             }
         }
         if (ranks == 1) {
-            if constexpr (SUFFIX) add_prefix(i, v);
+            if constexpr (SUFFIX) {
+                if (a.prefix.rest_o) {
+                    *reinterpret_cast<float4 *>(a.prefix.rest_o + part0 * D + 4 * i) = v;
+                    continue;
+                }
+                add_prefix(i, v);
+            }
             const float sum = lc[g];
             put(i, v, sum != 0.f ? v_scale / sum : 0.f);
         } else {
             *reinterpret_cast<float4 *>(csm + 4 * i) = v;
         }
     }
+    if constexpr (SUFFIX)  // the grid is not to end before the one in front: its last CTA waits for that
+        if (a.prefix.rest_o && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z) dependent_wait();
     if (ranks == 1) return;
 
     // ---- join the CTAs: each writes its share of the output -----------------------
@@ -848,7 +862,12 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         float mine = 1.f;
         if constexpr (SUFFIX)
             if (tid < a.group) mine = with_prefix(top, sum);
-        const float inv = sum != 0.f ? v_scale / sum : 0.f;
+        float inv = sum != 0.f ? v_scale / sum : 0.f;
+        if constexpr (SUFFIX)
+            if (a.prefix.rest_o) {
+                inv = 1.f;
+                if (rank == 0 && tid < a.group) a.prefix.rest_ml[part0 + tid] = make_float2(top, sum);
+            }
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) fsm[k * C::NP + tid] = m[k] * mine * inv;
         if constexpr (SUFFIX)
@@ -873,7 +892,13 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
                 v.w += f * __uint_as_float(x[k].w);
             }
         }
-        if constexpr (SUFFIX) add_prefix(i, v);
+        if constexpr (SUFFIX) {
+            if (a.prefix.rest_o) {
+                *reinterpret_cast<float4 *>(a.prefix.rest_o + part0 * D + 4 * i) = v;
+                continue;
+            }
+            add_prefix(i, v);
+        }
         put(i, v, 1.f);
     }
     // nobody leaves while another may still read its part

@@ -21,9 +21,9 @@ def api(cuda_device):
 def every_prefix_is_shared():
     """Small batches would be attended to sequence by sequence; the tests of that restore it."""
     lib = _lib.load()
-    assert lib.pa_test_set_share_bytes(0) == 0
+    assert lib.pa_test_set_share(0, -1) == 0
     yield
-    assert lib.pa_test_set_share_bytes(-1) == 0
+    assert lib.pa_test_set_share(-1, -1) == 0
 
 
 CASES = [
@@ -73,8 +73,8 @@ def test_matches_the_definition(api, cuda_device, kw):
     assert got.data_ptr() == out.tensor.data_ptr() and api.device_errors() == 0
     want = case.expected()
     within(got, want)
-    for s, n in enumerate(case.lens):
-        assert n or (got[s] == 0).all()
+    for s, length in enumerate(case.lens):
+        assert length or (got[s] == 0).all()
     ws.check("workspace")
     out.check("out")
     for a, b in ((case.pool.kd, k0), (case.pool.vd, v0), (case.q, q0)):  # NaN stays what it is: compare bits
@@ -87,7 +87,14 @@ def test_matches_the_definition(api, cuda_device, kw):
     within(case.call(api, max_prefix_blocks=None), want, "no bound")
     within(case.call(api, max_prefix_blocks=min(3, case.bt.shape[1])), want, "a bound below the prefix")
     within(case.call(api, max_prefix_blocks=0), want, "nothing shared")
-    _lib.load().pa_test_set_share_bytes(1 << 60)
+    for apart in (0, 1):
+        _lib.load().pa_test_set_share(0, apart)
+        ws.tensor.fill_(0xff)  # NaN wherever nothing is written
+        within(case.call(api, workspace=ws.tensor if n else None, out=out.tensor), want, f"joined apart: {apart}")
+        ws.check("workspace")
+        out.check("out")
+        within(case.call(api, max_prefix_blocks=None), want, f"joined apart, no bound: {apart}")
+    _lib.load().pa_test_set_share(1 << 60, -1)
     assert api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, case.most) is None
     within(case.call(api), want, "too little to share")
 

@@ -97,6 +97,10 @@ def test_cross_rejects_on_host(lib, kw, status):
     assert _cross(lib, **kw) == status
 
 
+def test_the_share_hook_is_checked(lib):
+    assert lib.pa_test_set_share(0, 2) == 1 and lib.pa_test_set_share(-1, -1) == 0
+
+
 def test_nothing_to_do_is_a_no_op(lib):
     assert _shared(lib, S=0, G=0, q=None, out=None) == 0
     assert _cross(lib, S=0, q=None, out=None) == 0
@@ -111,15 +115,15 @@ def test_workspace_sizes(lib):
     assert size(15, 1, 32, 8, 128, 16, 65) == 0 != size(16, 1, 32, 8, 128, 16, 62)  # 63.9 and 65.0 MB
     assert size(31, 1, 32, 8, 128, 16, 62, 1) == 0 != size(32, 1, 32, 8, 128, 16, 62, 1)  # E4M3: half of that each
     try:
-        assert lib.pa_test_set_share_bytes(0) == 0
+        assert lib.pa_test_set_share(0, -1) == 0
         for n in (1, 4, 256, 65535):
             row = n * 32 * (128 + 2) * 4
             got = size(n, 1, 32, 8, 128, 16, 2048)
-            assert got % row == 0 and 1 <= got // row <= 32
-        assert size(65535, 1, 32, 8, 128, 16, 128) == 65535 * 32 * 130 * 4     # enough tiles: one part
+            assert got % row == 0 and 2 <= got // row <= 33                   # the prefix's parts and the rest's
+        assert size(65535, 1, 32, 8, 128, 16, 128) == 2 * 65535 * 32 * 130 * 4  # enough tiles: one part
         assert size(4, 0, 8, 2, 128, 16, 32) == 0 == size(4, 1, 8, 2, 128, 16, 0)
     finally:
-        assert lib.pa_test_set_share_bytes(-1) == 0
+        assert lib.pa_test_set_share(-1, -1) == 0
     size = api.cross_workspace_size
     assert size(8192, 16, 512, 32, 8, 128, 128, 16) == 0                       # one part, which needs none
     assert size(1, 1, 1, 16, 16, 64, 94, 16) == 0                              # a handful of rows: a kernel that needs none
