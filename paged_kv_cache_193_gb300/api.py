@@ -722,6 +722,18 @@ def cross_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     return out
 
 
+def _append_of(step, q, k_new, v_new, stream):
+    """A step's rotate-and-append, of normalised q and k where the step has a norm."""
+    if step.norm:
+        norm_rope_append(q, k_new, v_new, step.positions, step.inv_freq, step.slots, step.k_cache, step.v_cache,
+                         step.q_weight, step.k_weight, step.eps, step.weight_offset, step.pair_axis, step.adjacent,
+                         step.magnitude, step.kv_scale, step.k_scales, step.v_scales, step.q_rotated, stream)
+    else:
+        rope_append(q, k_new, v_new, step.positions, step.inv_freq, step.slots, step.k_cache, step.v_cache,
+                    step.pair_axis, step.adjacent, step.magnitude, step.kv_scale, step.k_scales, step.v_scales,
+                    step.q_rotated, stream)
+
+
 class SharedPrefixDecodeStep:
     """One decode step of one attention layer for a batch that shares prefixes:
     slot mapping, rotate-and-append (with ``q_weight`` or ``k_weight`` given, or
@@ -761,14 +773,7 @@ class SharedPrefixDecodeStep:
 
     def __call__(self, q, k_new, v_new, stream=None):
         slot_mapping(self.block_tables, self.context_lens, self.B, out=self.slots, stream=stream)
-        if self.norm:
-            norm_rope_append(q, k_new, v_new, self.positions, self.inv_freq, self.slots, self.k_cache, self.v_cache,
-                             self.q_weight, self.k_weight, self.eps, self.weight_offset, self.pair_axis, self.adjacent,
-                             self.magnitude, self.kv_scale, self.k_scales, self.v_scales, self.q_rotated, stream)
-        else:
-            rope_append(q, k_new, v_new, self.positions, self.inv_freq, self.slots, self.k_cache, self.v_cache,
-                        self.pair_axis, self.adjacent, self.magnitude, self.kv_scale, self.k_scales, self.v_scales,
-                        self.q_rotated, stream)
+        _append_of(self, q, k_new, v_new, stream)
         return shared_prefix_decode(self.q_rotated, self.k_cache, self.v_cache, self.block_tables, self.context_lens,
                                     self.group_start, self.prefix_blocks, self.max_prefix_blocks, self.softmax_scale,
                                     self.kv_scale, self.k_scales, self.v_scales, self.workspace, self.out, stream)
@@ -782,12 +787,13 @@ class SparseDecodeStep:
     it allocates nothing.  ``positions`` (int32 [S] or [axes, S]) is the
     caller's, read at every call like ``context_lens``.  For a cache that
     already holds tokens give the ``summary`` and ``exponents`` that describe
-    its full blocks.  Works as a step of ``StepGraph``."""
+    its full blocks.  With ``q_weight`` or ``k_weight`` given, or ``norm`` true, q
+    and k are normalised first.  Works as a step of ``StepGraph``."""
 
     def __init__(self, k_cache, v_cache, block_tables, context_lens, positions, inv_freq, num_q_heads,
                  top_k, sink_blocks=1, recent_blocks=2, softmax_scale=None, kv_scale=1.0, k_scales=None,
                  v_scales=None, pair_axis=None, adjacent=False, magnitude=1.0, summary=None,
-                 exponents=None):
+                 exponents=None, norm=False, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0):
         if (summary is None) != (exponents is None):
             raise ValueError("summary and exponents must both be given or both be None")
         self.k_cache, self.v_cache = k_cache, v_cache
@@ -799,6 +805,8 @@ class SparseDecodeStep:
         self.top_k, self.sink_blocks, self.recent_blocks = top_k, sink_blocks, recent_blocks
         self.softmax_scale = softmax_scale
         self.kv_scale, self.k_scales, self.v_scales = kv_scale, k_scales, v_scales
+        self.norm = norm or q_weight is not None or k_weight is not None
+        self.q_weight, self.k_weight, self.eps, self.weight_offset = q_weight, k_weight, eps, weight_offset
         if summary is None:
             summary, exponents = alloc_block_summary(k_cache)
         self.summary, self.exponents = summary, exponents
@@ -814,9 +822,7 @@ class SparseDecodeStep:
 
     def __call__(self, q, k_new, v_new, stream=None):
         slot_mapping(self.block_tables, self.context_lens, self.B, out=self.slots, stream=stream)
-        rope_append(q, k_new, v_new, self.positions, self.inv_freq, self.slots, self.k_cache,
-                    self.v_cache, self.pair_axis, self.adjacent, self.magnitude, self.kv_scale,
-                    self.k_scales, self.v_scales, self.q_rotated, stream)
+        _append_of(self, q, k_new, v_new, stream)
         block_summary(self.k_cache, self.slots, self.summary, self.exponents, stream)
         return sparse_attend(self.q_rotated, self.k_cache, self.v_cache, self.summary, self.exponents,
                              self.block_tables, self.context_lens, self.top_k, self.sink_blocks,

@@ -94,7 +94,8 @@ __device__ __forceinline__ bool query_range(const Args &a, int first, int end) {
 
 // Joins the parts of one row and writes it: by a warp whose lane p has part p's
 // (m, l), and whose last lane has those of `rest` (or of part 31, or none); part p's
-// o is at o + p * stride.  Fewer than 32 parts with a rest.
+// o is at o + p * stride.  Fewer than 32 parts with a rest.  Loads past the first-level
+// cache: a part may be of the kernel before the one before.
 template <int D>
 __device__ __forceinline__ void join_row(float2 ml, int parts, const float *o, int64_t stride, const float *rest,
                                          float v_scale, __nv_bfloat16 *out) {
@@ -114,9 +115,9 @@ __device__ __forceinline__ void join_row(float2 ml, int parts, const float *o, i
     auto add = [&](const float *from, float w) {
         float x[E];
         if constexpr (E == 4)
-            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(from + lane * E);
+            *reinterpret_cast<float4 *>(x) = __ldcg(reinterpret_cast<const float4 *>(from + lane * E));
         else
-            *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(from + lane * E);
+            *reinterpret_cast<float2 *>(x) = __ldcg(reinterpret_cast<const float2 *>(from + lane * E));
         if (w != 0.f)  // an empty part's accumulator may be anything
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] += w * x[i];

@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const int s = static_cast<int>(seq), hq = static_cast<int>(row - seq * a.num_q_heads);
     const int skip = sparse::shared_pages(a.prefix, s, min(a.context_lens[s], a.max_blocks * block_size), block_size);
     const int parts = skip ? live_parts((skip * block_size + kKeys - 1) / kKeys, a.prefix.parts) : 0;
-    const float2 ml = lane < parts ? a.prefix.ml[lane * a.prefix.rows + row]
-                                   : lane == 31 ? a.prefix.rest_ml[row] : make_float2(-INFINITY, 0.f);
+    const float2 ml = lane < parts ? __ldcg(a.prefix.ml + lane * a.prefix.rows + row)
+                                   : lane == 31 ? __ldcg(a.prefix.rest_ml + row) : make_float2(-INFINITY, 0.f);
     join_row<D>(ml, parts, a.prefix.o + row * D, a.prefix.rows * D, a.prefix.rest_o + row * D,
                 a.v_scales ? a.v_scales[hq / a.group] : v_scale, a.out + row * D);
 }
@@ -161,10 +161,12 @@ pa_status check_rows(int num_seqs, int num_tokens, int num_q_heads, int num_kv_h
                      int block_size, int max_blocks, pa_kv_dtype kv_dtype, float kv_scale, const float *k_scales,
                      const float *v_scales, float softmax_scale) {
     if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d is negative", num_tokens);
-    if (max_blocks > sparse::kMaxTableBlocks && static_cast<int64_t>(max_blocks) * block_size <= 0x7fffffffLL)
-        max_blocks = sparse::kMaxTableBlocks;  // the choice's own limit
-    pa_status st = sparse::check_select(num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, max_blocks, 1, 0, 1);
+    const bool wide = max_blocks > sparse::kMaxTableBlocks && static_cast<int64_t>(max_blocks) * block_size <= 0x7fffffffLL;
+    pa_status st = sparse::check_select(num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size,
+                                        wide ? sparse::kMaxTableBlocks : max_blocks, 1, 0, 1);  // the choice's own limit
     if (st != PA_OK) return st;
+    if (static_cast<int64_t>(max_blocks) * block_size > 0x7fff0000LL)  // room to count past the end in blocks of keys
+        return fail(PA_ERR_UNSUPPORTED, "tables for more than 2^31 - 2^16 tokens");
     if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3)
         return fail(PA_ERR_UNSUPPORTED, "kv_dtype %d", static_cast<int>(kv_dtype));
     if (!isfinite(softmax_scale) || softmax_scale <= 0.f)

@@ -36,6 +36,16 @@ CASES = [
     dict(rows=[4, 1], states=[3000, 2999], Hq=8, Hkv=2),
     dict(rows=[2] * 80, states=[(37 * i) % 90 for i in range(80)], Hq=4, Hkv=2, D=64),  # one part
     dict(rows=[130] * 5, states=[200, 0, 64, 65, 1], Hq=16, Hkv=8, D=64),
+    dict(rows=[2, 3], states=[40, 50], Hq=8, Hkv=2, extra=200000),            # far wider: few rows, a tile, two
+    dict(rows=[20, 3], states=[40, 50], Hq=8, Hkv=2, extra=200000),
+    dict(rows=[70, 3], states=[40, 50], Hq=8, Hkv=2, extra=200000),
+    # taken by length: ties, none, bad ends
+    dict(rows=[(7 * i) % 90 for i in range(45)], states=[(53 * i) % 200 for i in range(45)], Hq=8, Hkv=4, D=64),
+    dict(rows=[40] * 33, states=[64] * 33, Hq=6, Hkv=3, fp8=True, gap=3),
+    dict(rows=[0] * 30 + [70], states=[100] * 31, Hq=20, Hkv=5),
+    dict(rows=[70] + [0] * 250, states=[i for i in range(251)], Hq=16, Hkv=8, D=64),
+    dict(rows=[9] * 300, states=[(11 * i) % 70 for i in range(300)], Hq=2, Hkv=1, D=64),  # more than are sorted
+    dict(rows=[2] * 40, states=[(97 * i) % 300 for i in range(40)], Hq=16, Hkv=2, fp8=True, per_head=True),
 ]
 
 
@@ -208,3 +218,39 @@ def test_long_runs_give_the_same_bits_every_time(api, cuda_device, fp8, D):
         got = outs[0][s * rows:(s + 1) * rows].double().view(rows, Hkv, 3, D).permute(1, 2, 0, 3).flatten(1, 2)
         # the output's rounding, and one of each probability (2^-8 of it in bf16, 2^-11 in fp16)
         assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 if fp8 else 2.0 ** -8) * mass + 2.0 ** -14).all()
+
+
+def test_refused_rows_among_many(api, cuda_device):
+    """The same where sequences are taken by length."""
+    case = Cross(cuda_device, [30] * 20, [(31 * i) % 150 for i in range(20)], 16, 8, D=64)
+    want = case.expected()
+    out = torch.full_like(case.q, -7.0)
+    start = case.qs.clone()
+    start[8] = 5 * 30  # sequence 7 has none that ascend, 8 twice as many as may be
+    case.qs.copy_(start)
+    case.call(api, out=out, most=30)
+    torch.cuda.synchronize()
+    assert api.device_errors() == _lib.PA_DEVERR_BAD_CONTEXT
+    bad = slice(7 * 30, 9 * 30)
+    assert (out[bad] == -7).all()
+    keep = np.r_[0:7 * 30, 9 * 30:600]
+    within(out[torch.from_numpy(keep)], tuple(x[keep] for x in want))
+
+
+def test_as_many_sequences_as_there_may_be(api, cuda_device):
+    """65,535 sequences of up to three rows, against the decode kernel over each row's table."""
+    B, D, S = 16, 64, 65535
+    g = torch.Generator().manual_seed(9)
+    kc, vc = (torch.randn(200, 1, B, D, generator=g).to(torch.bfloat16).to(cuda_device) for _ in range(2))
+    rows = torch.randint(0, 4, (S,), generator=g)
+    start = torch.cat([torch.zeros(1, dtype=torch.int64), rows.cumsum(0)]).to(torch.int32).to(cuda_device)
+    T = int(start[-1])
+    q = torch.randn(T, 8, D, generator=g).to(torch.bfloat16).to(cuda_device)
+    tables = torch.randint(0, 200, (S, 5), generator=g).to(torch.int32).to(cuda_device)
+    lens = torch.randint(0, 5 * B + 1, (S,), generator=g).to(torch.int32).to(cuda_device)
+    got = api.cross_attention(q, kc, vc, tables, lens, start, 3)
+    seq = torch.repeat_interleave(torch.arange(S), rows).to(cuda_device)
+    pick = torch.randint(0, T, (500,), generator=g).to(cuda_device)
+    want = api.decode(q[pick].contiguous(), kc, vc, tables[seq[pick]].contiguous(), lens[seq[pick]].contiguous())
+    assert ((got[pick].float() - want.float()).abs() <= 2.0 ** -7 * (want.float().abs() + vc.float().abs().max())).all()
+    assert (got[lens[seq] == 0] == 0).all() and api.device_errors() == 0

@@ -189,3 +189,28 @@ def test_the_same_as_the_rotation_of_rows_that_need_no_norm(api, cuda_device):  
     want, k2, v2 = test_gpu_rope.Case.call(case, api)
     assert torch.equal(vc, v2) and (out.float() - want.float()).abs().max() <= 2.0 ** -7
     assert (out != want).float().mean() < 0.01 and (kc.float() - k2.float()).abs().max() <= 2.0 ** -7
+
+
+def test_a_sparse_step_of_normalised_rows(api, cuda_device):  # noqa: F811
+    """SparseDecodeStep with a norm: the same as its parts called one after the other."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(8)
+    S, Hq, Hkv, D, B, MB = 3, 8, 2, 128, 16, 10
+    kv = torch.randn(2, S * MB, Hkv, B, D, generator=g).to(bf).to(dev)
+    tables = torch.randperm(S * MB, generator=g).view(S, MB).to(torch.int32).to(dev)
+    lens = torch.tensor([150, 33, 80], dtype=torch.int32, device=dev)
+    freq = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).to(dev)
+    w = (1 + 0.2 * torch.randn(2, D, generator=g)).to(bf).to(dev)
+    q, k, v = (torch.randn(S, h, D, generator=g).to(bf).to(dev) for h in (Hq, Hkv, Hkv))
+    s, e = api.alloc_block_summary(kv[0])
+    api.block_summary(kv[0], torch.arange(B - 1, S * MB * B, B, dtype=torch.int32, device=dev), s, e)
+    k1, v1, k2, v2 = kv[0].clone(), kv[1].clone(), kv[0].clone(), kv[1].clone()
+    step = api.SparseDecodeStep(k1, v1, tables, lens, lens - 1, freq, Hq, 4, q_weight=w[0], k_weight=w[1], eps=1e-5,
+                                summary=s.clone(), exponents=e.clone())
+    out = step(q, k, v)
+    slots = api.slot_mapping(tables, lens, B)
+    rq = api.norm_rope_append(q, k, v, lens - 1, freq, slots, k2, v2, q_weight=w[0], k_weight=w[1], eps=1e-5)
+    api.block_summary(k2, slots, s, e)
+    assert torch.equal(out, api.sparse_attend(rq, k2, v2, s, e, tables, lens, 4)) and torch.equal(k1, k2) and torch.equal(v1, v2)
+    plain = api.SparseDecodeStep(kv[0].clone(), kv[1].clone(), tables, lens, lens - 1, freq, Hq, 4, summary=s.clone(), exponents=e.clone())
+    assert not plain.norm and not torch.equal(plain(q, k, v), out)

@@ -164,11 +164,14 @@ def test_groups_that_are_no_ranges_stay_in_bounds(api, cuda_device):
     api.device_errors()
 
 
-def test_captured_and_replayed(api, cuda_device):
+@pytest.mark.parametrize("apart", [0, 1])
+def test_captured_and_replayed(api, cuda_device, apart):
     """Two graphs of one workspace, replayed in turn on one stream, with lengths and queries that change."""
+    _lib.load().pa_test_set_share(0, apart)
     case = Shared(cuda_device, [(30, [40, 9, 3, 70]), (5, [9, 9])], 8, 2)
     want = case.expected()
     ws = api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, case.most)
+    assert ws is not None
     outs = [torch.empty_like(case.q) for _ in range(2)]
     case.call(api, workspace=ws, out=outs[0])
     torch.cuda.synchronize()
@@ -216,10 +219,13 @@ def test_on_another_stream_behind_its_work(api, cuda_device):
     within(out, want)
 
 
-def test_back_to_back_calls_that_feed_each_other(api, cuda_device):
+@pytest.mark.parametrize("apart", [0, 1])
+@pytest.mark.parametrize("groups", [[(50, [40, 9, 3, 70, 300]), (9, [5, 100])], [(9, [i % 113 for i in range(264)])]])
+def test_back_to_back_calls_that_feed_each_other(api, cuda_device, groups, apart):
     """Each call's output is the next one's query, in one workspace: bit for bit what the same calls give when each is
     waited for."""
-    case = Shared(cuda_device, [(50, [40, 9, 3, 70, 300]), (9, [5, 100])], 8, 2)
+    _lib.load().pa_test_set_share(0, apart)
+    case = Shared(cuda_device, groups, 8, 2)
     ws = api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, case.most)
 
     def chain(after):
@@ -239,10 +245,11 @@ def test_back_to_back_calls_that_feed_each_other(api, cuda_device):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
-def test_a_wait_that_runs_out(api, cuda_device):
+@pytest.mark.parametrize("apart", [0, 1])
+def test_a_wait_that_runs_out(api, cuda_device, apart):
     """The kernels give up, say so and end; the next call is right."""
-    case = Shared(cuda_device, [(30, [40, 9])], 8, 2)
     lib = _lib.load()
+    lib.pa_test_set_share(0, apart)
     for fp8 in (False, True):
         case = Shared(cuda_device, [(30, [40, 9])], 8, 2, fp8=fp8)
         assert lib.pa_test_set_wait(1_000_000, 1) == 0
@@ -311,3 +318,94 @@ def test_the_step_eager_and_captured(api, cuda_device, norm, fp8):
         l2 += 1
         p2 += 1
     assert torch.equal(k2.view(torch.uint8), k1.view(torch.uint8))
+
+
+def _launches(lib, *sizes):
+    return lib.pa_shared_prefix_launches(*sizes)
+
+
+def test_a_large_batch_by_its_sizes_alone(api, cuda_device):
+    """As the call's own rules launch it: few sequences of a short prefix by themselves, more of them joined by the rest's
+    kernel, long ones joined apart; sampled rows against the definition, and every one of them the same bits again."""
+    lib = _lib.load()
+    lib.pa_test_set_share(-1, -1)
+    g = torch.Generator(device=cuda_device).manual_seed(11)
+    seen = set()
+    for S, P, own, Hq, Hkv, D, B, fp8 in ((3, 20, 200, 8, 8, 128, 16, False), (40, 64, 90, 32, 8, 128, 16, False), (64, 520, 900, 16, 4, 128, 16, True),
+                                          (70, 300, 1500, 32, 8, 64, 32, False), (300, 40, 200, 32, 8, 128, 16, True)):
+        mine = -(-own // B)
+        NB = P + S * mine
+        kv = torch.randn(2, NB, Hkv, B, D, generator=g, device=cuda_device)
+        kv = (kv * 16).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else kv.to(torch.bfloat16)
+        q = torch.randn(S, Hq, D, generator=g, device=cuda_device).to(torch.bfloat16)
+        perm = torch.randperm(NB, generator=g, device=cuda_device).to(torch.int32)
+        tables = torch.cat([perm[:P].expand(S, P), perm[P:].view(S, mine)], 1).contiguous()
+        lens = (P * B + torch.randint(0, own + 1, (S,), generator=g, device=cuda_device)).to(torch.int32)
+        gs = torch.tensor([0, S], dtype=torch.int32, device=cuda_device)
+        pb = torch.tensor([P], dtype=torch.int32, device=cuda_device)
+        seen.add(_launches(lib, S, 1, Hq, Hkv, D, B, P + mine, P, int(fp8)))
+        call = lambda: api.shared_prefix_decode(q, kv[0], kv[1], tables, lens, gs, pb, P, kv_scale=1 / 16)  # noqa: E731
+        outs = [call() for _ in range(5)]
+        assert all(torch.equal(o, outs[0]) for o in outs) and api.device_errors() == 0
+        for s in (0, S // 2, S - 1):
+            n = int(lens[s])
+            k, v = ((c.view(torch.float8_e4m3fn).double() / 16 if fp8 else c.double())[tables[s].long()].transpose(0, 1).flatten(1, 2)[:, :n]
+                    for c in (kv[0], kv[1]))
+            p = torch.softmax(q[s].double().view(Hkv, -1, D) @ k.transpose(1, 2) * D ** -0.5, -1)
+            want, mass = (p @ v).view(Hq, D), (p @ v.abs()).view(Hq, D)
+            # the output's rounding and one of each probability
+            assert ((outs[0][s].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 if fp8 else 2.0 ** -8) * mass + 2.0 ** -14).all()
+    assert seen == {1, 2, 3}
+
+
+def test_a_cache_past_32_bits(api, cuda_device):
+    """A prefix and rows of its own at the end of a cache of 4.6 GB a side, appended there with a norm and read back by all
+    three operators."""
+    B, Hkv, D, Hq = 16, 8, 128, 32
+    NB = 2 ** 32 // (Hkv * B * D * 2) + 9000
+    kc = torch.zeros(NB, Hkv, B, D, dtype=torch.bfloat16, device=cuda_device)
+    vc = torch.zeros_like(kc)
+    g = torch.Generator().manual_seed(2)
+    T = 700
+    first = NB - 60
+    slots = (first * B + torch.arange(T)).to(torch.int32).to(cuda_device)
+    q, k, v = (torch.randn(T, h, D, generator=g).to(torch.bfloat16).to(cuda_device) for h in (Hq, Hkv, Hkv))
+    pos = torch.arange(T, dtype=torch.int32, device=cuda_device)
+    freq = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).to(cuda_device)
+    low_k, low_v = torch.zeros(44, Hkv, B, D, dtype=torch.bfloat16, device=cuda_device), torch.zeros(44, Hkv, B, D, dtype=torch.bfloat16, device=cuda_device)
+    rq = api.norm_rope_append(q, k, v, pos, freq, slots, kc, vc)
+    low = api.norm_rope_append(q, k, v, pos, freq, slots - first * B, low_k, low_v)
+    assert torch.equal(rq, low) and torch.equal(kc[first:first + 44], low_k) and torch.equal(vc[first:first + 44], low_v)
+    assert not kc[:first].any() and not kc[first + 44:].any()
+    tables = torch.arange(44, dtype=torch.int32, device=cuda_device).expand(3, 44).contiguous()
+    lens = torch.tensor([700, 650, 641], dtype=torch.int32, device=cuda_device)
+    gs = torch.tensor([0, 3], dtype=torch.int32, device=cuda_device)
+    pb = torch.tensor([40], dtype=torch.int32, device=cuda_device)
+    a = api.shared_prefix_decode(rq[:3].contiguous(), kc, vc, tables + first, lens, gs, pb, 40)
+    assert torch.equal(a, api.shared_prefix_decode(rq[:3].contiguous(), low_k, low_v, tables, lens, gs, pb, 40))
+    for rows in (2, 100):
+        qs = torch.tensor([0, rows, 2 * rows, 2 * rows + 1], dtype=torch.int32, device=cuda_device)
+        x = rq[:2 * rows + 1].contiguous()
+        a = api.cross_attention(x, kc, vc, tables + first, lens, qs, rows)
+        assert torch.equal(a, api.cross_attention(x, low_k, low_v, tables, lens, qs, rows)) and a.any()
+    assert api.device_errors() == 0
+
+
+def test_as_many_sequences_as_there_may_be(api, cuda_device):
+    """65,535 of them in groups of all sizes, against the same call without sharing."""
+    B, Hkv, D, S = 16, 1, 64, 65535
+    g = torch.Generator().manual_seed(6)
+    kc, vc = (torch.randn(200, Hkv, B, D, generator=g).to(torch.bfloat16).to(cuda_device) for _ in range(2))
+    q = torch.randn(S, 2, D, generator=g).to(torch.bfloat16).to(cuda_device)
+    start = torch.cat([torch.tensor([0, 0, 1]), torch.randint(2, S, (500,), generator=g).sort().values, torch.tensor([S])]).to(torch.int32).to(cuda_device)
+    G = start.numel() - 1
+    pb = torch.randint(0, 7, (G,), generator=g).to(torch.int32).to(cuda_device)
+    of = torch.searchsorted(start, torch.arange(S, dtype=torch.int32, device=cuda_device), right=True) - 1
+    tables = torch.randint(0, 200, (G, 8), generator=g).to(torch.int32).to(cuda_device)[of]
+    tables[:, 6:] = torch.randint(0, 200, (S, 2), generator=g).to(torch.int32).to(cuda_device)
+    lens = torch.randint(0, 8 * B + 1, (S,), generator=g).to(torch.int32).to(cuda_device)
+    a = api.shared_prefix_decode(q, kc, vc, tables, lens, start, pb, 6)
+    b = api.shared_prefix_decode(q, kc, vc, tables, lens, start, pb, 0)
+    # each within 2^-8 of its size for the output's rounding and 2^-8 of the values' for the probabilities'
+    assert ((a.float() - b.float()).abs() <= 2.0 ** -7 * (b.float().abs() + vc.float().abs().max())).all()
+    assert (a.float() - b.float()).abs().mean() < 2.0 ** -8 and (a[lens == 0] == 0).all() and api.device_errors() == 0

@@ -72,7 +72,7 @@ def _cross(lib, **kw):
 @pytest.mark.parametrize("call", [_shared, _cross])
 @pytest.mark.parametrize("kw,status", [
     (dict(S=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hkv=3), 1), (dict(Hq=64, Hkv=2), 2), (dict(D=96), 2), (dict(B=8), 2),
-    (dict(NB=0), 1), (dict(mb=0), 1), (dict(mb=1 << 28), 1), (dict(S=70000), 2), (dict(NB=1 << 27), 2), (dict(dt=3), 2),
+    (dict(NB=0), 1), (dict(mb=0), 1), (dict(mb=1 << 28), 1), (dict(mb=(1 << 27) - 1), 2), (dict(S=70000), 2), (dict(NB=1 << 27), 2), (dict(dt=3), 2),
     (dict(sm=0.0), 1), (dict(sm=-1.0), 1), (dict(sm=float("nan")), 1), (dict(sm=float("inf")), 1), (dict(ksc=FAKE), 1),
     (dict(ksc=FAKE, vsc=FAKE), 1), (dict(dt=1, kvs=0.0), 1), (dict(dt=1, ksc=FAKE), 1),
     (dict(q=None), 1), (dict(kc=None), 1), (dict(vc=None), 1), (dict(bt=None), 1), (dict(cl=None), 1), (dict(out=None), 1),
