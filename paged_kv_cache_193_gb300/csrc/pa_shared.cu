@@ -90,8 +90,10 @@ struct Suffix {
 // longest is known for one group, whose prefix is the same for all.  Long lists are
 // shared out while 512 CTAs hold them (128 rows of up to 2,000 tokens in bf16: 36.7 us
 // with one, 24.0 with two, 18.7 with four; of up to 1,000 in E4M3 11.9, 13.5, 14.4),
-// and to twice that when very long (512 rows of up to 4,000, longest first: 97 with
-// one, 85 with two).
+// and some more when very long (with a prefix of 8,192, of up to 4,000 tokens: 512 rows
+// 105.8 with one and 92.3 with two, 192 rows 53.2 with two and 48.4 with four, 128 rows
+// 37.6 with four and 44.3 with eight; 512 rows of up to 2,000, behind 32,768: 79.0 with
+// one and 91.7 with two).
 //
 // The join is made apart where an estimate of both ways says so: then the prefix's CTAs
 // may leave SMs to the rest's, and neither waits for the other (64 sequences, 32,768
@@ -111,11 +113,9 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     Suffix l{false, z.num_groups == 1 && z.num_seqs > 1 && z.num_seqs <= sparse::kMaxSorted && pages >= 16, 1, false, p.parts};
     if (steps >= 48)
         for (int s : {2, 4, 8})
-            if (rows * s <= 512) l.splits = s;
-    if (l.splits == 1 && l.longest_first && rows <= 512 && steps >= 96) l.splits = 2;
+            if (rows * s <= (steps >= 160 ? 512 + 1024 / s : 512)) l.splits = s;
 
     const int mode = g_apart.load(std::memory_order_relaxed);
-    const bool heads = rows >= 2048 && steps <= 16;
     // Half of the pages that the tables have room for, at 6.2 TB/s; many short lists go
     // a little slower.
     const double rest = z.num_seqs * (max_blocks - z.max_prefix_blocks) * 0.5 * z.page_bytes() / 6.2e6 * (pages < 64 ? 1.3 : 1.0);
@@ -135,8 +135,16 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
         }
     }
     l.apart = mode == 1 || (mode < 0 && least < together);
-    if (l.apart) return l;
-    return heads ? Suffix{true, false, 1, false, p.parts} : Suffix{false, l.longest_first, l.splits, false, p.parts};
+    // A warp to a head (1,600 rows of up to 200 and 300 tokens, E4M3, apart: 30.7 and 30.8 us,
+    // 32.5 and 35.7 with a CTA to each; of up to 200 and 300 in bf16 31.6 and 39.4, 33.5 and 37.8;
+    // 2,048 rows of up to 512, E4M3, 45.8 and 44.9, but joined by them 49.0 and 50.1).
+    if (rows >= 1536 && steps <= (l.apart ? 13 : 16)) {
+        l.heads = true;
+        l.longest_first = false;
+        l.splits = 1;
+    }
+    if (!l.apart) l.parts = p.parts;
+    return l;
 }
 
 constexpr int kJoinWarps = 8;
@@ -322,13 +330,12 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     b.stall_first_wait = stall_first_wait();
     b.longest_first = l.longest_first;
     b.prefix = {group_start, prefix_blocks, num_groups, max_prefix_blocks, l.parts, part_o, part_ml, num_rows, nullptr, nullptr};
-    if (l.heads)
-        return sparse::launch_any<sparse::kSuffixHeads>(head_dim, block_size, fp8, tk, tv, b, num_seqs, 1, 4, stream, group);
     if (l.apart) {
         b.prefix.rest_o = part_o + l.parts * num_rows * head_dim;
         b.prefix.rest_ml = part_ml + l.parts * num_rows;
     }
-    st = sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, l.splits, 4, stream, group);
+    st = l.heads ? sparse::launch_any<sparse::kSuffixHeads>(head_dim, block_size, fp8, tk, tv, b, num_seqs, 1, 4, stream, group)
+                 : sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, l.splits, 4, stream, group);
     if (st != PA_OK || !l.apart) return st;
     const dim3 grid(static_cast<unsigned>((num_rows + rows::kJoinWarps - 1) / rows::kJoinWarps));
     auto *join = head_dim == 128 ? rows::join_prefix_kernel<128> : rows::join_prefix_kernel<64>;

@@ -184,6 +184,10 @@ __device__ __forceinline__ int shared_pages(const Prefix &p, int s, int n, int b
     return s < __shfl_sync(0xffffffffu, end, count - 1) && pages > 0 && n / block_size >= pages ? pages : 0;
 }
 
+__device__ __forceinline__ bool grids_last() {
+    return blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z;
+}
+
 // kChoose: the cluster first chooses the row's pages, in the ring's memory.
 // kSuffix: launched when the prefix's kernel is on the SMs, which has waited for
 // those before it; only the join waits for that kernel.
@@ -640,7 +644,8 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         // A warp has a head to itself: its part joins the prefix's and leaves, through its
         // own share of the ring.
         static_assert(C::NP * (C::OSTR + rows::kMaxParts) * 4 <= SPW * C::STAGE, "a warp's output in its share of the ring");
-        if (a.prefix.parts) dependent_wait();
+        const bool apart = a.prefix.rest_o != nullptr;
+        if (a.prefix.parts && (!apart || grids_last())) dependent_wait();
         if (idle) return;
         __syncwarp();  // the ring's last stage has been read by all lanes
         float *osm = join + warp * (SPW * C::STAGE / 4);
@@ -666,8 +671,9 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
                 }
             }
         const int g = lane & (C::NP - 1);
-        const int parts = skip ? rows::live_parts((skip * BS + rows::kKeys - 1) / rows::kKeys, a.prefix.parts) : 0;
+        const int parts = skip && !apart ? rows::live_parts((skip * BS + rows::kKeys - 1) / rows::kKeys, a.prefix.parts) : 0;
         const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + h * a.group;
+        if (apart && lane < a.group) a.prefix.rest_ml[row + lane] = make_float2(top, sum);
         const float2 *ml = a.prefix.ml + row + min(g, a.group - 1);
         float *pw = osm + C::NP * C::OSTR;  // [parts][NP] the prefix's weights
         auto weight = [](float m, float l, float best) { return m == -INFINITY ? (l == 0.f ? 0.f : l) : fast_exp2(m - best); };
@@ -689,6 +695,11 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         const int quads = a.group * (D / 4);
         for (int i0 = 0; i0 < quads; i0 += 32) {
             const int i = min(i0 + lane, quads - 1), gi = i / (D / 4);
+            if (apart) {
+                if (i0 + lane < quads)
+                    *reinterpret_cast<float4 *>(a.prefix.rest_o + row * D + 4 * i) = *reinterpret_cast<const float4 *>(osm + gi * C::OSTR + i % (D / 4) * 4);
+                continue;
+            }
             const float f0 = __shfl_sync(0xffffffffu, mine, gi), scale = __shfl_sync(0xffffffffu, inv, gi);
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             auto add = [&](float f, const float4 &x) {
@@ -839,7 +850,7 @@ __global__ void __launch_bounds__(NW * 32, resident_ctas(D, BS, FP8, NT * 8) * 4
         }
     }
     if constexpr (SUFFIX)  // the grid is not to end before the one in front: its last CTA waits for that
-        if (a.prefix.rest_o && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z) dependent_wait();
+        if (a.prefix.rest_o && grids_last()) dependent_wait();
     if (ranks == 1) return;
 
     // ---- join the CTAs: each writes its share of the output -----------------------

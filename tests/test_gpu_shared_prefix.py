@@ -53,6 +53,10 @@ CASES = [
     dict(groups=[(5, [i % 120 for i in range(130)])], Hq=64, Hkv=4),
     dict(groups=[(40, [i % 101 for i in range(110)])], Hq=20, Hkv=5, fp8=True, per_head=True),
     dict(groups=[(9, [i % 90 for i in range(260)] + [-1, None, -100])], Hq=2, Hkv=2, D=64, fp8=True),
+    # the same beside the prefix, of more than eight pages
+    dict(groups=[(9, [(7 * i) % 190 for i in range(226)] + [-1, None, -100])], Hq=7, Hkv=7, D=64),
+    dict(groups=[(4, [(7 * i) % 120 for i in range(150)]), (0, [9]), (3, [(5 * i) % 160 for i in range(120)])], Hq=24, Hkv=6),
+    dict(groups=[(30, [(11 * i) % 400 for i in range(200)])], Hq=16, Hkv=8, fp8=True, per_head=True),
     # longest first, and several CTAs to a row
     dict(groups=[(12, [(37 * i) % 400 for i in range(30)])], Hq=8, Hkv=2),
     dict(groups=[(12, [(211 * i) % 1100 for i in range(9)] + [None, -3])], Hq=8, Hkv=2),
