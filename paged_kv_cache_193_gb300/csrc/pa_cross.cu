@@ -22,17 +22,20 @@ constexpr int kFewRows = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Args a, const float v_scale, __nv_bfloat16 *out) {
-    dependent_wait();
     const int lane = threadIdx.x & 31, s = blockIdx.y;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
     const int t = static_cast<int>(row / a.num_q_heads), hq = static_cast<int>(row - static_cast<int64_t>(t) * a.num_q_heads);
-    const int first = a.query_start[s], end = a.query_start[s + 1];
+    // What the call was given is there already: the kernel before has waited for those
+    // before it.
+    const int first = __ldcg(a.query_start + s), end = __ldcg(a.query_start + s + 1);
+    const int keys = min(max(__ldcg(a.lens + s), 0), a.max_blocks * a.block_size);
+    const float scale = a.v_scales ? __ldcg(a.v_scales + hq / a.group) : v_scale;
+    dependent_wait();
     if (!query_range(a, first, end) || t >= end - first) return;
-    const int keys = min(max(a.lens[s], 0), a.max_blocks * a.block_size);
     const int parts = live_parts((keys + kKeys - 1) / kKeys, a.parts);
     const int64_t at = (static_cast<int64_t>(first) + t) * a.num_q_heads + hq, rows = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
-    const float2 ml = lane < parts ? a.part_ml[lane * rows + at] : make_float2(-INFINITY, 0.f);
-    join_row<D>(ml, parts, a.part_o + at * D, rows * D, nullptr, a.v_scales ? a.v_scales[hq / a.group] : v_scale, out + at * D);
+    const float2 ml = lane < parts ? __ldcg(a.part_ml + lane * rows + at) : make_float2(-INFINITY, 0.f);
+    join_row<D>(ml, parts, a.part_o + at * D, rows * D, nullptr, scale, out + at * D);
 }
 
 // How a call is launched: by its sizes alone, which the workspace's size goes by too.

@@ -152,17 +152,24 @@ constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     join_prefix_kernel(const sparse::Args a, const int num_seqs, const int block_size, const float v_scale) {
-    dependent_wait();
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5), seq = row / a.num_q_heads;
-    if (seq >= num_seqs) return;
     const int s = static_cast<int>(seq), hq = static_cast<int>(row - seq * a.num_q_heads);
-    const int skip = sparse::shared_pages(a.prefix, s, min(a.context_lens[s], a.max_blocks * block_size), block_size);
-    const int parts = skip ? live_parts((skip * block_size + kKeys - 1) / kKeys, a.prefix.parts) : 0;
+    // What the call was given is there already: the prefix's kernel has waited for those
+    // before it.
+    int parts = 0;
+    float scale = v_scale;
+    if (seq < num_seqs) {
+        const int skip = sparse::shared_pages(a.prefix, s, min(__ldcg(a.context_lens + s), a.max_blocks * block_size), block_size);
+        if (skip) parts = live_parts((skip * block_size + kKeys - 1) / kKeys, a.prefix.parts);
+        if (a.v_scales) scale = __ldcg(a.v_scales + hq / a.group);
+    }
+    dependent_wait();
+    if (seq >= num_seqs) return;
     const float2 ml = lane < parts ? __ldcg(a.prefix.ml + lane * a.prefix.rows + row)
                                    : lane == 31 ? __ldcg(a.prefix.rest_ml + row) : make_float2(-INFINITY, 0.f);
     join_row<D>(ml, parts, a.prefix.o + row * D, a.prefix.rows * D, a.prefix.rest_o + row * D,
-                a.v_scales ? a.v_scales[hq / a.group] : v_scale, a.out + row * D);
+                scale, a.out + row * D);
 }
 
 pa_status check_rows(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
