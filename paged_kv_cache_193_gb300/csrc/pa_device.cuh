@@ -274,4 +274,17 @@ __device__ __forceinline__ uint2 quantize8_e4m3(const uint4 &bf16x8, float scale
     return make_uint2(words[0], words[1]);
 }
 
+// 16 bytes from global to shared memory, past the first-level cache.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_l1(uint32_t dst, const void *src) {  // through it
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 }  // namespace pa

@@ -22,10 +22,10 @@
 // three shuffles and no pass of its own over memory.
 //
 // Bound: memory.  Every q, k, v element is read once and written once: 8192
-// tokens of 32 query and 8 KV heads, 201 MB, take 35 us, where a library copy of
-// as much takes 32.5; few tokens are bound by the launch (one: 2.0 us) and by the
-// chain position, sine and cosine, row, so a thread's first row is on its way
-// while the angles are made.
+// tokens of 32 query and 8 KV heads, 201 MB, take 32.5 us, with NORM 34.3, where a
+// library copy of as much takes 32.5; few tokens are bound by the launch (one: 2.0
+// and 2.4 us) and by the chain position, sine and cosine, row, so a thread's first rows
+// are on their way while the angles are made.
 #include <algorithm>
 #include <cstring>
 #include <tuple>
@@ -43,9 +43,9 @@ namespace rope {
 // mathematical functions with correctly rounded last bit", 1991).  The borders,
 // and the codes, have at most five significant bits, so near them the lower 19
 // of a float's are almost all 0 or almost all 1.  Below 2^-126 and above 448 the
-// code is 0 or the largest, whatever the last place.  (8192 tokens, 32 + 8 heads:
-// 36.5 us with it, 39.5 with a division for every element; 256 tokens of 64 + 8
-// heads 3.7 and 4.0.)
+// code is 0 or the largest, whatever the last place.  (8192 tokens, 32 + 8 heads,
+// when all rows still came by registers: 36.5 us with it, 39.5 with a division for
+// every element; 256 tokens of 64 + 8 heads 3.7 and 4.0.)
 struct Divisor {
     float scale, inverse;
     // Of the 2^19 endings of a product, how many are in doubt, times 2^13: none when
@@ -103,9 +103,9 @@ __device__ __forceinline__ float2 mul2(float2 x, float2 y) { return __fmul2_rn(x
 __device__ __forceinline__ float2 add2(float2 x, float2 y) { return __fadd2_rn(x, y); }
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) { return __ffma2_rn(x, y, z); }
 
-// Where entry p of a table in shared memory lies: the first halves of all groups of
-// eight, then the second, so that lanes that read a group each find their 16 bytes
-// side by side.
+// Where entry p of a table in shared memory lies that is read in groups of eight: the
+// first halves of all groups, then the second, so that lanes that read a group each
+// find their 16 bytes side by side.
 template <int N>
 __device__ __forceinline__ constexpr int spread(int p) {
     return (p & 4) * (N / 8) + (p >> 3) * 4 + (p & 3);
@@ -157,10 +157,14 @@ __device__ __forceinline__ uint2 codes8(const float2 (&x)[4], const Divisor &by)
     return make_uint2(w[0], w[1]);
 }
 
-// A thread works on 16 elements of one head's row at a time: with pairs
-// (i, i + R/2) elements 8j .. 8j+7 and their partners, with adjacent pairs
-// elements 16j .. 16j+15; either way pairs 8j .. 8j+7, and two 16-byte loads.
-// Its j is the same for every row it takes.
+// A thread works on 16 elements of one head's row at a time, two vectors of eight:
+// with pairs (i, i + R/2) elements 8j .. 8j+7 and their partners, otherwise those
+// from 8j and from D/2 + 8j on, so that the lanes' 16 bytes lie side by side.  Its j is
+// the same for every row it takes.  Its first row comes by registers, the next by
+// shared memory, where two more are on their way while it works on one: 8192 tokens, 32 +
+// 8 heads, 32.5 us, in E4M3 31.3, with NORM 34.3; with the next row asked for when one is
+// done 34.5, 36.5 and 42.2; with one more on its way 33.7 and (NORM) 37.0, with three
+// 32.3 and 37.4, each at five CTAs to an SM.
 // NORM: none, with weights (or none) that all heads share, which are kept in shared
 // memory, or with each head's own.  CTAS: of the kernel to an SM, which caps its
 // registers.
@@ -179,28 +183,66 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
     const int rows = a.num_q_heads + 2 * a.num_kv_heads;
     const int row0 = blockIdx.y * a.rows_per_y;
     const int nrows = min(a.rows_per_y, rows - row0);
-    const bool turn = 8 * j < a.pairs;
-    // first elements of the thread's two vectors
-    const int rest = 2 * a.pairs + 16 * (j - a.pairs / 8);
-    const int ea = !turn ? rest : ADJACENT ? 16 * j : 8 * j;
-    const int eb = !turn || ADJACENT ? ea + 8 : a.pairs + 8 * j;
-    uint4 wa, wb;  // the thread's present piece
+    // which of the thread's two vectors are turned, and their first elements
+    const bool turn = ADJACENT ? 8 * j < 2 * a.pairs : 8 * j < a.pairs, turn_b = ADJACENT ? D / 2 + 8 * j < 2 * a.pairs : turn;
+    const int ea = ADJACENT || turn ? 8 * j : a.pairs + 8 * j;
+    const int eb = ADJACENT || !turn ? D / 2 + 8 * j : a.pairs + 8 * j;
+    // Pieces behind the first, kPieces - 1 of them on their way: each lands in the thread's
+    // own place, so no barrier is needed, and the one that is written to was used the turn before.
+    // With weights of each head's own these come beside their row.
+    constexpr int kPieces = NORM == kHeads ? 2 : 3;
+    __shared__ __align__(16) uint4 piece[kPieces][NORM == kHeads ? 4 : 2][kThreads];
+    uint4 ga, gb;  // the present one's weights
+    uint4 wa, wb;  // the present one
     const int first = threadIdx.x / VPR;
-    int tt = first / nrows, at = first - tt * nrows;  // token and row of the piece
+    int tt = first / nrows, at = first - tt * nrows;  // its token and row
+    int next_tt = tt, next_at = at;                   // of the next to be fetched
     int h;
     bool is_q, is_v;
-    auto load = [&]() {
+    auto what = [&](int at) {
         const int row = row0 + at;
-        const int64_t t = t0 + tt;
         is_q = row < a.num_q_heads;
         is_v = row >= a.num_q_heads + a.num_kv_heads;
         h = row - (is_q ? 0 : is_v ? a.num_q_heads + a.num_kv_heads : a.num_q_heads);
-        const __nv_bfloat16 *src = (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) +
-                                   static_cast<int64_t>(h) * D;
-        wa = *reinterpret_cast<const uint4 *>(src + (is_v ? 16 * j : ea));
-        wb = *reinterpret_cast<const uint4 *>(src + (is_v ? 16 * j + 8 : eb));
     };
-    if (tt < live) load();  // on its way while the angles are made
+    auto advance = [&](int &tt, int &at) {
+        for (at += kThreads / VPR; at >= nrows; at -= nrows) ++tt;
+    };
+    auto source = [&](int tt) {
+        const int64_t t = t0 + tt;
+        return (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + static_cast<int64_t>(h) * D;
+    };
+    auto weights = [&]() -> const __nv_bfloat16 * {  // the head's own, if any
+        const __nv_bfloat16 *weight = NORM != kHeads || is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+        return weight ? weight + h * (is_q ? a.q_weight_stride : a.k_weight_stride) : nullptr;
+    };
+    auto fetch = [&](int place) {
+        if (next_tt < live) {
+            what(next_at);
+            const __nv_bfloat16 *src = source(next_tt);
+            cp_async16(smem_addr(&piece[place][0][threadIdx.x]), src + (is_v ? 8 * j : ea));
+            cp_async16(smem_addr(&piece[place][1][threadIdx.x]), src + (is_v ? D / 2 + 8 * j : eb));
+            if (const __nv_bfloat16 *weight = weights()) {
+                cp_async16_l1(smem_addr(&piece[place][2][threadIdx.x]), weight + ea);
+                cp_async16_l1(smem_addr(&piece[place][3][threadIdx.x]), weight + eb);
+            }
+            advance(next_tt, next_at);
+        }
+        cp_async_commit();
+    };
+    if (tt < live) {  // on their way while the angles are made
+        what(at);
+        const __nv_bfloat16 *src = source(tt);
+        wa = *reinterpret_cast<const uint4 *>(src + (is_v ? 8 * j : ea));
+        wb = *reinterpret_cast<const uint4 *>(src + (is_v ? D / 2 + 8 * j : eb));
+        if (const __nv_bfloat16 *weight = weights()) {
+            ga = *reinterpret_cast<const uint4 *>(weight + ea);
+            gb = *reinterpret_cast<const uint4 *>(weight + eb);
+        }
+        advance(next_tt, next_at);
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces - 1; ++i) fetch(i);
 
     for (int x = threadIdx.x; x < live * a.pairs; x += kThreads) {
         const int tok = x / a.pairs, p = x - tok * a.pairs;
@@ -216,8 +258,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;
         float s, c;
         sincospif(half_turns, &s, &c);
-        cs[tok][spread<D / 2>(p)] = c * a.magnitude;
-        sn[tok][spread<D / 2>(p)] = s * a.magnitude;
+        const int to = ADJACENT ? p : spread<D / 2>(p);
+        cs[tok][to] = c * a.magnitude;
+        sn[tok][to] = s * a.magnitude;
     }
     if constexpr (NORM == kShared)
         for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
@@ -238,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         const int64_t t = t0 + tt;
         const int64_t row = row_s[tt];
         if (!is_q && row < 0) return;
-        const int da = is_v ? 16 * j : ea, db = is_v ? da + 8 : eb;
+        const int da = is_v ? 8 * j : ea, db = is_v ? D / 2 + 8 * j : eb;
         const int64_t dst = (is_q ? t * a.num_q_heads + h : row + h * a.block_size) * D;
         const bool rotate = turn && !is_v;
         if (!rotate && (!FP8 || is_q) && (!NORM || is_v)) {  // bits as they are
@@ -252,13 +295,6 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         unpack8(wb, xb);
         if constexpr (NORM) {
             if (!is_v) {
-                uint4 ra, rb;
-                const __nv_bfloat16 *weight = is_q ? a.q_weight : a.k_weight;
-                if (NORM == kHeads && weight) {
-                    weight += h * (is_q ? a.q_weight_stride : a.k_weight_stride);
-                    ra = *reinterpret_cast<const uint4 *>(weight + ea);
-                    rb = *reinterpret_cast<const uint4 *>(weight + eb);
-                }
                 float2 sum = mul2(xa[0], xa[0]), more = mul2(xb[0], xb[0]);
 #pragma unroll
                 for (int u = 1; u < 4; ++u) {
@@ -281,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
                     if constexpr (NORM == kShared) {
                         take8<D>(weight_s[is_q ? 0 : 1], e / 8, g);
                     } else {
-                        if (!weight) return;
+                        if (!(is_q ? a.q_weight : a.k_weight)) return;
                         unpack8(raw, g);
 #pragma unroll
                         for (int u = 0; u < 4; ++u) g[u] = add2(g[u], make_float2(a.weight_offset, a.weight_offset));
@@ -289,14 +325,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
 #pragma unroll
                     for (int u = 0; u < 4; ++u) x[u] = mul2(x[u], g[u]);
                 };
-                scale(xa, ea, ra);
-                scale(xb, eb, rb);
+                scale(xa, ea, ga);
+                scale(xb, eb, gb);
             }
         }
         if (rotate) {
-            float2 c[4], s[4];
-            take8<D / 2>(cs[tt], j, c);
-            take8<D / 2>(sn[tt], j, s);
             // (p, r) of a pair become (p c - r s, p s + r c): the inner product is rounded,
             // then a fused multiply-add
             auto turn2 = [](float2 &p, float2 &r, float2 co, float2 si) {
@@ -305,25 +338,31 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
                 r = fma2(x, si, w);
             };
             if constexpr (ADJACENT) {
-                auto turn4 = [&](float2 (&x)[4], int first) {  // pairs first .. first + 3 of c, s
+                auto turn4 = [&](float2 (&x)[4], int first) {  // by pairs first .. first + 3
+                    const float4 c = *reinterpret_cast<const float4 *>(cs[tt] + first), s = *reinterpret_cast<const float4 *>(sn[tt] + first);
 #pragma unroll
                     for (int u = 0; u < 4; u += 2) {
                         float2 p = make_float2(x[u].x, x[u + 1].x), r = make_float2(x[u].y, x[u + 1].y);
-                        turn2(p, r, c[(first + u) / 2], s[(first + u) / 2]);
+                        turn2(p, r, u ? make_float2(c.z, c.w) : make_float2(c.x, c.y), u ? make_float2(s.z, s.w) : make_float2(s.x, s.y));
                         x[u] = make_float2(p.x, r.x);
                         x[u + 1] = make_float2(p.y, r.y);
                     }
                 };
-                turn4(xa, 0);
-                turn4(xb, 4);
+                turn4(xa, 4 * j);
+                if (turn_b) turn4(xb, D / 4 + 4 * j);
             } else {
+                float2 c[4], s[4];
+                take8<D / 2>(cs[tt], j, c);
+                take8<D / 2>(sn[tt], j, s);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) turn2(xa[u], xb[u], c[u], s[u]);
             }
         }
+        // the bits as they are of a vector that nothing is done to
+        auto second = [&] { return ADJACENT && !NORM && !turn_b ? wb : pack8(xb); };
         if (is_q) {
             *reinterpret_cast<uint4 *>(a.q_out + dst + da) = pack8(xa);
-            *reinterpret_cast<uint4 *>(a.q_out + dst + db) = pack8(xb);
+            *reinterpret_cast<uint4 *>(a.q_out + dst + db) = second();
         } else if constexpr (FP8) {
             const float *scales = is_v ? a.v_scales : a.k_scales;
             const Divisor by = scales ? Divisor::of(scales[h]) : a.kv_scale;
@@ -333,38 +372,47 @@ __global__ void __launch_bounds__(kThreads, CTAS) append_kernel(const Args a) {
         } else {
             __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.k_cache);
             *reinterpret_cast<uint4 *>(to + dst + da) = pack8(xa);
-            *reinterpret_cast<uint4 *>(to + dst + db) = pack8(xb);
+            *reinterpret_cast<uint4 *>(to + dst + db) = second();
         }
     };
     dependent_release();
-    while (tt < live) {
+    for (int place = 0; tt < live; place = place + 1 == kPieces ? 0 : place + 1) {
+        what(at);
         store();
-        for (at += kThreads / VPR; at >= nrows; at -= nrows) ++tt;
-        if (tt < live) load();
+        advance(tt, at);
+        if (tt >= live) break;
+        cp_async_wait<kPieces - 2>();
+        wa = piece[place][0][threadIdx.x];
+        wb = piece[place][1][threadIdx.x];
+        if constexpr (NORM == kHeads) {
+            ga = piece[place][2][threadIdx.x];
+            gb = piece[place][3][threadIdx.x];
+        }
+        fetch(place == 0 ? kPieces - 1 : place - 1);
     }
 }
 
-// Grids of several waves want a fifth CTA on each SM at head dim 128 (8192
-// tokens, 32 + 8 heads: 34.8 against 38.9 us, E4M3 36.5 against 38.8), others the
-// registers (1000 tokens 5.6 against 6.4 us; 8192 of head dim 64, E4M3 cache, 21.1
-// against 22.6).
-static constexpr bool five_to_an_sm(int head_dim, int64_t ctas) { return head_dim == 128 && ctas > 4 * 152; }
+// Grids of several waves want a fifth CTA on each SM at head dim 128 (32 + 8 heads:
+// 700 tokens 3.8 against 4.4 us, 8192 32.5 against 33.1), others the registers (1000
+// tokens 4.6 against 5.2 us), and so does NORM, which would keep some of its values in
+// memory (8192 tokens 34.5 against 36.8 us, E4M3 34.5 against 40.2).
+static constexpr bool five_to_an_sm(int head_dim, bool norm, int64_t ctas) { return head_dim == 128 && !norm && ctas > 4 * 152; }
 
 // Tokens to a CTA: the least of tokens on the fullest SM plus, for each wave of
 // CTAs, its start (the angles) and its last CTA's own time, in units of 6144
-// elements.  Weights fitted to tiles of 1 to 8 over 400 to 7000 tokens of 24 to
-// 80 rows at both head dims: within 2% of the best tile.  (32 + 8 heads, 700
-// tokens: 4.3 us with 1 to a CTA, 5.3 with 2; 1500: 6.4 with 2, 8.5 with 4; 3500:
-// 16.8 with 5, 19.4 with 4; 8192: 34.7 with 6, 39.6 with 8.)
-static int tokens_per_cta(int num_tokens, int rows, int head_dim) {
+// elements.  Weights fitted to tiles of 1 to 8 over 256 to 8192 tokens of 48 and
+// 80 rows at both head dims, with and without NORM: 0.6% from the best tile on average,
+// 7% at worst.  (32 + 8 heads, 700 tokens: 3.9 us with 1 to a CTA, 5.1 with 4; 3500: 15.7
+// with 5, 19.5 with 1; NORM, 2500: 13.5 with 5, 15.2 with 4.)
+static int tokens_per_cta(int num_tokens, int rows, int head_dim, bool norm) {
     const double work = static_cast<double>(rows) * head_dim / 6144;
     int best = 1;
     double least = INFINITY;
     for (int tile = 1; tile <= kMaxTile; ++tile) {
         const int64_t ctas = (static_cast<int64_t>(num_tokens) + tile - 1) / tile;
-        const int64_t places = static_cast<int64_t>(five_to_an_sm(head_dim, ctas) ? 5 : 4) * 152;
+        const int64_t places = static_cast<int64_t>(five_to_an_sm(head_dim, norm, ctas) ? 5 : 4) * 152;
         const int64_t waves = (ctas + places - 1) / places, fullest = (ctas + 151) / 152 * tile;
-        const double cost = work * fullest + waves * (3.5 + 1.5 * work * tile);
+        const double cost = work * fullest + waves * (4.25 + 2 * work * tile);
         if (cost < least) {
             least = cost;
             best = tile;
@@ -375,8 +423,8 @@ static int tokens_per_cta(int num_tokens, int rows, int head_dim) {
 
 template <int D, bool FP8, bool ADJACENT, int NORM>
 static cudaError_t launch_ctas(const Args &a, dim3 grid, cudaStream_t stream) {
-    if constexpr (D == 128 && NORM != kHeads)
-        if (five_to_an_sm(D, static_cast<int64_t>(grid.x) * grid.y))
+    if constexpr (D == 128 && NORM == kNone)
+        if (five_to_an_sm(D, false, static_cast<int64_t>(grid.x) * grid.y))
             return launch_dependent(append_kernel<D, FP8, ADJACENT, NORM, 5>, grid, kThreads, 0, 0, stream, a);
     return launch_dependent(append_kernel<D, FP8, ADJACENT, NORM, 4>, grid, kThreads, 0, 0, stream, a);
 }
@@ -520,7 +568,7 @@ static pa_status append(const void *q, int64_t q_stride, const void *k, int64_t 
     a.eps = norm ? norm->eps : 0.f;
     const int kind = !norm ? kNone : a.q_weight_stride || a.k_weight_stride ? kHeads : kShared;
     const int rows = num_q_heads + 2 * num_kv_heads;
-    a.tile = tokens_per_cta(num_tokens, rows, head_dim);
+    a.tile = tokens_per_cta(num_tokens, rows, head_dim, norm != nullptr);
     const int at_once = kThreads / (head_dim / 16);  // rows of one pass of the CTA's threads
     // With few tokens a token's rows are shared out too, up to four CTAs to an SM.
     const int shares = std::max(1, std::min((rows + at_once - 1) / at_once, 4 * 152 / num_tokens));

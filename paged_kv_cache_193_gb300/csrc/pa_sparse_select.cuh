@@ -51,15 +51,6 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Four signed bytes of a word as fp16 pairs, even = bytes 0 and 2, odd = bytes
 // 1 and 3: 0x6400 | (x + 128) is the fp16 value kOffset + x, exactly.
 constexpr float kOffset = 1152.f;
