@@ -6,7 +6,8 @@
 // The rows' products are pa_rows.cu's.  With few rows to a batch a run of states
 // is cut into parts, so that all SMs read it, and the kernel here joins them:
 // a warp to a row, whose parts' weights are made once, a lane to a part.  Up to 16
-// rows of a KV head (one decoded token, some beams) go to pa_sparse_attend.cuh.
+// rows of a KV head (one decoded token, some beams) go to pa_sparse_attend.cuh (one row
+// to 1,500 states, 16 heads of 64 dims: 5.5 us, 8.7 by the rows kernel).
 #include <math.h>
 
 #include "pa_sparse_attend.cuh"

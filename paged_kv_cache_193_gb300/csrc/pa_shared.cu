@@ -17,7 +17,7 @@
 //
 // Bound: a prefix's products by the tensor cores and the chain of its softmax (64
 // sequences of 64 heads over 32,768 tokens: 69 GFLOP in 55 us alone), the rest by
-// memory.  Both, with up to 2,048 tokens more each: 90.6 us, where the decode that
+// memory.  Both, with up to 2,048 tokens more each: 78.2 us, where the decode that
 // reads every prefix again takes 570.
 #include <math.h>
 
@@ -97,8 +97,8 @@ struct Suffix {
 //
 // The join is made apart where an estimate of both ways says so: then the prefix's CTAs
 // may leave SMs to the rest's, and neither waits for the other (64 sequences, 32,768
-// tokens of prefix and up to 2,048 more: 99.5 us joined by the rest's kernel, 90.6
-// apart; 256 in E4M3, 2,048 and up to 512: 49.2 and 45.2; a few sequences of a few
+// tokens of prefix and up to 2,048 more: 101.2 us joined by the rest's kernel, 78.6
+// apart; 256 in E4M3, 2,048 and up to 512: 50.1 and 44.9; a few sequences of a few
 // thousand tokens take 2 us more apart).
 static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     const int64_t rows = z.num_seqs * z.num_kv_heads;
