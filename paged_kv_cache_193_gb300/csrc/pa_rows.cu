@@ -786,7 +786,8 @@ pa_status launch_rows(const void *q, const void *k_cache, const void *v_cache, i
     dim3 grid(1, a.num_kv_heads, seqs);
     int64_t x = ctas * a.parts;
     // A few waves or more of CTAs, of sequences that a CTA can sort: by length.
-    a.sorted = !a.group_start && seqs > 1 && seqs <= kMaxSorted && x * a.num_kv_heads * seqs > kSms;
+    a.sorted = !a.group_start && seqs > 1 && seqs <= kMaxSorted && x * a.num_kv_heads * seqs > kSms &&
+               ctas < 1 << 22;  // a sequence's place and CTAs share a word
     if (a.sorted) {
         const int64_t each = static_cast<int64_t>(tiles) * a.tile_tokens;
         x = std::min(ctas * seqs, a.num_tokens / each + seqs) * a.parts * a.num_kv_heads;

@@ -5,7 +5,7 @@ import torch
 
 from gpu_helpers import Guarded
 from paged_kv_cache_193_gb300 import _lib
-from rows_cases import Cross, within
+from rows_cases import Cross, Shared, within
 
 pytestmark = pytest.mark.gpu
 
@@ -254,3 +254,57 @@ def test_as_many_sequences_as_there_may_be(api, cuda_device):
     want = api.decode(q[pick].contiguous(), kc, vc, tables[seq[pick]].contiguous(), lens[seq[pick]].contiguous())
     assert ((got[pick].float() - want.float()).abs() <= 2.0 ** -7 * (want.float().abs() + vc.float().abs().max())).all()
     assert (got[lens[seq] == 0] == 0).all() and api.device_errors() == 0
+
+
+def test_calls_at_once(api, cuda_device):
+    """Cross attention in small and large tiles, shared prefixes joined in both ways, and a chunked prefill, each in a graph
+    and a workspace of its own, replayed on streams that run together: the same bits as one after the other."""
+    lib = _lib.load()
+    small = Cross(cuda_device, [(5 * i) % 30 for i in range(40)], [(53 * i) % 900 for i in range(40)], 16, 8)
+    large = Cross(cuda_device, [(7 * i) % 200 for i in range(25)], [(97 * i) % 600 for i in range(25)], 16, 4, D=64, fp8=True)
+    shared = [Shared(cuda_device, [(60, [(7 * i) % 90 for i in range(40)])], 8, 4, seed=i) for i in range(2)]
+    outs = [torch.zeros_like(c.q) for c in (small, large, *shared)]
+    T = 300
+    chunk = torch.tensor([0, T], dtype=torch.int32, device=cuda_device)
+    table = torch.arange(30, dtype=torch.int32, device=cuda_device).view(1, 30)
+    length = torch.tensor([400], dtype=torch.int32, device=cuda_device)
+    kv = torch.randn(2, 30, 4, 16, 64, device=cuda_device).to(torch.bfloat16)
+    qp = torch.randn(T, 16, 64, device=cuda_device).to(torch.bfloat16)
+    outs.append(torch.zeros_like(qp))
+    ws = [api.alloc_cross_workspace(c.q, c.pool.kd, c.bt, c.most) for c in (small, large)]
+
+    def prefix(i):
+        lib.pa_test_set_share(0, i)
+        try:
+            shared[i].call(api, out=outs[2 + i], workspace=ws[2 + i])
+        finally:
+            lib.pa_test_set_share(-1, -1)
+
+    lib.pa_test_set_share(0, -1)
+    ws += [api.alloc_shared_prefix_workspace(c.q, c.pool.kd, c.gs, c.most) for c in shared]
+    lib.pa_test_set_share(-1, -1)
+    calls = [lambda: small.call(api, out=outs[0], workspace=ws[0]), lambda: large.call(api, out=outs[1], workspace=ws[1]),
+             lambda: prefix(0), lambda: prefix(1),
+             lambda: api.prefill(qp, kv[0], kv[1], table, length, chunk, T, out=outs[4])]
+    for c in calls:
+        c()
+        torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    graphs, streams = [], [torch.cuda.Stream() for _ in calls]
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(10):
+                c()
+        graphs.append(g)
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    assert api.device_errors() == 0

@@ -214,3 +214,32 @@ def test_a_sparse_step_of_normalised_rows(api, cuda_device):  # noqa: F811
     assert torch.equal(out, api.sparse_attend(rq, k2, v2, s, e, tables, lens, 4)) and torch.equal(k1, k2) and torch.equal(v1, v2)
     plain = api.SparseDecodeStep(kv[0].clone(), kv[1].clone(), tables, lens, lens - 1, freq, Hq, 4, summary=s.clone(), exponents=e.clone())
     assert not plain.norm and not torch.equal(plain(q, k, v), out)
+
+
+@pytest.mark.parametrize("heads", [False, True])
+def test_weights_that_the_call_before_writes(api, cuda_device, heads):  # noqa: F811
+    """Each call's weights are the query rows that the one before has written, without a wait between: the same as with one."""
+    dev = cuda_device
+    g = torch.Generator().manual_seed(3)
+    T, H, D = 40, 24, 64
+    kc, vc = (torch.zeros(H, H, 16, D, dtype=bf, device=dev) for _ in range(2))
+    freq = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).to(dev)
+    pos = torch.arange(T, dtype=torch.int32, device=dev)
+    q, k, v = (torch.randn(T, H, D, generator=g).to(bf).to(dev) for _ in range(3))
+    bufs = [torch.ones(T, H, D, dtype=bf, device=dev) for _ in range(2)]
+
+    def chain(wait):
+        bufs[0].fill_(1)
+        for i in range(30):
+            w = bufs[i % 2][i] if heads else bufs[i % 2][i, i % H]
+            api.norm_rope_append(q, k, v, pos, freq, pos, kc, vc, q_weight=w, k_weight=w, out=bufs[1 - i % 2])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return bufs[0].clone(), kc.clone()
+
+    want = chain(True)
+    for _ in range(5):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
+    assert want[0].float().abs().max() < 2.0 ** 20 and api.device_errors() == 0
