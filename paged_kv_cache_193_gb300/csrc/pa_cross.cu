@@ -131,9 +131,9 @@ pa_status pa_cross_attention(const void *q, const void *k_cache, const void *v_c
         b.num_tokens = num_tokens;
         b.max_query_len = max_query_len;
         const int live = max_query_len * group;
-        const int splits = sparse::splits_of_four_warps(static_cast<int64_t>(num_seqs) * num_kv_heads, max_blocks_per_seq,
-                                                        sparse::resident_ctas(head_dim, block_size, fp8, live));
-        return sparse::launch_any<sparse::kRows>(head_dim, block_size, fp8, tk, tv, b, num_seqs, splits, 4, stream, live);
+        const sparse::Spread l = sparse::spread_of_tables(static_cast<int64_t>(num_seqs) * num_kv_heads, max_blocks_per_seq,
+                                                          sparse::resident_ctas(head_dim, block_size, fp8, live), live);
+        return sparse::launch_any<sparse::kRows>(head_dim, block_size, fp8, tk, tv, b, num_seqs, l.splits, l.warps, stream, live);
     }
     a.block_tables = block_tables;
     a.lens = state_lens;

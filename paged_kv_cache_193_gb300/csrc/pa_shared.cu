@@ -77,7 +77,7 @@ static size_t plan_bytes(const Sizes &z, const Plan &p) {
 struct Suffix {
     bool heads;          // a warp to a KV head, not a CTA
     bool longest_first;
-    int splits;          // CTAs to a sequence and KV head
+    int splits, warps;   // CTAs to a sequence and KV head, and warps of a CTA
     bool apart;          // the join is a kernel of its own, and the prefix has so many parts
     int parts;
 };
@@ -93,7 +93,10 @@ struct Suffix {
 // and some more when very long (with a prefix of 8,192, of up to 4,000 tokens: 512 rows
 // 105.8 with one and 92.3 with two, 192 rows 53.2 with two and 48.4 with four, 128 rows
 // 37.6 with four and 44.3 with eight; 512 rows of up to 2,000, behind 32,768: 79.0 with
-// one and 91.7 with two).
+// one and 91.7 with two).  Rows that find places at once as CTAs of eight warps have those
+// (the same prefix, of up to 1,000: 128 rows 20.7 us, 22.1 by two CTAs of four warps, 26.9 by
+// one; 32 rows in E4M3 19.5, 20.9, 21.3), and two of them to each of up to 2,000 (128 rows 29.1
+// us, 31.2 with one).
 //
 // The join is made apart where an estimate of both ways says so: then the prefix's CTAs
 // may leave SMs to the rest's, and neither waits for the other (64 sequences, 32,768
@@ -104,14 +107,21 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     const int64_t rows = z.num_seqs * z.num_kv_heads;
     // pages behind the prefix: of several groups, the shortest may be none
     const int pages = max_blocks - (p.shared && z.num_groups == 1 ? z.max_prefix_blocks : 0);
-    if (!p.shared)
-        return {false, false, sparse::splits_of_four_warps(rows, pages, sparse::resident_ctas(z.head_dim, z.block_size, z.fp8, z.group())),
-                false, 0};
+    const int resident = sparse::resident_ctas(z.head_dim, z.block_size, z.fp8, z.group());
+    if (!p.shared) {
+        const sparse::Spread s = sparse::spread_of_tables(rows, pages, resident, z.group());
+        return {false, false, s.splits, s.warps, false, 0};
+    }
     const int at_once = z.fp8 && z.block_size == 16 ? 2 : 1;  // pages of a warp's step
     const int steps = (pages + at_once - 1) / at_once;        // of one warp
-    if (rows >= 512 && pages <= 8) return {true, false, 1, false, p.parts};
-    Suffix l{false, z.num_groups == 1 && z.num_seqs > 1 && z.num_seqs <= sparse::kMaxSorted && pages >= 16, 1, false, p.parts};
-    if (steps >= 48)
+    if (rows >= 512 && pages <= 8) return {true, false, 1, 4, false, p.parts};
+    Suffix l{false, z.num_groups == 1 && z.num_seqs > 1 && z.num_seqs <= sparse::kMaxSorted && pages >= 16, 1, 4, false, p.parts};
+    const int64_t wide = sparse::places_of_eight_warps(resident, z.group());
+    if (rows <= wide && pages >= 12 && (steps < 160 || rows * 4 <= wide)) {
+        l.warps = 8;
+        for (int s : {2, 4, 8})
+            if (rows * s <= wide && steps >= 48 * s) l.splits = s;
+    } else if (steps >= 48)
         for (int s : {2, 4, 8})
             if (rows * s <= (steps >= 160 ? 512 + 1024 / s : 512)) l.splits = s;
 
@@ -142,6 +152,7 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
         l.heads = true;
         l.longest_first = false;
         l.splits = 1;
+        l.warps = 4;
     }
     if (!l.apart) l.parts = p.parts;
     return l;
@@ -342,7 +353,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
         b.prefix.rest_ml = part_ml + l.parts * num_rows;
     }
     st = l.heads ? sparse::launch_any<sparse::kSuffixHeads>(head_dim, block_size, fp8, tk, tv, b, num_seqs, 1, 4, stream, group)
-                 : sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, l.splits, 4, stream, group);
+                 : sparse::launch_any<sparse::kSuffix>(head_dim, block_size, fp8, tk, tv, b, num_seqs, l.splits, l.warps, stream, group);
     if (st != PA_OK || !l.apart) return st;
     const dim3 grid(static_cast<unsigned>((num_rows + rows::kJoinWarps - 1) / rows::kJoinWarps));
     auto *join = head_dim == 128 ? rows::join_prefix_kernel<128> : rows::join_prefix_kernel<64>;

@@ -935,6 +935,24 @@ inline int splits_of_four_warps(int64_t rows, int pages, int resident) {
     return splits;
 }
 
+// How whole tables are read: CTAs of a row and KV head, and warps of a CTA.  Eight
+// warps, two CTAs to an SM, where they find places at once: long lists of few rows
+// (one row and 8 heads, 1,000 pages: 22.5 us, 37.0 with four warps; 4 rows, 250 pages
+// 11.0 and 13.7; but 69 pages 8.2 and 7.4), and one CTA to a row where there are rows
+// for most places (128 rows of 19 pages 5.7 us, 6.7 with four; 256 of 94 24.2, 25.1 by
+// two CTAs of four).  Of more rows four CTAs to an SM hide more of each other (512 of 25
+// pages 15.7 and 14.1).  `live`: rows of queries.
+struct Spread {
+    int splits, warps;
+};
+inline int64_t places_of_eight_warps(int resident, int live) { return live <= 8 ? resident / 2 * kSms * 7 / 8 : 0; }
+inline Spread spread_of_tables(int64_t rows, int pages, int resident, int live) {
+    const int64_t places = places_of_eight_warps(resident, live);
+    if (rows * 8 <= places && pages >= 128) return {8, 8};
+    if (rows <= places && (rows >= 200 ? pages >= 16 : rows >= 96 && pages >= 16 && pages < 40)) return {1, 8};
+    return {splits_of_four_warps(rows, pages, resident), 4};
+}
+
 // Steps of a warp's ring.  Up to 8 query heads at head dim 128 one step, 32 KB
 // to a CTA and four CTAs to an SM, against two steps and three CTAs: 112 and 116
 // us over 64 sequences of 4K-32K tokens, 60 and 63 with E4M3 pages (512 clusters
@@ -976,12 +994,12 @@ static pa_status launch_attend(const CUtensorMap &tk, const CUtensorMap &tv, con
                       "sparse decode launch");
 }
 
-// Eight warps to a CTA: only for the kernel that chooses, up to 8 query heads.
+// Eight warps to a CTA: up to 8 query heads, and not for lists that come with the call.
 template <int D, int BS, bool FP8, int MODE>
 static pa_status launch_group(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int num_rows, int splits,
                               int warps, cudaStream_t stream, int live) {
     if (live > 8) return launch_attend<D, BS, FP8, 2, 4, MODE>(tk, tv, a, num_rows, splits, stream);
-    if constexpr (MODE == kChoose)
+    if constexpr (MODE == kChoose || MODE == kSuffix || MODE == kRows)
         if (warps == 8) return launch_attend<D, BS, FP8, 1, 8, MODE>(tk, tv, a, num_rows, splits, stream);
     return launch_attend<D, BS, FP8, 1, 4, MODE>(tk, tv, a, num_rows, splits, stream);
 }

@@ -45,6 +45,11 @@ CASES = [
     dict(rows=[0] * 30 + [70], states=[100] * 31, Hq=20, Hkv=5),
     dict(rows=[70] + [0] * 250, states=[i for i in range(251)], Hq=16, Hkv=8, D=64),
     dict(rows=[9] * 300, states=[(11 * i) % 70 for i in range(300)], Hq=2, Hkv=1, D=64),  # more than are sorted
+    # few rows, by eight warps: one CTA to a row, eight
+    dict(rows=[1] * 60, states=[(53 * i) % 400 for i in range(60)], Hq=8, Hkv=4),
+    dict(rows=[2, 1, 0] * 25, states=[(31 * i) % 300 for i in range(75)], Hq=12, Hkv=3, D=64, fp8=True, per_head=True),
+    dict(rows=[1, 3], states=[3000, 777], Hq=4, Hkv=2, D=64),
+    dict(rows=[2], states=[5001], Hq=8, Hkv=2, B=32, fp8=True),
     dict(rows=[2] * 40, states=[(97 * i) % 300 for i in range(40)], Hq=16, Hkv=2, fp8=True, per_head=True),
 ]
 

@@ -57,6 +57,11 @@ CASES = [
     dict(groups=[(9, [(7 * i) % 190 for i in range(226)] + [-1, None, -100])], Hq=7, Hkv=7, D=64),
     dict(groups=[(4, [(7 * i) % 120 for i in range(150)]), (0, [9]), (3, [(5 * i) % 160 for i in range(120)])], Hq=24, Hkv=6),
     dict(groups=[(30, [(11 * i) % 400 for i in range(200)])], Hq=16, Hkv=8, fp8=True, per_head=True),
+    # by eight warps: one CTA to a row, two, four
+    dict(groups=[(12, [(29 * i) % 380 for i in range(31)])], Hq=16, Hkv=4),
+    dict(groups=[(5, [(29 * i) % 300 for i in range(40)]), (9, [3, 70, 200, None, -5])], Hq=8, Hkv=4, D=64, B=32, fp8=True),
+    dict(groups=[(12, [1700, 20, 900, 0, 1])], Hq=8, Hkv=2, D=64),
+    dict(groups=[(12, [3500, 40, -7])], Hq=16, Hkv=2),
     # longest first, and several CTAs to a row
     dict(groups=[(12, [(37 * i) % 400 for i in range(30)])], Hq=8, Hkv=2),
     dict(groups=[(12, [(211 * i) % 1100 for i in range(9)] + [None, -3])], Hq=8, Hkv=2),
