@@ -44,12 +44,14 @@ struct Plan {
     int parts;
 };
 
-// A prefix's kernel costs some 6 us beside its work; up to 64 MB of prefixes, each
+// A prefix's kernel costs some 6 us beside its work; up to 100 MB of prefixes, each
 // counted for every sequence, are read faster than that, from the second-level cache
-// but for the first time (8 KV heads of 128 dims, microseconds with and without it:
-// 4 sequences of 1,024 tokens 10.0 and 7.4, 4 of 4,096 11.7 and 12.4, 32 of 1,024 in
-// E4M3 11.6 and 12.7, 16 of 1,024 in bf16 10.5 and 10.3).
-constexpr int64_t kShareBytes = 64000000;
+// but for the first time, and to twice that where a group has fewer than eight sequences
+// (8 KV heads of 128 dims, microseconds shared and not: 4 sequences of 1,024 tokens 10.2 and
+// 7.7, 16 of 1,024 11.0 and 10.4, 16 of 2,048 12.1 and 14.3, 4 of 8,192 18.6 and 16.6, 4 of
+// 16,384 23.2 and 25.5; in E4M3 32 of 1,024 14.5 and 11.6, 32 of 2,048 15.8 and 17.5, 4 of 16,384
+// 24.3 and 20.1).
+constexpr int64_t kShareBytes = 100000000;
 static std::atomic<int64_t> g_share_bytes{kShareBytes};  // pa_test_set_share
 static std::atomic<int> g_apart{-1};
 
@@ -60,7 +62,7 @@ static int prefix_blocks_of(const Sizes &z) {
 static Plan plan(const Sizes &z) {
     const double all = z.num_seqs * z.max_prefix_blocks * z.page_bytes();
     if (z.num_groups == 0 || z.max_prefix_blocks == 0 ||
-        all <= static_cast<double>(g_share_bytes.load(std::memory_order_relaxed)))
+        all <= static_cast<double>(g_share_bytes.load(std::memory_order_relaxed)) * (z.num_seqs < 8 * static_cast<int64_t>(z.num_groups) ? 2 : 1))
         return {false, 0, 0, 0};
     const int tiles = z.num_seqs <= static_cast<int64_t>(tile_rows(1) / z.group()) * z.num_groups ? 1 : 2;
     const int64_t ctas = std::min(tile_ctas(z.num_seqs, z.group(), tiles) + z.num_groups - 1, z.num_seqs);

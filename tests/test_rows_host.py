@@ -112,8 +112,10 @@ def test_workspace_sizes(lib):
     assert size(4, 0, 8, 2, 128, 16, 32) == 0 == size(4, 1, 8, 2, 128, 16, 0)  # nothing shared
     assert size(4, 1, 9, 2, 128, 16, 32) == 0                                  # the call refuses such heads
     assert size(4, 1, 32, 8, 128, 16, 63) == 0                                 # little to share: 16.5 MB
-    assert size(15, 1, 32, 8, 128, 16, 65) == 0 != size(16, 1, 32, 8, 128, 16, 62)  # 63.9 and 65.0 MB
-    assert size(31, 1, 32, 8, 128, 16, 62, 1) == 0 != size(32, 1, 32, 8, 128, 16, 62, 1)  # E4M3: half of that each
+    assert size(23, 1, 32, 8, 128, 16, 65) == 0 != size(24, 1, 32, 8, 128, 16, 65)  # 98.0 and 102.2 MB
+    assert size(46, 1, 32, 8, 128, 16, 65, 1) == 0 != size(48, 1, 32, 8, 128, 16, 65, 1)  # E4M3: half of that each
+    assert size(7, 1, 32, 8, 128, 16, 435) == 0 != size(7, 1, 32, 8, 128, 16, 436)  # few sequences: 199.6 and 200.02 MB
+    assert size(8, 1, 32, 8, 128, 16, 435) != 0 == size(8, 2, 32, 8, 128, 16, 381)  # eight to a group, four: 228 and 199.8 MB
     try:
         assert lib.pa_test_set_share(0, -1) == 0
         for n in (1, 4, 256, 65535):
