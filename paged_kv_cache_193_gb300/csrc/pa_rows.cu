@@ -748,7 +748,8 @@ double join_time(int parts, int head_dim, int64_t num_rows) {
 // remains of it at the end has its SM to itself; else in their order, and the last CTA
 // is half done when the others end.  (32 sequences of up to 4,000 states, 5 rows of 32 / 8
 // heads: 61.3 us with one part, 50.2 with two, 57.2 with three; 100 sequences 131 with
-// one, 165 with two; 8 sequences 53 with one, 20.8 with five, 24.1 with eight.)
+// one, 165 with two; 8 sequences 53 with one, 20.8 with five, 24.1 with eight; 26 of up to 452
+// states, 6 rows, 11.5 with one, 15.0 with two.)
 int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_rows, bool even, bool direct) {
     const int64_t places = tiles == 1 ? 2 * kSms : kSms;
     int best = 1;
@@ -763,7 +764,7 @@ int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_
             cost = std::max(start + (one - start) * (tiles == 1 ? 0.65 : 1.0), (n * start + work * 0.7) / places);
         else
             cost = std::max(one, (n * start + work * 0.6) / places + one / 2);
-        if (parts > 1 || !direct) cost += join_time(parts, head_dim, num_rows);
+        if (parts > 1 || !direct) cost += join_time(parts, head_dim, num_rows) + (direct ? 3.0 : 0.0);  // a kernel more
         if (cost < least) {
             least = cost;
             best = parts;

@@ -108,7 +108,8 @@ struct Suffix {
 static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     const int64_t rows = z.num_seqs * z.num_kv_heads;
     // pages behind the prefix: of several groups, the shortest may be none
-    const int pages = max_blocks - (p.shared && z.num_groups == 1 ? z.max_prefix_blocks : 0);
+    const int own = std::max(max_blocks - z.max_prefix_blocks, 0);
+    const int pages = p.shared && z.num_groups == 1 ? own : max_blocks;
     const int resident = sparse::resident_ctas(z.head_dim, z.block_size, z.fp8, z.group());
     if (!p.shared) {
         const sparse::Spread s = sparse::spread_of_tables(rows, pages, resident, z.group());
@@ -130,7 +131,7 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     const int mode = g_apart.load(std::memory_order_relaxed);
     // Half of the pages that the tables have room for, at 6.2 TB/s; many short lists go
     // a little slower.
-    const double rest = z.num_seqs * (max_blocks - z.max_prefix_blocks) * 0.5 * z.page_bytes() / 6.2e6 * (pages < 64 ? 1.3 : 1.0);
+    const double rest = z.num_seqs * own * 0.5 * z.page_bytes() / 6.2e6 * (pages < 64 ? 1.3 : 1.0);
     const int64_t ctas = p.ctas * z.num_kv_heads, places = (p.tiles == 1 ? 2 : 1) * kSms;
     const int blocks = prefix_blocks_of(z);
     const double average = z.num_groups == 1 ? 1.0 : 0.6;  // of runs of unlike lengths, beside the longest
@@ -274,8 +275,8 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     if (st != PA_OK) return st;
     if (num_groups < 0 || max_prefix_blocks < 0)
         return fail(PA_ERR_INVALID_ARG, "bad size (num_groups=%d, max_prefix_blocks=%d)", num_groups, max_prefix_blocks);
-    if (max_prefix_blocks > max_blocks_per_seq)
-        return fail(PA_ERR_INVALID_ARG, "max_prefix_blocks %d exceeds the tables' width %d", max_prefix_blocks, max_blocks_per_seq);
+    if (static_cast<int64_t>(max_prefix_blocks) * block_size > 0x7fffffffLL)
+        return fail(PA_ERR_UNSUPPORTED, "prefixes of more than 2^31 - 1 tokens");
     if (num_groups > num_seqs)
         return fail(PA_ERR_INVALID_ARG, "%d groups of %d sequences", num_groups, num_seqs);
     if (num_seqs == 0) return PA_OK;
@@ -320,7 +321,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
         a.group_start = group_start;
         a.prefix_blocks = prefix_blocks;
         a.num_groups = num_groups;
-        a.max_prefix_blocks = max_prefix_blocks;
+        a.max_prefix_blocks = std::min(max_prefix_blocks, max_blocks_per_seq);
         a.err = err;
         st = rows::launch_rows(q, k_cache, v_cache, head_dim, fp8, a, p.tiles, p.ctas, 1, stream);
         if (st != PA_OK) return st;
@@ -349,7 +350,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     b.wait_limit_ns = wait_limit_ns();
     b.stall_first_wait = stall_first_wait();
     b.longest_first = l.longest_first;
-    b.prefix = {group_start, prefix_blocks, num_groups, max_prefix_blocks, l.parts, part_o, part_ml, num_rows, nullptr, nullptr};
+    b.prefix = {group_start, prefix_blocks, num_groups, std::min(max_prefix_blocks, max_blocks_per_seq), l.parts, part_o, part_ml, num_rows, nullptr, nullptr};
     if (l.apart) {
         b.prefix.rest_o = part_o + l.parts * num_rows * head_dim;
         b.prefix.rest_ml = part_ml + l.parts * num_rows;

@@ -329,6 +329,20 @@ def test_the_step_eager_and_captured(api, cuda_device, norm, fp8):
     assert torch.equal(k2.view(torch.uint8), k1.view(torch.uint8))
 
 
+@pytest.mark.parametrize("apart", [0, 1])
+def test_a_bound_past_the_tables_width(api, cuda_device, apart):
+    """Prefixes that no sequence holds to their end: the tables are narrower than the longest one."""
+    _lib.load().pa_test_set_share(0, apart)
+    case = Shared(cuda_device, [(40, [-300, -17, -639]), (9, [5, 100, 0]), (30, [-1])], 8, 2)
+    assert case.bt.shape[1] < case.most
+    for most in (case.most, 1000, 100000):
+        ws = api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, most)
+        within(case.call(api, max_prefix_blocks=most, workspace=ws), case.expected())
+    case.pb.fill_(2 ** 31 - 1)  # no sequence has so much: each by itself
+    within(case.call(api, max_prefix_blocks=1000), case.expected())
+    assert api.device_errors() == 0
+
+
 def _launches(lib, *sizes):
     return lib.pa_shared_prefix_launches(*sizes)
 

@@ -86,7 +86,7 @@ def test_both_attentions_reject_on_host(lib, call, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(G=-1), 1), (dict(G=9), 1), (dict(mp=-1), 1), (dict(mp=4097), 1), (dict(gs=None), 1), (dict(pb=None), 1),
+    (dict(G=-1), 1), (dict(G=9), 1), (dict(mp=-1), 1), (dict(mp=1 << 28), 2), (dict(gs=None), 1), (dict(pb=None), 1),
 ])
 def test_shared_prefix_rejects_on_host(lib, kw, status):
     assert _shared(lib, **kw) == status
