@@ -743,7 +743,7 @@ double join_time(int parts, int head_dim, int64_t num_rows) {
 }
 
 // Least of an estimated time.  Runs of one length (`even`) end in whole waves.  Of
-// others 0.6 or 0.7 of the longest is taken for the average, and the work is shared out:
+// others 0.6 or 0.65 of the longest is taken for the average, and the work is shared out:
 // where one part needs no joining (cross attention) the longest run first, and what
 // remains of it at the end has its SM to itself; else in their order, and the last CTA
 // is half done when the others end.  (32 sequences of up to 4,000 states, 5 rows of 32 / 8
@@ -761,7 +761,7 @@ int choose_parts(int64_t ctas, int blocks, int tiles, int head_dim, int64_t num_
         if (even)
             cost = std::ceil(n / places) * one;
         else if (direct)
-            cost = std::max(start + (one - start) * (tiles == 1 ? 0.65 : 1.0), (n * start + work * 0.7) / places);
+            cost = std::max(start + (one - start) * (tiles == 1 ? 0.65 : 1.0), (n * start + work * 0.65) / places);
         else
             cost = std::max(one, (n * start + work * 0.6) / places + one / 2);
         if (parts > 1 || !direct) cost += join_time(parts, head_dim, num_rows) + (direct ? 3.0 : 0.0);  // a kernel more
