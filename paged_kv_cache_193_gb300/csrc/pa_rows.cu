@@ -24,8 +24,9 @@
 // Bound: by the tensor cores and, below their rate, by the chain of a block: scores,
 // maximum, powers, product, two blocks of a tile in flight.  16 x 512 rows of 32 / 8 heads
 // of 128 dims over 2,048 keys: 212 us, 1,297 TFLOP/s, 0.66 of a library product's rate and
-// 0.76 within the loop; a CTA spends some 4 us on its start (lengths, table, first page) and
-// its end.  E4M3 pages: 1.1 us a block of two tiles where bf16 takes 0.85, for the widening
+// 0.76 within the loop; a CTA spends some 6.5 us beside it: 1.3 on finding its rows, 0.8 on
+// barriers and tensor memory, 1.3 until its queries are there, 1.0 until the first scores are,
+// 1.5 on its stores, and 0.5 until the next one starts.  E4M3 pages: 1.1 us a block of two tiles where bf16 takes 0.85, for the widening
 // and for 128 registers to a thread.  Small tiles are bound by the copies: 32 x 5 rows over
 // up to 4,000 keys, 265 MB, 49.5 us.
 //
@@ -177,7 +178,8 @@ __device__ __forceinline__ bool longest_unit(const Args &a, int unit, void *room
         w.tokens = start[s + 1] - w.token0;
         w.keys = len[s];
     }
-    __syncthreads();  // the room is used again
+    fence_proxy_async_smem();  // copies land in the room next
+    __syncthreads();
     return s >= 0;
 }
 
