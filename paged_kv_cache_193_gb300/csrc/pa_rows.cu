@@ -26,9 +26,9 @@
 // of 128 dims over 2,048 keys: 212 us, 1,297 TFLOP/s, 0.66 of a library product's rate and
 // 0.76 within the loop; a CTA spends some 6.5 us beside it: 1.3 on finding its rows, 0.8 on
 // barriers and tensor memory, 1.3 until its queries are there, 1.0 until the first scores are,
-// 1.5 on its stores, and 0.5 until the next one starts.  E4M3 pages: 1.1 us a block of two tiles where bf16 takes 0.85, for the widening
-// and for 128 registers to a thread.  Small tiles are bound by the copies: 32 x 5 rows over
-// up to 4,000 keys, 265 MB, 49.5 us.
+// 1.5 on its stores, and 0.5 until the next one starts.  E4M3 pages: 1.1 us a block of two
+// tiles where bf16 takes 0.85, for the widening and for 128 registers to a thread.  Small
+// tiles are bound by the copies: 32 x 5 rows over up to 4,000 keys, 265 MB, 49.5 us.
 //
 // Every wait is bounded (2 s unless a test sets another limit).
 #include <cudaTypedefs.h>
