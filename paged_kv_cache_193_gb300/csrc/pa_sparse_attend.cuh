@@ -153,7 +153,10 @@ __device__ __forceinline__ int longest_row(const int32_t *lens, int n, int z, vo
     if (i < n && before == z) len[n] = i;
     __syncthreads();
     const int row = len[n];
-    __syncthreads();  // the room is used again
+    // The room is used again, by page copies too: a barrier alone does not order these
+    // accesses before what the copies write.
+    fence_proxy_async_smem();
+    __syncthreads();
     return row;
 }
 

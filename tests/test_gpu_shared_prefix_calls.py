@@ -1,0 +1,54 @@
+"""Shared-prefix decode as it is called by a server: chains of calls, tables wider than what they hold, bounds that say
+little, groups that are none."""
+import pytest
+import torch
+
+from paged_kv_cache_193_gb300 import _lib
+from rows_cases import Shared, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api(cuda_device):
+    from paged_kv_cache_193_gb300 import api as a
+    a._lib_handle()
+    return a
+
+
+@pytest.fixture(autouse=True)
+def every_prefix_is_shared():
+    """Small batches would be attended to sequence by sequence."""
+    lib = _lib.load()
+    assert lib.pa_test_set_share(0, -1) == 0
+    yield
+    assert lib.pa_test_set_share(-1, -1) == 0
+
+
+@pytest.mark.parametrize("apart", [0, 1])
+@pytest.mark.parametrize("S,fp8", [(2, False), (9, True), (128, False)])
+def test_longest_first_in_calls_that_feed_each_other(api, cuda_device, S, fp8, apart):
+    """One group of 2 to 128 sequences with 16 pages of their own and more: CTAs rank the lengths where the first pages land
+    next.  Each call's output is the next one's query; bit for bit what the same calls give when each is waited for, and
+    the first of them the definition."""
+    _lib.load().pa_test_set_share(0, apart)
+    case = Shared(cuda_device, [(12, [(53 * i) % 290 for i in range(S - 1)] + [16 * 18])], 8, 2, fp8=fp8)
+    ws = api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, case.most)
+
+    def chain(after):
+        x, got = case.q.clone(), []
+        for _ in range(40):
+            y = case.call(api, q=x, workspace=ws)
+            after()
+            x = (y * 3).contiguous()
+            after()
+            got.append(y)
+        return got
+
+    want = chain(torch.cuda.synchronize)
+    within(want[0], case.expected())
+    for _ in range(5):
+        got = chain(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert api.device_errors() == 0
