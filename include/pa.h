@@ -593,7 +593,8 @@ pa_status pa_norm_rope_append(const void *q, int64_t q_stride, const void *k, in
  *                 table row.
  *   max_prefix_blocks  a bound for the launch: of longer prefixes so many blocks
  *                 are taken together, the others for each sequence.  More
- *                 than max_blocks_per_seq counts as that.
+ *                 than max_blocks_per_seq counts as that; the workspace may be
+ *                 sized by either.
  *   num_groups <= num_seqs; 0 groups, or max_prefix_blocks 0: nothing is shared,
  *                 and group_start and prefix_blocks may be NULL.
  *   workspace     pa_shared_prefix_workspace_size bytes (0: NULL will do),

@@ -75,6 +75,19 @@ static size_t plan_bytes(const Sizes &z, const Plan &p) {
     return p.shared ? workspace_bytes(p.parts + 1, z.rows(), z.head_dim) : 0;
 }
 
+// A call's sizes, and how it takes its prefixes, where the tables' width is known: no prefix
+// is longer than that.  The workspace may have been sized by the bound as it was given or
+// by the width, so there are no more parts than either has room for.
+static Sizes within_tables(Sizes z, int max_blocks) {
+    z.max_prefix_blocks = std::min(z.max_prefix_blocks, max_blocks);
+    return z;
+}
+static Plan plan(const Sizes &z, int max_blocks) {
+    Plan p = plan(within_tables(z, max_blocks));
+    if (p.shared && z.max_prefix_blocks > max_blocks) p.parts = std::min(p.parts, plan(z).parts);  // the longer are shared too
+    return p;
+}
+
 // How the rest is launched.
 struct Suffix {
     bool heads;          // a warp to a KV head, not a CTA
@@ -259,7 +272,8 @@ int pa_shared_prefix_launches(int num_seqs, int num_groups, int num_q_heads, int
                                         kv_dtype) == 0)
         return 1;
     const rows::Sizes z{num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks, kv_dtype == PA_KV_FP8_E4M3};
-    return rows::suffix_launch(z, rows::plan(z), max_blocks_per_seq).apart ? 3 : 2;
+    const rows::Plan p = rows::plan(z, max_blocks_per_seq);
+    return !p.shared ? 1 : rows::suffix_launch(rows::within_tables(z, max_blocks_per_seq), p, max_blocks_per_seq).apart ? 3 : 2;
 }
 
 pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
@@ -283,8 +297,9 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     st = rows::check_row_pointers(q, k_cache, v_cache, block_tables, context_lens, out, num_seqs, num_q_heads, head_dim);
     if (st != PA_OK) return st;
     const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
-    const rows::Sizes z{num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks, fp8};
-    const rows::Plan p = rows::plan(z);
+    const rows::Sizes given{num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, block_size, max_prefix_blocks, fp8};
+    const rows::Plan p = rows::plan(given, max_blocks_per_seq);
+    const rows::Sizes z = rows::within_tables(given, max_blocks_per_seq);
     const rows::Suffix l = rows::suffix_launch(z, p, max_blocks_per_seq);
     const int64_t num_rows = z.rows();
     if (p.shared) {
@@ -321,7 +336,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
         a.group_start = group_start;
         a.prefix_blocks = prefix_blocks;
         a.num_groups = num_groups;
-        a.max_prefix_blocks = std::min(max_prefix_blocks, max_blocks_per_seq);
+        a.max_prefix_blocks = z.max_prefix_blocks;
         a.err = err;
         st = rows::launch_rows(q, k_cache, v_cache, head_dim, fp8, a, p.tiles, p.ctas, 1, stream);
         if (st != PA_OK) return st;
@@ -350,7 +365,7 @@ pa_status pa_shared_prefix_decode(const void *q, const void *k_cache, const void
     b.wait_limit_ns = wait_limit_ns();
     b.stall_first_wait = stall_first_wait();
     b.longest_first = l.longest_first;
-    b.prefix = {group_start, prefix_blocks, num_groups, std::min(max_prefix_blocks, max_blocks_per_seq), l.parts, part_o, part_ml, num_rows, nullptr, nullptr};
+    b.prefix = {group_start, prefix_blocks, num_groups, z.max_prefix_blocks, l.parts, part_o, part_ml, num_rows, nullptr, nullptr};
     if (l.apart) {
         b.prefix.rest_o = part_o + l.parts * num_rows * head_dim;
         b.prefix.rest_ml = part_ml + l.parts * num_rows;

@@ -52,3 +52,26 @@ def test_longest_first_in_calls_that_feed_each_other(api, cuda_device, S, fp8, a
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("share", [0, 10 ** 7, -1])
+@pytest.mark.parametrize("groups,Hkv", [([(40, [-300, -17, -639]), (9, [5, 100, 0]), (30, [-1])], 2), ([(200, [9, -100, 30, None])], 8)])
+def test_a_workspace_for_the_bound_or_for_the_width(api, cuda_device, groups, Hkv, share):
+    """A bound past the tables' width counts as the width, so a workspace for either does, and none where the width says
+    that nothing is shared."""
+    lib = _lib.load()
+    lib.pa_test_set_share(share, -1)
+    case = Shared(cuda_device, groups, 8, Hkv)
+    S, Hq, D = case.q.shape
+    width, want = case.bt.shape[1], case.expected()
+    taken = set()
+    for most in (width, width + 1, 3 * width, 4096, 1 << 20):
+        shared = lib.pa_shared_prefix_launches(S, len(case.pb), Hq, Hkv, D, case.pool.B, width, most, 0) > 1
+        for sized in (most, width):
+            ws = api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, sized)
+            assert ws is not None or not shared
+            if ws is not None:
+                ws.fill_(0xff)
+            within(case.call(api, max_prefix_blocks=most, workspace=ws), want, f"{most} {sized}")
+        taken.add(shared)
+    assert len(taken) == 1 and api.device_errors() == 0
