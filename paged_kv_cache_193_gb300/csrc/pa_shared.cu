@@ -130,7 +130,9 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     }
     const int at_once = z.fp8 && z.block_size == 16 ? 2 : 1;  // pages of a warp's step
     const int steps = (pages + at_once - 1) / at_once;        // of one warp
-    if (rows >= 512 && pages <= 8) return {true, false, 1, 4, false, p.parts};
+    const int mode = g_apart.load(std::memory_order_relaxed);
+    if (rows >= 512 && pages <= 8)  // joined by these, unless a test asks for the other way
+        return {true, false, 1, 4, mode == 1, mode == 1 ? std::min(p.parts, kMaxParts - 1) : p.parts};
     Suffix l{false, z.num_groups == 1 && z.num_seqs > 1 && z.num_seqs <= sparse::kMaxSorted && pages >= 16, 1, 4, false, p.parts};
     const int64_t wide = sparse::places_of_eight_warps(resident, z.group());
     if (rows <= wide && pages >= 12 && (steps < 160 || rows * 4 <= wide)) {
@@ -141,7 +143,6 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
         for (int s : {2, 4, 8})
             if (rows * s <= (steps >= 160 ? 512 + 1024 / s : 512)) l.splits = s;
 
-    const int mode = g_apart.load(std::memory_order_relaxed);
     // Half of the pages that the tables have room for, at 6.2 TB/s; many short lists go
     // a little slower.
     const double rest = z.num_seqs * own * 0.5 * z.page_bytes() / 6.2e6 * (pages < 64 ? 1.3 : 1.0);

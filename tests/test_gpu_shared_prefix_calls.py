@@ -75,3 +75,27 @@ def test_a_workspace_for_the_bound_or_for_the_width(api, cuda_device, groups, Hk
             within(case.call(api, max_prefix_blocks=most, workspace=ws), want, f"{most} {sized}")
         taken.add(shared)
     assert len(taken) == 1 and api.device_errors() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(groups=[(9, [i % 113 for i in range(86)])], Hq=6, Hkv=6),
+                                dict(groups=[(70, [i % 60 for i in range(175)])], Hq=9, Hkv=3, D=64, B=32),
+                                dict(groups=[(40, [i % 101 for i in range(108)] + [-1, None])], Hq=20, Hkv=5, fp8=True, per_head=True),
+                                dict(groups=[(12, [(211 * i) % 1100 for i in range(9)] + [None, -3])], Hq=8, Hkv=2)])
+def test_both_ways_of_joining_are_the_ways_meant(api, cuda_device, kw):
+    """Two and three kernels by the library's own answer, for lists so short that a warp takes a head too; each against the
+    definition, and twice the same bits with a workspace of NaN."""
+    lib = _lib.load()
+    case = Shared(cuda_device, **kw)
+    S, Hq, D = case.q.shape
+    ws, want = api.alloc_shared_prefix_workspace(case.q, case.pool.kd, case.gs, case.most), case.expected()
+    for apart in (0, 1):
+        lib.pa_test_set_share(0, apart)
+        assert lib.pa_shared_prefix_launches(S, len(case.pb), Hq, case.pool.Hkv, D, case.pool.B, case.bt.shape[1], case.most,
+                                             int(case.pool.fp8)) == 2 + apart
+        outs = []
+        for _ in range(2):
+            ws.fill_(0xff)
+            outs.append(case.call(api, workspace=ws))
+            within(outs[-1], want, f"apart: {apart}")
+        assert torch.equal(*outs)
+    assert api.device_errors() == 0

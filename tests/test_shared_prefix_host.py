@@ -20,3 +20,17 @@ def test_a_bound_past_the_tables_width_is_that(lib, S, G, Hq, Hkv, D, B, width, 
 
     for bound in (width + 1, 2 * width, 1 << 20):
         assert (launches(bound) > 1) == (launches(width) > 1)
+
+
+@pytest.mark.parametrize("width,bound", [(40, 40), (40, 33), (40, 30), (40, 4), (700, 300), (9000, 33), (9000, 9000)])
+@pytest.mark.parametrize("S,G", [(1, 1), (9, 1), (64, 1), (130, 3), (300, 1), (2000, 1), (2000, 70)])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_the_join_is_apart_where_a_test_asks_for_it(lib, S, G, width, bound, dt):
+    """And with it in the rest's kernel: of every launch that there is, a warp to a head for short lists among them."""
+    try:
+        for Hq, Hkv, D, B in ((8, 2, 128, 16), (32, 8, 128, 16), (16, 16, 64, 32), (64, 4, 128, 32)):
+            for apart in (0, 1):
+                assert lib.pa_test_set_share(0, apart) == 0
+                assert lib.pa_shared_prefix_launches(S, G, Hq, Hkv, D, B, width, bound, dt) == 2 + apart
+    finally:
+        assert lib.pa_test_set_share(-1, -1) == 0
