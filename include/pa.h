@@ -78,7 +78,7 @@ typedef enum pa_kv_dtype {
 
 /* Bits of the device error word (pa_device_errors). */
 #define PA_DEVERR_BAD_BLOCK   0x1u /* a block-table entry outside [0, num_blocks): page read as zeros */
-#define PA_DEVERR_BAD_CONTEXT 0x2u /* context_lens[s] > max_blocks_per_seq * block_size: clamped */
+#define PA_DEVERR_BAD_CONTEXT 0x2u /* context_lens[s] > max_blocks_per_seq * block_size: clamped; rows or groups that are no range */
 #define PA_DEVERR_TIMEOUT     0x4u /* a wait for a page copy exceeded its time limit; output invalid */
 #define PA_DEVERR_BAD_SLOT    0x8u /* slot_mapping entry >= num_blocks * block_size: token skipped */
 #define PA_DEVERR_OUT_OF_BLOCKS 0x10u /* pa_block_alloc: free stack too short; nothing changed */
@@ -585,12 +585,15 @@ pa_status pa_norm_rope_append(const void *q, int64_t q_stride, const void *k, in
  *   softmax over all of its context_lens[s] tokens; zeros for none.
  *   group_start   int32 [num_groups + 1] (device), ascending: group g is the
  *                 sequences group_start[g] .. group_start[g + 1] - 1 (none, if the
- *                 two are equal); those in no group share nothing.
+ *                 two are equal); those in no group share nothing.  A group that
+ *                 is no range of 0 .. num_seqs sets PA_DEVERR_BAD_CONTEXT where
+ *                 prefixes are taken once (two kernels or three; one does not read
+ *                 the groups), and what the call writes to out is not defined.
  *   prefix_blocks int32 [num_groups] (device): the first prefix_blocks[g] entries
- *                 of the group's table rows are the same physical blocks.  A
- *                 sequence that has fewer tokens than those hold (a padded row of
- *                 none, for instance) is attended to by itself, through its own
- *                 table row.
+ *                 of the group's table rows are the same physical blocks (none, if
+ *                 negative).  A sequence that has fewer tokens than those hold (a
+ *                 padded row of none, for instance) is attended to by itself,
+ *                 through its own table row.
  *   max_prefix_blocks  a bound for the launch: of longer prefixes so many blocks
  *                 are taken together, the others for each sequence.  More
  *                 than max_blocks_per_seq counts as that; the workspace may be

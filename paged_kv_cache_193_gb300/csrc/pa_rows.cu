@@ -264,6 +264,16 @@ __device__ __forceinline__ bool find_work(const Args &a, void *room, Work &w) {
     return w.table >= 0;
 }
 
+// Groups that are no range of the sequences are reported: a group to a thread, of the CTAs of
+// the first KV head.  A CTA looks no further than its own group, so none of them meets all.
+__device__ __forceinline__ void check_groups(const Args &a) {
+    const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t g = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; g < a.num_groups; g += threads) {
+        const int lo = a.group_start[g], hi = a.group_start[g + 1];
+        if (lo < 0 || hi < lo || hi > a.num_seqs) set_device_error(a.err, PA_DEVERR_BAD_CONTEXT);
+    }
+}
+
 template <int D, bool FP8, int TILES>
 __global__ void __launch_bounds__(Layout<D, FP8, TILES>::kThreads, Layout<D, FP8, TILES>::kCtas)
     rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -286,7 +296,9 @@ __global__ void __launch_bounds__(Layout<D, FP8, TILES>::kThreads, Layout<D, FP8
     // them, and waits for this one's end itself.
     if (a.group_start) dependent_release();
     Work w;
-    if (!find_work<TILES>(a, smem_raw, w)) return;
+    const bool work = find_work<TILES>(a, smem_raw, w);
+    if (a.group_start && blockIdx.y == 0) check_groups(a);  // behind it: the loads are in the cache by now
+    if (!work) return;
     const int h = w.head;
     const int all = (w.keys + kKeys - 1) / kKeys, each = blocks_per_part(all, a.parts);
     const int first = w.part * each, nkb = min(each, all - first);  // this part's blocks

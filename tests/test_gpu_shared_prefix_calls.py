@@ -99,3 +99,42 @@ def test_both_ways_of_joining_are_the_ways_meant(api, cuda_device, kw):
             within(outs[-1], want, f"apart: {apart}")
         assert torch.equal(*outs)
     assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("apart", [0, 1])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_groups_that_are_no_ranges_are_reported(api, cuda_device, fp8, apart):
+    """Whichever group it is, among few and among more than a CTA has threads; and not those that are, empty ones, sequences
+    of none and prefixes of none among them."""
+    _lib.load().pa_test_set_share(0, apart)
+    case = Shared(cuda_device, [(4, [8, 9]), (0, []), (3, [1, 2])], 4, 2, alone=[20], fp8=fp8)
+    want = case.expected()
+    within(case.call(api), want)
+    assert api.device_errors() == 0
+    for start in ([-1, 2, 2, 4], [0, 2, 2, 6], [0, 2, 1, 4], [3, 1, 0, 0], [0, 2, 2, -4], [2 ** 31 - 1, 0, -2 ** 31, 1], [6, 6, 6, 6]):
+        case.gs.copy_(torch.tensor(start, dtype=torch.int32))
+        case.call(api)
+        assert api.device_errors() == _lib.PA_DEVERR_BAD_CONTEXT, start
+    case.gs.copy_(torch.tensor([0, 2, 2, 4], dtype=torch.int32))
+    case.pb[1:] = -7
+    within(case.call(api), want)
+    assert api.device_errors() == 0
+    many = Shared(cuda_device, [(1 + i % 2, [i % 3]) for i in range(1500)], 2, 2, D=64, fp8=fp8)
+    within(many.call(api), many.expected())
+    assert api.device_errors() == 0
+    for g in (1, 31, 700, 1499):
+        was = int(many.gs[g])
+        many.gs[g] = was + 2  # behind the start of the next
+        many.call(api)
+        assert api.device_errors() == _lib.PA_DEVERR_BAD_CONTEXT, g
+        many.gs[g] = was
+    within(many.call(api), many.expected())
+    assert api.device_errors() == 0
+
+
+def test_groups_are_not_read_where_nothing_is_shared(api, cuda_device):
+    _lib.load().pa_test_set_share(1 << 60, -1)
+    case = Shared(cuda_device, [(4, [8, 9]), (3, [1, 2])], 4, 2)
+    case.gs.copy_(torch.tensor([3, 1, 0], dtype=torch.int32))
+    within(case.call(api), case.expected())
+    assert api.device_errors() == 0
