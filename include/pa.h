@@ -597,7 +597,13 @@ pa_status pa_norm_rope_append(const void *q, int64_t q_stride, const void *k, in
  *   max_prefix_blocks  a bound for the launch: of longer prefixes so many blocks
  *                 are taken together, the others for each sequence.  More
  *                 than max_blocks_per_seq counts as that; the workspace may be
- *                 sized by either.
+ *                 sized by either.  Results do not depend on it, the launch does:
+ *                 with one group, what the tables have room for behind the bound
+ *                 is taken for the most that a sequence has of its own, and with
+ *                 a bound of their width nothing is known of that (a call takes
+ *                 up to half as long again).  A sequence with more, of no group
+ *                 or without its prefix, may be read by a warp alone, about a
+ *                 microsecond to a page and KV head.
  *   num_groups <= num_seqs; 0 groups, or max_prefix_blocks 0: nothing is shared,
  *                 and group_start and prefix_blocks may be NULL.
  *   workspace     pa_shared_prefix_workspace_size bytes (0: NULL will do),

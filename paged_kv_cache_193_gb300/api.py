@@ -663,8 +663,9 @@ def shared_prefix_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     ``group_start`` int32 [G + 1]: group g is sequences group_start[g] ..
     group_start[g + 1] - 1; ``prefix_blocks`` int32 [G]: how many of the first
     entries of their table rows are the same blocks.  ``max_prefix_blocks``: no
-    entry of prefix_blocks counts for more (None: the tables' width; a closer
-    bound launches a better shape)."""
+    entry of prefix_blocks counts for more (None: the tables' width, by which
+    nothing is known of what the sequences have behind their prefix, and a call
+    takes up to half as long again as with the longest prefix for a bound)."""
     if max_prefix_blocks is None:
         max_prefix_blocks = block_tables.shape[1]
     if softmax_scale is None:

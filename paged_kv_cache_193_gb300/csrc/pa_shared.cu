@@ -97,21 +97,32 @@ struct Suffix {
     int parts;
 };
 
-// A CTA for every KV head costs about 3.6 us, however little it reads, so few pages
-// are better read by a warp to a head (1,024 rows of up to 100 tokens: 16.1 us, 22.1
-// with a CTA to each; of up to 500 43 and 29), where all CTAs are on the SMs at once
-// also some more.  With as many rows as places or a few more, the longest go first
-// (512 rows of up to 1,000 tokens, E4M3: 19.5 us, 28.9 in their order); who is
-// longest is known for one group, whose prefix is the same for all.  Long lists are
-// shared out while 512 CTAs hold them (128 rows of up to 2,000 tokens in bf16: 36.7 us
-// with one, 24.0 with two, 18.7 with four; of up to 1,000 in E4M3 11.9, 13.5, 14.4),
-// and some more when very long (with a prefix of 8,192, of up to 4,000 tokens: 512 rows
-// 105.8 with one and 92.3 with two, 192 rows 53.2 with two and 48.4 with four, 128 rows
-// 37.6 with four and 44.3 with eight; 512 rows of up to 2,000, behind 32,768: 79.0 with
-// one and 91.7 with two).  Rows that find places at once as CTAs of eight warps have those
-// (the same prefix, of up to 1,000: 128 rows 20.7 us, 22.1 by two CTAs of four warps, 26.9 by
-// one; 32 rows in E4M3 19.5, 20.9, 21.3), and two of them to each of up to 2,000 (128 rows 29.1
-// us, 31.2 with one).
+// A CTA for every KV head costs about 3.6 us, however little it reads, so few pages are better read
+// by a warp to a head (1,024 rows of up to 100 tokens, behind 1,024: 15.2 us, 20.8 with a CTA to
+// each; of up to 500 43 and 29), where all CTAs are on the SMs at once also some more.
+//
+// A row without its group's prefix, or of no group, has all its pages among the rest's, and a warp
+// takes a microsecond to a page: under 2,048 rows a warp to a head is for tables of up to 128 pages
+// (128 sequences, up to 100 tokens behind 16,384, one of them a token short of those: 1,087 us, 305
+// with CTAs, and without it 46 and 45; behind 8,000 8,192 rows take 137 and 164).
+//
+// A bound as wide as the tables says nothing of the rest, which is then planned as if it had the
+// tables to itself (64 sequences behind 32,768, up to 2,048 more, without a bound: 99 us, 204 when
+// that was taken for no room, 79 with it; behind 1,024, up to 8,000 more: 170, 542 and 169), but
+// for 2,048 rows and more of up to 512 pages, which a warp to a head serves whatever they are
+// (1,024 sequences behind 1,024, up to 100 more: 62 us, 88 with CTAs; 256, up to 2,000 more: 194
+// and 167).
+//
+// With as many rows as places or a few more, the longest go first (512 rows of up to 1,000 tokens,
+// E4M3: 19.5 us, 28.9 in their order); who is longest is known for one group, whose prefix is the
+// same for all.  Long lists are shared out while 512 CTAs hold them (128 rows of up to 2,000 tokens
+// in bf16: 36.7 us with one, 24.0 with two, 18.7 with four; of up to 1,000 in E4M3 11.9, 13.5,
+// 14.4), and some more when very long (with a prefix of 8,192, of up to 4,000 tokens: 512 rows
+// 105.8 with one and 92.3 with two, 192 rows 53.2 with two and 48.4 with four, 128 rows 37.6 with
+// four and 44.3 with eight; 512 rows of up to 2,000, behind 32,768: 79.0 with one and 91.7 with
+// two).  Rows that find places at once as CTAs of eight warps have those (the same prefix, of up to
+// 1,000: 128 rows 20.7 us, 22.1 by two CTAs of four warps, 26.9 by one; 32 rows in E4M3 19.5, 20.9,
+// 21.3), and two of them to each of up to 2,000 (128 rows 29.1 us, 31.2 with one).
 //
 // The join is made apart where an estimate of both ways says so: then the prefix's CTAs
 // may leave SMs to the rest's, and neither waits for the other (64 sequences, 32,768
@@ -121,8 +132,8 @@ struct Suffix {
 static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     const int64_t rows = z.num_seqs * z.num_kv_heads;
     // pages behind the prefix: of several groups, the shortest may be none
-    const int own = std::max(max_blocks - z.max_prefix_blocks, 0);
-    const int pages = p.shared && z.num_groups == 1 ? own : max_blocks;
+    const int own = max_blocks - z.max_prefix_blocks;  // 0: not known
+    const int pages = p.shared && z.num_groups == 1 && own > 0 ? own : max_blocks;
     const int resident = sparse::resident_ctas(z.head_dim, z.block_size, z.fp8, z.group());
     if (!p.shared) {
         const sparse::Spread s = sparse::spread_of_tables(rows, pages, resident, z.group());
@@ -131,7 +142,9 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     const int at_once = z.fp8 && z.block_size == 16 ? 2 : 1;  // pages of a warp's step
     const int steps = (pages + at_once - 1) / at_once;        // of one warp
     const int mode = g_apart.load(std::memory_order_relaxed);
-    if (rows >= 512 && pages <= 8)  // joined by these, unless a test asks for the other way
+    const bool lone = rows >= 2048 || max_blocks <= 128;
+    if ((rows >= 512 && pages <= 8 && lone) || (z.num_groups == 1 && own == 0 && rows >= 2048 && pages <= 512))
+        // joined by these, unless a test asks for the other way
         return {true, false, 1, 4, mode == 1, mode == 1 ? std::min(p.parts, kMaxParts - 1) : p.parts};
     Suffix l{false, z.num_groups == 1 && z.num_seqs > 1 && z.num_seqs <= sparse::kMaxSorted && pages >= 16, 1, 4, false, p.parts};
     const int64_t wide = sparse::places_of_eight_warps(resident, z.group());
@@ -143,15 +156,21 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
         for (int s : {2, 4, 8})
             if (rows * s <= (steps >= 160 ? 512 + 1024 / s : 512)) l.splits = s;
 
-    // Half of the pages that the tables have room for, at 6.2 TB/s; many short lists go
-    // a little slower.
-    const double rest = z.num_seqs * own * 0.5 * z.page_bytes() / 6.2e6 * (pages < 64 ? 1.3 : 1.0);
     const int64_t ctas = p.ctas * z.num_kv_heads, places = (p.tiles == 1 ? 2 : 1) * kSms;
     const int blocks = prefix_blocks_of(z);
     const double average = z.num_groups == 1 ? 1.0 : 0.6;  // of runs of unlike lengths, beside the longest
     auto one = [&](int parts) { return cta_time(blocks_per_part(blocks, parts), p.tiles, z.head_dim); };
     auto waves = [&](int parts) { return std::ceil(static_cast<double>(ctas) * parts / places); };
-    const double together = waves(p.parts) * one(p.parts) * average + join_time(p.parts, z.head_dim, z.rows()) + rest;
+    const double alone = waves(p.parts) * one(p.parts) * average;
+    // Half of the pages that the tables have room for, at 6.2 TB/s; many short lists go
+    // a little slower.  Tables may be far wider than what they hold, and a prefix that is cut
+    // for a rest of that length ends long after the real one, so a rest of several times the
+    // prefix's own time counts for as much as that (64 sequences behind 32,768 tokens, up to
+    // 2,048 more, tables for 131,072: 92 us, 376 else; where there is so much, 64 sequences
+    // behind 1,024, up to 8,000 more: 170.7 and 169.0).
+    double rest = z.num_seqs * own * 0.5 * z.page_bytes() / 6.2e6 * (pages < 64 ? 1.3 : 1.0);
+    if (rest > 4 * alone) rest = alone;
+    const double together = alone + join_time(p.parts, z.head_dim, z.rows()) + rest;
     double least = INFINITY;
     for (int parts = 1; parts <= p.parts && parts < kMaxParts; ++parts) {
         const double cost = std::max(waves(parts) * one(parts), ctas * parts * one(parts) * average / places + rest) +
@@ -165,7 +184,7 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     // A warp to a head (1,600 rows of up to 200 and 300 tokens, E4M3, apart: 30.7 and 30.8 us,
     // 32.5 and 35.7 with a CTA to each; of up to 200 and 300 in bf16 31.6 and 39.4, 33.5 and 37.8;
     // 2,048 rows of up to 512, E4M3, 45.8 and 44.9, but joined by them 49.0 and 50.1).
-    if (rows >= 1536 && steps <= (l.apart ? 13 : 16)) {
+    if (rows >= 1536 && steps <= (l.apart ? 13 : 16) && lone) {
         l.heads = true;
         l.longest_first = false;
         l.splits = 1;

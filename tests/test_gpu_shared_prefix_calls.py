@@ -138,3 +138,62 @@ def test_groups_are_not_read_where_nothing_is_shared(api, cuda_device):
     case.gs.copy_(torch.tensor([3, 1, 0], dtype=torch.int32))
     within(case.call(api), case.expected())
     assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(groups=[(9, [(53 * i) % 400 for i in range(257)])], Hq=8, Hkv=8, D=64, fp8=True),       # a warp to a head
+                                dict(groups=[(9, [(53 * i) % 330 for i in range(100)] + [None, -7])], Hq=16, Hkv=8, extra=40),  # a CTA
+                                dict(groups=[(4, [(7 * i) % 90 for i in range(40)]), (20, [3, 700, -100])], Hq=8, Hkv=2, extra=3000),
+                                dict(groups=[(140, [(i * 5) % 60 for i in range(69)] + [-1])], Hq=8, Hkv=8, alone=[1500, 3]),
+                                dict(groups=[(30, [(i * 5) % 60 for i in range(69)] + [-1])], Hq=8, Hkv=8, alone=[300, 0])])
+def test_without_a_bound_and_in_wide_tables(api, cuda_device, kw):
+    """The bound is the tables' width, or they have room for far more than they hold; sequences without their prefix, and
+    of no group, among others with little of their own."""
+    lib = _lib.load()
+    case = Shared(cuda_device, **kw)
+    want = case.expected()
+    for apart in (-1, 0, 1):
+        lib.pa_test_set_share(0, apart)
+        for most in (None, case.most):
+            within(case.call(api, max_prefix_blocks=most), want, f"{apart} {most}")
+    assert api.device_errors() == 0
+
+
+def _time(call, n=5):
+    call()
+    best = float("inf")
+    for _ in range(4):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(n):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) / n)
+    return best
+
+
+@pytest.mark.parametrize("S,P,own,Hq,extra", [(64, 64, 8000, 32, 0), (64, 2048, 2048, 64, 0), (64, 2048, 2048, 64, 6000), (16, 512, 1000, 32, 7000)])
+def test_what_no_bound_and_wide_tables_cost(api, cuda_device, S, P, own, Hq, extra):
+    """Neither sends a batch the long way round: within twice the time of the exact bound over exact tables (two and a half
+    to five times, when a bound was taken for what is there)."""
+    _lib.load().pa_test_set_share(-1, -1)
+    Hkv, D, B = 8, 128, 16
+    g = torch.Generator(device=cuda_device).manual_seed(1)
+    mine = -(-own // B)
+    NB = P + S * mine
+    kv = torch.randn(2, NB, Hkv, B, D, generator=g, device=cuda_device, dtype=torch.bfloat16)
+    q = torch.randn(S, Hq, D, generator=g, device=cuda_device).to(torch.bfloat16)
+    exact = torch.cat([torch.arange(P, device=cuda_device).expand(S, P), P + torch.arange(S * mine, device=cuda_device).view(S, mine)], 1).to(torch.int32)
+    wide = torch.cat([exact, torch.full((S, extra), -1, dtype=torch.int32, device=cuda_device)], 1).contiguous()
+    lens = (P * B + torch.randint(1, own + 1, (S,), generator=g, device=cuda_device)).to(torch.int32)
+    gs = torch.tensor([0, S], dtype=torch.int32, device=cuda_device)
+    pb = torch.tensor([P], dtype=torch.int32, device=cuda_device)
+    out = torch.empty_like(q)
+
+    def call(tables, bound):
+        ws = api.alloc_shared_prefix_workspace(q, kv[0], gs, tables.shape[1] if bound is None else bound)
+        return lambda: api.shared_prefix_decode(q, kv[0], kv[1], tables, lens, gs, pb, bound, workspace=ws, out=out)
+
+    least = _time(call(exact, P))
+    assert _time(call(wide, P if extra else None)) < 2 * least
+    assert api.device_errors() == 0
