@@ -197,3 +197,56 @@ def test_what_no_bound_and_wide_tables_cost(api, cuda_device, S, P, own, Hq, ext
     least = _time(call(exact, P))
     assert _time(call(wide, P if extra else None)) < 2 * least
     assert api.device_errors() == 0
+
+
+@pytest.mark.parametrize("apart", [0, 1])
+@pytest.mark.parametrize("norm,fp8", [(False, False), (True, True)])
+def test_every_step_against_the_definition(api, cuda_device, norm, fp8, apart):
+    """Twenty tokens through SharedPrefixDecodeStep, over the ends of pages: the attention of each, eager and from a graph,
+    against the definition over the cache that the steps wrote.  (A cache only grows, so the last one serves them all.)"""
+    _lib.load().pa_test_set_share(0, apart)
+    B, D, Hq, Hkv, steps = 16, 128, 8, 2, 20
+    case = Shared(cuda_device, [(6, [1, 5, 14, 16]), (3, [2, 2])], Hq, Hkv, fp8=fp8, extra=2)
+    S, dev = case.q.shape[0], cuda_device
+    g = torch.Generator().manual_seed(6)
+    more = torch.zeros(40, Hkv, B, D, dtype=case.pool.kd.dtype, device=dev)
+    kc, vc = torch.cat([case.pool.kd, more]), torch.cat([case.pool.vd, more])
+    fresh = iter(range(case.pool.kd.shape[0], kc.shape[0]))
+    bt = case.bt.clone()
+    for s in range(S):  # blocks for what is to come
+        for j in range(-(-case.lens[s] // B), bt.shape[1]):
+            if j * B < case.lens[s] + steps:
+                bt[s, j] = next(fresh)
+    freq = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).to(dev)
+    w = (1 + 0.2 * torch.randn(2, D, generator=g)).to(torch.bfloat16).to(dev)
+    extra = dict(q_weight=w[0], k_weight=w[1], eps=1e-5) if norm else {}
+    new = [[torch.randn(S, h, D, generator=g).to(torch.bfloat16).to(dev) for h in (Hq, Hkv, Hkv)] for _ in range(steps)]
+
+    def run(captured):
+        k, v, lens = kc.clone(), vc.clone(), case.cl.clone()
+        pos, buf, got = lens.clone(), [x.clone() for x in new[0]], []
+        lens += 1
+        step = api.SharedPrefixDecodeStep(k, v, bt, lens, pos, freq, Hq, case.gs, case.pb, case.most, kv_scale=1 / 16, **extra)
+        assert step.launches() == 4 + apart
+        graph = api.StepGraph([step], [buf]) if captured else None
+        for x in new:
+            for a, b in zip(buf, x):
+                a.copy_(b)
+            if captured:
+                graph.replay()
+            else:
+                step(*buf)
+            got.append((step.out.clone(), step.q_rotated.clone(), lens.tolist()))
+            lens += 1
+            pos += 1
+        torch.cuda.synchronize()
+        assert api.device_errors() == 0
+        return k, v, got
+
+    case.tables, case.scale = bt.cpu(), D ** -0.5
+    for captured in (False, True):
+        k, v, got = run(captured)
+        case.pool.k, case.pool.v = k.cpu(), v.cpu()
+        for i, (out, q, lens) in enumerate(got):
+            case.q, case.lens = q, lens
+            within(out, case.expected(), f"captured {captured}, step {i}")

@@ -1,5 +1,9 @@
-"""How shared-prefix decode is launched, by its sizes (no GPU)."""
+"""How shared-prefix decode is launched, by its sizes, and what its tests' bounds let through (no GPU)."""
+import numpy as np
 import pytest
+import torch
+
+import rows_cases
 
 
 @pytest.fixture(scope="module")
@@ -34,3 +38,23 @@ def test_the_join_is_apart_where_a_test_asks_for_it(lib, S, G, width, bound, dt)
                 assert lib.pa_shared_prefix_launches(S, G, Hq, Hkv, D, B, width, bound, dt) == 2 + apart
     finally:
         assert lib.pa_test_set_share(-1, -1) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [0, 3, 5])
+def test_a_prefix_of_one_page_less_is_past_the_bound(page, fp8):
+    """A page of the prefix that is left out, as a kernel would that counts one too few: every sequence that holds the prefix
+    is outside its bound, one that does not is untouched."""
+    case = rows_cases.Shared("cpu", [(6, [40, 3, -90])], 4, 2, D=64, fp8=fp8)
+    good = case.expected()
+    rows_cases.within(torch.from_numpy(good[0]), good)
+    full, lens = case.tables.clone(), list(case.lens)
+    for s in range(2):
+        row = torch.cat([full[s, :page], full[s, page + 1:], torch.tensor([-1], dtype=torch.int32)])
+        case.tables[s] = row
+        case.lens[s] = lens[s] - 16
+    wrong = case.expected()[0]
+    assert np.array_equal(wrong[2], good[0][2])
+    for s in range(2):
+        with pytest.raises(AssertionError):
+            rows_cases.within(torch.from_numpy(wrong[s]), tuple(x[s] for x in good))
