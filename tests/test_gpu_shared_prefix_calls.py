@@ -250,3 +250,39 @@ def test_every_step_against_the_definition(api, cuda_device, norm, fp8, apart):
         for i, (out, q, lens) in enumerate(got):
             case.q, case.lens = q, lens
             within(out, case.expected(), f"captured {captured}, step {i}")
+
+
+@pytest.mark.parametrize("apart", [0, 1])
+def test_groups_that_change_between_replays(api, cuda_device, apart):
+    """One graph for all ways to group a batch: in each replay other groups, prefixes and lengths, an empty group, one of
+    all sequences and sequences of none among them."""
+    _lib.load().pa_test_set_share(0, apart)
+    case = Shared(cuda_device, [(20, [(17 * i) % 150 for i in range(37)])], 8, 2)
+    S, G, most = len(case.lens), 4, 20
+    out = torch.empty_like(case.q)
+    gs, pb = torch.zeros(G + 1, dtype=torch.int32, device=cuda_device), torch.zeros(G, dtype=torch.int32, device=cuda_device)
+    ws = api.alloc_shared_prefix_workspace(case.q, case.pool.kd, gs, most)
+    case.gs, case.pb = gs, pb
+
+    def call():
+        case.call(api, max_prefix_blocks=most, workspace=ws, out=out)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    full = list(case.lens)
+    for start, pages in (([0, 0, 0, 0, 0], [20] * 4), ([0, 37, 37, 37, 37], [20, 1, 1, 1]), ([0, 1, 2, 36, 37], [3, 20, 19, 7]),
+                         ([5, 5, 20, 20, 30], [9, 0, 8, 20]), ([0, 9, 18, 27, 37], [20, 0, 13, 40])):
+        gs.copy_(torch.tensor(start, dtype=torch.int32))
+        pb.copy_(torch.tensor(pages, dtype=torch.int32))
+        for cut in (0, 200):  # some shorter than their prefix
+            case.lens = [max(0, n - cut * (i % 3)) for i, n in enumerate(full)]
+            case.cl.copy_(torch.tensor(case.lens, dtype=torch.int32))
+            ws.fill_(0xff)
+            out.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            within(out, case.expected(), f"{start} {pages} {cut}")
+    assert api.device_errors() == 0
