@@ -102,7 +102,7 @@ struct Suffix {
 // each; of up to 500 43 and 29), where all CTAs are on the SMs at once also some more.
 //
 // A row without its group's prefix, or of no group, has all its pages among the rest's, and a warp
-// takes a microsecond to a page: under 2,048 rows a warp to a head is for tables of up to 128 pages
+// takes a microsecond to a page: under 1,536 rows a warp to a head is for tables of up to 128 pages
 // (128 sequences, up to 100 tokens behind 16,384, one of them a token short of those: 1,087 us, 305
 // with CTAs, and without it 46 and 45; behind 8,000 8,192 rows take 137 and 164).
 //
@@ -142,7 +142,7 @@ static Suffix suffix_launch(const Sizes &z, const Plan &p, int max_blocks) {
     const int at_once = z.fp8 && z.block_size == 16 ? 2 : 1;  // pages of a warp's step
     const int steps = (pages + at_once - 1) / at_once;        // of one warp
     const int mode = g_apart.load(std::memory_order_relaxed);
-    const bool lone = rows >= 2048 || max_blocks <= 128;
+    const bool lone = rows >= 1536 || max_blocks <= 128;
     if ((rows >= 512 && pages <= 8 && lone) || (z.num_groups == 1 && own == 0 && rows >= 2048 && pages <= 512))
         // joined by these, unless a test asks for the other way
         return {true, false, 1, 4, mode == 1, mode == 1 ? std::min(p.parts, kMaxParts - 1) : p.parts};
