@@ -449,7 +449,8 @@ pa_status pa_prefill_mma(const void *q, const void *k_cache, const void *v_cache
  *   k_cache, v_cache  row slot_mapping[t] gets the rotated k and v as they
  *                 are (PA_KV_BF16), or e4m3_rn_satfinite(x / scale) of the
  *                 fp32 rotated k and of v (PA_KV_FP8_E4M3), scale = kv_scale,
- *                 or k_scales[h] / v_scales[h] when both arrays are given.
+ *                 or k_scales[h] / v_scales[h] when both arrays are given
+ *                 (device, positive and finite: not checked).
  *   A negative slot writes no k and v for the token (its q is rotated all the
  *   same); distinct tokens must have distinct slots.  num_axes 1..16.
  */
@@ -600,8 +601,8 @@ pa_status pa_norm_rope_append(const void *q, int64_t q_stride, const void *k, in
  *                 sized by either.  Results do not depend on it, the launch does:
  *                 with one group, what the tables have room for behind the bound
  *                 is taken for the most that a sequence has of its own, and with
- *                 a bound of their width nothing is known of that (a call takes
- *                 up to half as long again).  A sequence with more, of no group
+ *                 a bound of their width nothing is known of that (a call may
+ *                 take 1.6 times as long).  A sequence with more, of no group
  *                 or without its prefix, may be read by a warp alone, about a
  *                 microsecond to a page and KV head.
  *   num_groups <= num_seqs; 0 groups, or max_prefix_blocks 0: nothing is shared,

@@ -664,8 +664,8 @@ def shared_prefix_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     group_start[g + 1] - 1; ``prefix_blocks`` int32 [G]: how many of the first
     entries of their table rows are the same blocks.  ``max_prefix_blocks``: no
     entry of prefix_blocks counts for more (None: the tables' width, by which
-    nothing is known of what the sequences have behind their prefix, and a call
-    takes up to half as long again as with the longest prefix for a bound)."""
+    nothing is known of what the sequences have behind their prefix: a call may
+    take 1.6 times as long as with the longest prefix for a bound)."""
     if max_prefix_blocks is None:
         max_prefix_blocks = block_tables.shape[1]
     if softmax_scale is None:
@@ -741,8 +741,9 @@ class SharedPrefixDecodeStep:
     ``norm`` true, of normalised q and k), attention with each group's prefix
     taken once.  Every buffer is allocated here; calling it allocates nothing.
     ``positions``, ``context_lens``, ``block_tables``, ``group_start`` and
-    ``prefix_blocks`` are the caller's and read at every call.  Works as a step
-    of ``StepGraph``."""
+    ``prefix_blocks`` are the caller's and read at every call;
+    ``max_prefix_blocks`` is shared_prefix_decode's.  Works as a step of
+    ``StepGraph``."""
 
     def __init__(self, k_cache, v_cache, block_tables, context_lens, positions, inv_freq, num_q_heads,
                  group_start, prefix_blocks, max_prefix_blocks=None, softmax_scale=None, kv_scale=1.0,

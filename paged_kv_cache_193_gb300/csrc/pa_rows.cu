@@ -75,8 +75,9 @@ struct Layout {
     static constexpr int kWiden = kSoft + 2 * TILES;
     static constexpr int kThreads = 32 * (kWiden + (FP8 ? 4 : 0));
     // Where 512 threads leave 128 registers to each, a row's scores do not stay in them:
-    // half of a block's are read again for their powers.  (E4M3, 40 sequences: 148 us,
-    // 187 with all of them held and some of them spilled.)
+    // half of a block's are read again for their powers.  (E4M3, 40 sequences: 148 us, 187
+    // with all of them held and more of them spilled; 28 bytes a thread still are with two
+    // tiles, 12 with one.)
     static constexpr bool kReread = kThreads * kCtas == 512;
     static constexpr int kSlabs = D / 64;
     static constexpr int kQSlab = kTileRows * 128;  // 64 dims of a tile's queries
@@ -553,7 +554,9 @@ __global__ void __launch_bounds__(Layout<D, FP8, TILES>::kThreads, Layout<D, FP8
             if constexpr (FP8) scale *= a.k_scales ? a.k_scales[h] : a.kv_scale;
             float m_ref = -INFINITY, l_run = 0.f;
             bool ok = mbar_wait_suspend(smem_addr(&bar.q_full), 0, limit);
-            if constexpr (FP8) {  // the row's query to fp16, in place
+            // The row's query to fp16, in place: K is fp16, which holds all E4M3 values, and a
+            // product's two sides have one type.  Exact between 2^-17 and 65,504.
+            if constexpr (FP8) {
                 for (int sl = 0; sl < L::kSlabs; ++sl)
                     for (int c = 0; c < 8; ++c) {
                         const uint32_t ad = base + T * L::kQTile + sl * kQSlab + row * 128 + ((c ^ (row & 7)) << 4);
@@ -640,6 +643,11 @@ __global__ void __launch_bounds__(Layout<D, FP8, TILES>::kThreads, Layout<D, FP8
                 }
                 // no finite score so far: any reference will do for the zeros
                 const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                // The sum takes the powers as they are, the product as 16 bits, of V's type as
+                // it has to: one bf16 number, off by up to 2^-8 of it (an output's error is 0.0023
+                // of its norm, 0.0017 by the output's own rounding alone), or one fp16 number, up
+                // to 2^-11 (0.0017 as well).  The list kernel keeps what the bf16 number leaves as
+                // a second one and is bound by memory; here that is half as many products again.
                 uint32_t pk[32];
                 auto powers = [&](int half, float (&x)[32]) {
                     float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
